@@ -288,6 +288,143 @@ int qr_mx_gemm(const void* Xq, const uint8_t* sx, const void* Wq, const uint8_t*
                int64_t N, int64_t K, int out, void* Y, int64_t ldy, void* stream);
 
 /*
+ * Formats of a linear's input: what the block norms and the MXFP4 operators write
+ * and read. The block formats hold one power-of-two scale per 32 consecutive
+ * elements of a row, in the panels of qr_mx_quantize, [ceil(K/128)][rows][4].
+ */
+enum {
+  QR_ACT_INT8 = 0,  /* per-token INT8 codes, fp32 scales [M] */
+  QR_ACT_FP8 = 1,   /* per-token E4M3FN codes, fp32 scales [M] */
+  QR_ACT_MXFP8 = 2, /* block-wise E4M3FN codes [M, K], E8M0 scale panels */
+  QR_ACT_MXFP4 = 3, /* block-wise E2M1 codes [M, K/2], E8M0 scale panels */
+  QR_ACT_BF16 = 4   /* bf16 [M, K], no scales */
+};
+
+/*
+ * qr_mxfp4_quantize -- microscaled 4-bit floating point (MXFP4), the half-size
+ * sibling of qr_mx_quantize: for the weights of a rollout actor (from the fp32
+ * master weights, s = 1 or already divided by s) and for tokens.
+ *
+ * For every row r and block b of 32 elements v (widened exactly to fp32):
+ *   X = the smallest integer with max |v| <= 6 * 2^X (clamped to [-127, 127]; an
+ *       all-zero block gives -127); the block's scale byte is X + 127;
+ *   code = E2M1(v_i * 2^-X): 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with v_i's sign, nearest,
+ *       ties to the even code, sign kept on zero. No element is clipped.
+ *   A block that holds a NaN or an infinity gets scale byte 255 (NaN) and zero
+ *   codes: its products are NaN.
+ *
+ *   A        [R, lda] fp32 (src_bf16 = 0) or bf16 bit patterns (src_bf16 = 1),
+ *            rows on 16-byte boundaries.
+ *   K        multiple of 32.
+ *   codes    [R, K/2] bytes (written): element 2 i in the low half of byte i,
+ *            element 2 i + 1 in its high half.
+ *   scales   [ceil(K/128)][R][4] bytes, 4-byte aligned (written; the bytes of
+ *            a partial last panel that belong to no block are set to 0).
+ */
+int qr_mxfp4_quantize(const void* A, int64_t R, int64_t K, int64_t lda, int src_bf16, void* codes,
+                      uint8_t* scales, void* stream);
+
+/*
+ * qr_mx_dequantize -- the values that block-wise codes stand for,
+ *   out[r, k] = element(codes[r, k]) * 2^X(r, k / 32)
+ * (exact in bf16 and fp32 up to overflow to infinity; scale byte 255 gives NaN).
+ *
+ *   fmt      QR_ACT_MXFP4 (codes [R, K/2]) or QR_ACT_MXFP8 (codes [R, K]).
+ *   out      [R, ldo] bf16 (out_bf16 = 1) or fp32 (written), rows on 16-byte
+ *            boundaries. K a multiple of 32.
+ */
+int qr_mx_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int fmt, void* out,
+                     int64_t ldo, int out_bf16, void* stream);
+
+/*
+ * qr_mxfp4_gemm -- product of quantized tokens with MXFP4 weights:
+ *   acc[m,n] = sum_b 2^(Xx[m,b] + Xw[n,b]) sum_{k in block b} x[m,k] w[n,k]
+ *   (gfx950 scaled MFMA, fp32 accumulators; with E4M3 tokens the products within
+ *   a group of k are added at the FP8 MFMA's reduced precision, as in qr_mx_gemm).
+ *   out = QR_OUT_BF16: Y[m,n] = bf16_rne(acc);  QR_OUT_RAW: Y = acc (fp32).
+ *   The result of a call is the same bits on every run.
+ *
+ *   Xq, sx   tokens of format xfmt: QR_ACT_MXFP4 (qr_mxfp4_quantize) or
+ *            QR_ACT_MXFP8 (qr_mx_quantize), or from qr_block_norm_quant or
+ *            qr_silu_mul_mx.
+ *   Wq, sw   [N, K/2] codes and scale panels of qr_mxfp4_quantize.
+ *            Xq, Wq, sx, sw and Y start on 16-byte boundaries.
+ *   K        multiple of 128; code matrices below 2^31 - 2^16 bytes.
+ *   Y        [M, ldy] bf16 or fp32, any ldy >= N (written).
+ *   workspace  qr_workspace_size("qr_mxfp4_gemm", M, N, K, xfmt) bytes, 256-byte
+ *            aligned, contents irrelevant; may be NULL when that is 0.
+ */
+int qr_mxfp4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq, const uint8_t* sw,
+                  int64_t M, int64_t N, int64_t K, int out, void* Y, int64_t ldy, void* workspace,
+                  size_t ws_bytes, void* stream);
+
+/*
+ * qr_mxfp4_linear -- the per-linear call of a rollout engine with MXFP4 weights:
+ *   tokens X quantized block-wise to xfmt (QR_ACT_MXFP4 as qr_mxfp4_quantize,
+ *   QR_ACT_MXFP8 as qr_mx_quantize, non-finite blocks as above), then
+ *   qr_mxfp4_gemm with out = QR_OUT_BF16.
+ *
+ *   X        [M, ldx] bf16, rows on 16-byte boundaries (read).
+ *   workspace  qr_workspace_size("qr_mxfp4_linear", M, N, K, xfmt) bytes (never 0
+ *            when M, N, K > 0), 256-byte aligned: the product's, then codes and
+ *            scales.
+ */
+int qr_mxfp4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const uint8_t* sw, int64_t M,
+                    int64_t N, int64_t K, void* Y, int64_t ldy, void* workspace, size_t ws_bytes,
+                    void* stream);
+
+/*
+ * qr_block_norm_quant -- what stands between two blocks of a decoder layer (the
+ * attention's O projection and the MLP, or the down projection and the next
+ * layer), in one pass: the norm of the block's output, its gate, the scaled
+ * residual stream, and the next block's norm with the quantization of its output.
+ *
+ * For every token m (K = row length, values widened exactly to fp32):
+ *   n_k  = norm(Y[m,:])_k with post_gamma, post_beta   (Y[m,k] without post_gamma)
+ *   t_k  = fl32(n_k * gate_k)                           (n_k without a gate)
+ *   h'_k = bf16_rne(fl32(fl32(res_scale * H[m,k]) + t_k))  -> Hout[m,k]
+ *   z_k  = norm(h')_k with gamma, beta (UAQ's s folded in, as for qr_norm_quant)
+ *   codes, scales = z in format fmt: the per-token formats as qr_norm_quant, the
+ *   block formats as qr_mxfp4_quantize / qr_mx_quantize of the fp32 z, QR_ACT_BF16
+ *   bf16_rne(z) (for qr_linear_fused and qr_mxfp4_linear).
+ * Both norms are of kind `norm` with the arithmetic of qr_norm_quant: codes and
+ * scales are bit for bit those of qr_norm_quant(Hout, gamma, beta).
+ *
+ *   Y, H     [M, ldy], [M, ldh] bf16: block output and residual stream (read).
+ *   post_gamma, post_beta  NULL or [K] fp32 (post_beta only with post_gamma).
+ *   gate     NULL, or with ldgate = 0 a gate per channel, [K] fp32, else a gate
+ *            per token and channel, [M, ldgate] bf16.
+ *   res_scale  finite. gamma [K] fp32, beta NULL or [K] fp32; 16-byte aligned.
+ *   eps      finite, >= 0 (both norms).
+ *   Hout     [M, ldo] bf16 (written). It may be H, Y or a per-token gate itself
+ *            (same pointer and stride); rows that overlap in another way are
+ *            refused.
+ *   codes, scales  as fmt says (written); codes dense and 16-byte, scales 4-byte
+ *            aligned. scales is not used by QR_ACT_BF16.
+ * K a multiple of 16 (32 for the block formats), at most 32768; strides multiples
+ * of 8. Per-token formats take finite inputs; the block formats and bf16 follow the
+ * formula for others (a NaN in a row makes its z NaN, an infinity makes r zero), and
+ * a block whose z is not finite is a NaN block.
+ */
+int qr_block_norm_quant(const void* Y, int64_t ldy, const void* H, int64_t ldh, int64_t M, int64_t K,
+                        int norm, const float* post_gamma, const float* post_beta, const void* gate,
+                        int64_t ldgate, float res_scale, const float* gamma, const float* beta, float eps,
+                        int fmt, void* Hout, int64_t ldo, void* codes, void* scales, void* stream);
+
+/*
+ * qr_silu_mul_mx -- the input of an MXFP4 down projection: SiLU(gate) * up as
+ * qr_silu_mul_quant evaluates it, quantized block-wise to fmt (QR_ACT_MXFP4 or
+ * QR_ACT_MXFP8). The block scales are powers of two, so there is no act_mult: a
+ * UAQ factor belongs into the weights of the other side.
+ *
+ *   G, U     [M, ldg] / [M, ldu] bf16 (read), strides multiples of 8.
+ *   N        multiple of 32. codes [M, N/2] or [M, N], scales
+ *            [ceil(N/128)][M][4], 4-byte aligned (written).
+ */
+int qr_silu_mul_mx(const void* G, const void* U, int64_t M, int64_t N, int64_t ldg, int64_t ldu, int fmt,
+                   void* codes, uint8_t* scales, void* stream);
+
+/*
  * qr_w8a8_gemm -- quantized product and dequantization epilogue
  *   [Notes/System] (INT8/FP8 matmul), [Notes/Training].
  *
@@ -407,7 +544,9 @@ int qr_linear_fused_noalloc(const void* X, int64_t ldx, float act_mult, const vo
 /*
  * qr_workspace_size -- bytes of workspace needed by `fn` ("qr_w8a8_gemm",
  * "qr_w8a8_gemm_quant" or "qr_linear_fused") for this shape; 0 if none. For "qr_acr_tis_loss" M is
- * the token count n (N, K and qt are ignored). Pure host function: it
+ * the token count n (N, K and qt are ignored); for "qr_mxfp4_gemm" and
+ * "qr_mxfp4_linear" qt is the tokens' format (QR_ACT_MXFP4 or QR_ACT_MXFP8). Pure
+ * host function: it
  * depends only on its arguments (and on qr_set_plan_override). Returns
  * (size_t)-1 for an unknown fn or invalid sizes.
  */

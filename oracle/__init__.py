@@ -32,6 +32,8 @@ from .formats import (
     e4m3fn_decode,
     e4m3fn_encode,
     E4M3FN_MAX,
+    e2m1_decode,
+    e2m1_encode,
 )
 from .qurl import (
     QMAX,
@@ -55,6 +57,11 @@ from .qurl import (
     mx_exponent,
     mx_quantize_rows,
     mx_linear,
+    mxfp4_exponent,
+    mxfp4_quantize_rows,
+    mxfp4_pack,
+    mx_values,
+    block_norm,
     requantize_weights,
     flip_expectation,
     decode_chain,
@@ -68,5 +75,7 @@ __all__ = [
     "count_flips", "count_flips_rows",
     "norm_folded", "norm_quant", "silu_mul", "silu_mul_quant", "acr_tis_loss",
     "MX_BLOCK", "mx_exponent", "mx_quantize_rows", "mx_linear", "requantize_weights",
+    "e2m1_decode", "e2m1_encode", "mxfp4_exponent", "mxfp4_quantize_rows", "mxfp4_pack", "mx_values",
+    "block_norm",
     "decode_chain",
 ]

@@ -119,3 +119,34 @@ def e4m3fn_encode(x):
     mag_code = np.where(take_hi, _POS_CODES[idx_hi], _POS_CODES[idx_lo])
     sign = np.signbit(x).astype(np.uint8) << np.uint8(7)
     return (mag_code.astype(np.uint8) | sign).astype(np.uint8)
+
+
+# ----------------------------------------------------------------------------
+# FP4 E2M1
+# ----------------------------------------------------------------------------
+
+E2M1_MAX = 6.0
+
+
+def e2m1_decode(codes):
+    """Decode E2M1 codes 0..15 (sign, two exponent bits, one mantissa bit, bias 1)."""
+    c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+    e, m = (c >> 1) & 3, c & 1
+    mag = np.where(e == 0, 0.5 * m, (1.0 + 0.5 * m) * np.power(2.0, (e - 1).astype(np.float64)))
+    return np.where(c & 8, -mag, mag)
+
+
+def e2m1_encode(x):
+    """Round float32 values in [-6, 6] to E2M1, nearest with ties to the even code; the sign
+    bit is x's, also for values that round to zero."""
+    x = np.ascontiguousarray(x, dtype=np.float32)
+    ax = np.abs(x.astype(np.float64))
+    if not np.all(ax <= E2M1_MAX):
+        raise ValueError("e2m1_encode: |x| > 6 or not finite")
+    vals = e2m1_decode(np.arange(8))
+    mids = (vals[:-1] + vals[1:]) / 2  # exact
+    # values above the midpoint below an odd code and at or above the one below an even code
+    up = np.searchsorted(mids, ax, side="left").astype(np.uint8)
+    tie = np.isin(ax, mids)
+    code = np.where(tie & (up & 1 == 1), up + 1, up).astype(np.uint8)
+    return code | (np.signbit(x).astype(np.uint8) << np.uint8(3))

@@ -22,6 +22,8 @@ from .formats import (
     bf16_bits_to_f32,
     e4m3fn_decode,
     e4m3fn_encode,
+    e2m1_decode,
+    e2m1_encode,
     f32_to_bf16_bits,
 )
 
@@ -506,3 +508,66 @@ def mx_linear(Xc, Xe, Wc, We, block=MX_BLOCK):
         acc += np.ldexp(part, (Xe[:, b:b + 1].astype(np.int64) + We[None, :, b].astype(np.int64)))
     return acc, f32_to_bf16_bits(acc.astype(np.float32))
 
+
+
+# ----------------------------------------------------------------------------
+# MXFP4: E2M1 elements, power-of-two scale per 32 elements
+# ----------------------------------------------------------------------------
+
+def mxfp4_exponent(amax):
+    """Smallest integer X with amax <= 6 * 2^X, clamped to [-127, 127]; 0 gives -127.
+    With amax = f 2^e, f in [0.5, 1) and 6 = 0.75 2^3: X = e - 3 if f <= 0.75 else e - 2."""
+    a = np.asarray(amax, np.float64)
+    f, e = np.frexp(a)
+    X = np.where(f <= 0.75, e - 3, e - 2)
+    X = np.where(a == 0, -127, X)
+    return np.clip(X, -127, 127).astype(np.int16)
+
+
+def mxfp4_quantize_rows(A, block=MX_BLOCK):
+    """MXFP4 of fp32 rows: (codes uint8 [R, K], one E2M1 code each, X int16 [R, K / block]).
+    A block with a NaN or an infinity has X = 128 (scale byte 255) and zero codes."""
+    A = np.ascontiguousarray(A, dtype=np.float32)
+    R, K = A.shape
+    if K % block:
+        raise ValueError("K must be a multiple of the block")
+    Ab = A.reshape(R, K // block, block).astype(np.float64)
+    bad = ~np.isfinite(Ab).all(axis=2)
+    Ab = np.where(bad[:, :, None], 0.0, Ab)
+    X = mxfp4_exponent(np.abs(Ab).max(axis=2) if K else np.zeros((R, 0)))
+    v = np.ldexp(Ab, -X[:, :, None].astype(np.int64))
+    v = np.copysign(v.astype(np.float32), np.where(bad[:, :, None], 0.0, Ab))
+    codes = e2m1_encode(v.reshape(R, K))
+    return codes, np.where(bad, 128, X).astype(np.int16)
+
+
+def mxfp4_pack(codes):
+    """[R, K] codes -> [R, K / 2] bytes, element 2 i in the low half."""
+    c = np.asarray(codes, np.uint8)
+    return (c[:, 0::2] | (c[:, 1::2] << 4)).astype(np.uint8)
+
+
+def mx_values(codes, X, fmt, block=MX_BLOCK):
+    """float64 values of block-wise codes ("mxfp4": unpacked E2M1 codes, "mxfp8": E4M3FN bytes)."""
+    v = e2m1_decode(codes) if fmt == "mxfp4" else e4m3fn_decode(codes)
+    X = np.asarray(X)
+    s = np.where(X == 128, np.nan, np.ldexp(1.0, np.where(X == 128, 0, X).astype(np.int64)))
+    return v * np.repeat(s, block, axis=1)
+
+
+def block_norm(Y_bits, H_bits, gamma, post_gamma=None, gate=None, res=1.0, beta=None, post_beta=None,
+               eps=1e-6, kind="rms"):
+    """The step between two blocks: n = norm(Y) (or Y), t = fl32(n * gate) (or n),
+    h' = bf16(fl32(fl32(res * H) + t)), z = norm(h'). gate: None, fp32 [K], or bf16 bits [M, K].
+    Returns (bf16 bits of h', z float32)."""
+    n = bf16_bits_to_f32(Y_bits).astype(np.float32)
+    if post_gamma is not None:
+        n, _ = norm_folded(Y_bits, post_gamma, post_beta, eps, kind)
+    if gate is not None:
+        g = np.asarray(gate)
+        g = bf16_bits_to_f32(g) if g.dtype == np.uint16 else g[None, :]
+        n = (n * g.astype(np.float32)).astype(np.float32)
+    h = (bf16_bits_to_f32(H_bits).astype(np.float32) * np.float32(res)).astype(np.float32)
+    hb = f32_to_bf16_bits((h + n).astype(np.float32))
+    z, _ = norm_folded(hb, gamma, beta, eps, kind)
+    return hb, z

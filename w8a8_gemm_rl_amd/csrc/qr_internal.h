@@ -34,6 +34,38 @@ hipError_t launch_acr_tis(const float* logp, const float* lprox, const float* lb
 hipError_t launch_requant(const float* Wp, int64_t N, int64_t K, int64_t ldw, int qt, void* Wq,
                           float* scale_w, uint32_t* row_flips, hipStream_t st);
 
+// MXFP4 operators (mxfp4_kernels.hip) and block norms (block_kernels.hip). `fmt` is
+// one of the header's QR_ACT_* formats.
+hipError_t launch_mx4_quant(const void* A, int64_t R, int64_t K, int64_t lda, int bf16, int fmt,
+                            void* codes, uint8_t* scales, hipStream_t st);
+hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int fmt,
+                             void* out, int64_t ldo, int bf16, hipStream_t st);
+size_t mx4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int xfmt);
+hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq,
+                           const uint8_t* sw, int64_t M, int64_t N, int64_t K, int out_raw, void* Y,
+                           int64_t ldy, void* ws, hipStream_t st);
+hipError_t launch_mx4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const uint8_t* sw,
+                             int64_t M, int64_t N, int64_t K, void* Y, int64_t ldy, void* ws,
+                             hipStream_t st);
+// Workspace of qr_mxfp4_gemm / qr_mxfp4_linear; (size_t)-1 for invalid sizes.
+size_t mx4_workspace(const char* fn, int64_t M, int64_t N, int64_t K, int xfmt);
+
+struct BlockNormArgs {
+  const uint16_t *Y, *H;
+  const void* gate;  // NULL, fp32 [K], or (gate_rows) bf16 [M, ldgate]
+  const float *post_gamma, *post_beta, *gamma, *beta;
+  uint16_t* Hout;
+  uint8_t* codes;
+  void* scales;
+  int64_t ldy, ldh, ldgate, ldo, M, K;
+  float res, eps;
+  int fmt;
+  bool gate_rows;
+};
+hipError_t launch_block_norm(const BlockNormArgs& p, int kind, hipStream_t st);
+hipError_t launch_silu_mx(const void* G, const void* U, int64_t M, int64_t N, int64_t ldg, int64_t ldu,
+                          int fmt, void* codes, uint8_t* scales, hipStream_t st);
+
 // Error reporting of the C ABI (qr_last_error): set the thread-local message
 // and return `code`; hip_error maps a HIP error to QR_ERR_HIP / QR_ERR_NO_DEVICE.
 int set_error(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));

@@ -1,0 +1,130 @@
+// Block-scaled (microscaled) formats: device helpers shared by the kernels that
+// write or read 32-element blocks with one power-of-two scale.
+//
+//   E2M1   S.EE.M, bias 1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two to
+//          a byte, element 2 i in the low half.
+//   E4M3   as in qr_device.h, a byte each.
+//   scale  byte X + 127 for 2^X (E8M0), 255 for a block that holds a NaN or an
+//          infinity. X is the smallest integer in [-127, 127] with
+//          max |v| <= top 2^X (top = 6 or 448), so no element is clipped.
+//
+// Scale bytes lie in panels of 128 elements of K, [ceil(K / 128)][rows][4].
+#pragma once
+
+#include "qr_device.h"
+
+namespace qr {
+
+// Formats of token codes (the header's QR_ACT_*).
+constexpr int kActInt8 = 0, kActFp8 = 1, kActMxFp8 = 2, kActMxFp4 = 3, kActBf16 = 4;
+
+// Scale byte of a block from the bits of max |v| (sign cleared). amax = 1.m 2^(E - 127);
+// 6 = 1.5 2^2 and 448 = 1.75 2^8, so X + 127 is E - 2 (E - 8), one more where the
+// mantissa exceeds top's. Integers only: subnormal and zero blocks give 0 (X = -127).
+template <bool FP4>
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t abits) {
+  if (abits >= 0x7f800000u) return 255u;
+  const int s = (int)(abits >> 23) - (FP4 ? 2 : 8) +
+                ((abits & 0x7fffffu) > (FP4 ? 0x400000u : 0x600000u) ? 1 : 0);
+  return (uint32_t)(s < 0 ? 0 : s);
+}
+
+// 2^-X for a scale byte other than 255 (a normal fp32: the byte is at most 253).
+// Products with it are exact unless they fall below fp32's normal range, far under
+// half of the formats' smallest step.
+__device__ __forceinline__ float mx_inv_scale(uint32_t sb) {
+  return __uint_as_float((254u - sb) << 23);
+}
+
+// 2^X (byte 0 is the subnormal 2^-127), NaN for byte 255.
+__device__ __forceinline__ float mx_scale_value(uint32_t sb) {
+  return __uint_as_float(sb == 0u ? 0x400000u : (sb == 255u ? 0x7fc00000u : sb << 23));
+}
+
+// Eight E2M1 codes of values already divided by the scale (|v| <= 6), packed low
+// half first; v_cvt_scalef32_pk_fp4_f32 rounds to nearest, ties to even, and keeps
+// the sign of values that round to zero.
+__device__ __forceinline__ uint32_t mx_fp4_codes8(const float* v) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], 1.0f, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], 1.0f, 3);
+  return w;
+}
+
+__device__ __forceinline__ uint2 mx_fp8_codes8(const float* v) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+__device__ __forceinline__ uint32_t abs_bits_max8(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t a = __float_as_uint(v[e]) & 0x7fffffffu;
+    m = a > m ? a : m;
+  }
+  return m;
+}
+
+// Scale byte of the 32-element block that lanes 4 j .. 4 j + 3 hold, eight values
+// each (every lane of the four gets it). Integer maximum of the sign-cleared bits:
+// the order of non-negative floats, with NaN above infinity above every number.
+template <bool FP4>
+__device__ __forceinline__ uint32_t mx_block_scale(const float* v) {
+  uint32_t m = abs_bits_max8(v);
+  uint32_t o = (uint32_t)__shfl_xor((int)m, 1, 64);
+  m = o > m ? o : m;
+  o = (uint32_t)__shfl_xor((int)m, 2, 64);
+  m = o > m ? o : m;
+  return mx_scale_byte<FP4>(m);
+}
+
+// Codes of eight values of a block with scale byte sb (zero codes in a NaN block).
+template <bool FP4>
+__device__ __forceinline__ uint2 mx_codes8(const float* v, uint32_t sb) {
+  if (sb == 255u) return make_uint2(0u, 0u);
+  const float inv = mx_inv_scale(sb);
+  float t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = v[e] * inv;
+  if constexpr (FP4) return make_uint2(mx_fp4_codes8(t), 0u);
+  else return mx_fp8_codes8(t);
+}
+
+// Stores the codes and scale bytes of a row's values when every lane holds eight
+// consecutive ones: chunk c (values 8 c .. 8 c + 7) of row `row`, c ascending with
+// the lane and c % 16 == lane % 16. `live` lanes hold values (whole blocks of 32),
+// the others zeros. A panel's four scale bytes are stored as one word; the bytes of a
+// last panel that no block owns come out zero.
+template <bool FP4>
+__device__ __forceinline__ void mx_store_row8(const float* v, bool live, int64_t row, int64_t R,
+                                              int64_t c, int64_t K, uint8_t* codes, uint8_t* scales) {
+  const uint32_t sb = mx_block_scale<FP4>(v);
+  const int lane = threadIdx.x & 63;
+  uint32_t w = sb << (8 * ((lane >> 2) & 3));
+  w |= (uint32_t)__shfl_xor((int)w, 4, 64);
+  w |= (uint32_t)__shfl_xor((int)w, 8, 64);
+  if (!live) return;
+  const uint2 q = mx_codes8<FP4>(v, sb);
+  if constexpr (FP4) *reinterpret_cast<uint32_t*>(codes + row * (K >> 1) + 4 * c) = q.x;
+  else *reinterpret_cast<uint2*>(codes + row * K + 8 * c) = q;
+  if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + ((c >> 4) * R + row) * 4) = w;
+}
+
+// fp32 -> bf16 bits, round to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t f32_to_bf16_any(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return (u & 0x7fffffffu) > 0x7f800000u ? ((u >> 16) | 0x40u) : f32_to_bf16_rne(f);
+}
+
+__device__ __forceinline__ void bf16x8(const uint4 v, float* h) {
+  h[0] = bf16_lo(v.x); h[1] = bf16_hi(v.x); h[2] = bf16_lo(v.y); h[3] = bf16_hi(v.y);
+  h[4] = bf16_lo(v.z); h[5] = bf16_hi(v.z); h[6] = bf16_lo(v.w); h[7] = bf16_hi(v.w);
+}
+
+}  // namespace qr
