@@ -349,7 +349,7 @@ int qr_mx_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_
  *            qr_silu_mul_mx.
  *   Wq, sw   [N, K/2] codes and scale panels of qr_mxfp4_quantize.
  *            Xq, Wq, sx, sw and Y start on 16-byte boundaries.
- *   K        multiple of 128; code matrices below 2^31 - 2^16 bytes.
+ *   K        multiple of 128; code matrices below 2^31 - 2^16 bytes, M N < 2^38.
  *   Y        [M, ldy] bf16 or fp32, any ldy >= N (written).
  *   workspace  qr_workspace_size("qr_mxfp4_gemm", M, N, K, xfmt) bytes, 256-byte
  *            aligned, contents irrelevant; may be NULL when that is 0.

@@ -34,6 +34,8 @@ int check_product(const char* fn, int64_t M, int64_t N, int64_t K, int xfmt) {
     return qr::set_error(QR_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 128", fn, (long long)K);
   if (N * (K / 2) >= kMaxCodeBytes || M * code_row_bytes(K, xfmt) >= kMaxCodeBytes)
     return qr::set_error(QR_ERR_UNSUPPORTED, "%s: code matrices must stay below 2^31 - 2^16 bytes", fn);
+  if (M * N >= (int64_t)1 << 38)
+    return qr::set_error(QR_ERR_UNSUPPORTED, "%s: M * N must stay below 2^38", fn);
   return QR_OK;
 }
 

@@ -10,6 +10,9 @@
 // E4M3: elements [16 g, 16 g + 16) and [64 + 16 g, 64 + 16 g + 16); in both the
 // lane's scale byte is that of block g. Register i of the result is weight row
 // 4 g + i, token l % 16.
+#include <type_traits>
+
+#include "qr_copy.h"
 #include "qr_internal.h"
 #include "qr_mx.h"
 
@@ -18,6 +21,7 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 // One chunk of eight values per lane, four lanes a block; 256 chunks per block of
 // threads, rows padded to whole 16-chunk panels so that lanes keep their place.
@@ -100,7 +104,8 @@ struct Mx4Params {
   int out_raw;
 };
 
-// Store of a lane's four consecutive output channels of one token.
+// Store of a lane's four consecutive output channels n .. n + 3 (n a multiple of 4) of
+// one token.
 __device__ __forceinline__ void mx4_store4(const Mx4Params& p, int64_t m, int64_t n, const float* a) {
   if (m >= p.M || n >= p.N) return;
   const bool full = n + 3 < p.N && (p.ldy & 3) == 0;
@@ -120,48 +125,630 @@ __device__ __forceinline__ void mx4_store4(const Mx4Params& p, int64_t m, int64_
   }
 }
 
-// A block owns 16 weight rows x 16 tokens; its 8 waves take the 128-element panels
-// of K in turn (operands straight from memory to registers), and the waves' partial
-// sums are added in a fixed order.
-template <bool XFP4>
-__global__ __launch_bounds__(512) void mx4_stream_kernel(const Mx4Params p) {
-  __shared__ float4 red[8][64];
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+// Few tokens: a weight stream. A block owns 16 weight rows and up to 16 tokens; its NW
+// waves take the 256-element pairs of panels of K in turn (a row's pair is one 128-byte
+// line), weights straight from memory to registers with D pairs a wave in flight, and
+// the waves' partial sums are added in a fixed order. FUSED: the block first quantizes
+// the bf16 tokens into LDS itself (the first weights are on their way meanwhile), else
+// token codes are read from memory like the weights.
+template <bool XFP4, bool FUSED, int NW, int KW, int D>
+__global__ __launch_bounds__(64 * NW) void mx4_decode_kernel(const Mx4Params p,
+                                                             const uint16_t* __restrict__ X,
+                                                             int64_t ldx) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // FUSED: codes, then scales
+  __shared__ float4 red[KW > 1 ? NW : 1][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wid = wave % KW;  // the wave's part of K
   const int r = lane & 15, g = lane >> 4;
-  const int64_t tiles_m = (p.M + 15) >> 4;
-  const int64_t tn = blockIdx.x / tiles_m, tm = blockIdx.x % tiles_m;
-  const int64_t n = tn * 16 + r < p.N ? tn * 16 + r : p.N - 1;
-  const int64_t m = tm * 16 + r < p.M ? tm * 16 + r : p.M - 1;
-  const uint8_t* wr = p.Wq + n * (p.K >> 1) + 16 * g;
-  const uint8_t* xr = p.Xq + (XFP4 ? m * (p.K >> 1) : m * p.K) + 16 * g;
+  const int M = (int)p.M, K = (int)p.K, np = K >> 7, npair = (np + 1) >> 1;
+  const int64_t n0 = ((int64_t)blockIdx.x * (NW / KW) + wave / KW) * 16;
+  const int64_t n = n0 + r < p.N ? n0 + r : p.N - 1;  // rows past N repeat the last, unstored
+  const int m = r < M ? r : M - 1;
+  const int rb = XFP4 ? K >> 1 : K;
+  const uint8_t* wr = p.Wq + n * (K >> 1) + 16 * g;
+  const uint8_t* ws = p.sw + n * 4 + g;
+
+  uint4 a[D][2];
+  int ea[D][2];
+  auto load = [&](int d, int pair) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = 2 * pair + e;
+      if (k < np) {
+        a[d][e] = *reinterpret_cast<const uint4*>(wr + k * 64);
+        ea[d][e] = ws[(int64_t)k * p.N * 4];
+      }
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (wid + d * KW < npair) load(d, wid + d * KW);
+
+  if constexpr (FUSED) {
+    // eight values a thread, four threads a block of 32; XC loads a thread at once
+    constexpr int XC = 4;
+    const int cpr = K >> 3, total = M * cpr;
+    uint8_t* xsc = xs + M * rb;
+    for (int c0 = threadIdx.x; c0 < (total + 63) / 64 * 64; c0 += XC * 64 * NW) {
+      uint4 x[XC];
+#pragma unroll
+      for (int u = 0; u < XC; ++u) {
+        const int c = c0 + u * 64 * NW, t = c / cpr;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < total) x[u] = *reinterpret_cast<const uint4*>(X + t * ldx + 8 * (c - t * cpr));
+      }
+#pragma unroll
+      for (int u = 0; u < XC; ++u) {
+        const int c = c0 + u * 64 * NW, t = c / cpr, q = c - t * cpr;
+        float v[8];
+        bf16x8(x[u], v);
+        const uint32_t sb = mx_block_scale<XFP4>(v);
+        if (c < total) {
+          const uint2 w = mx_codes8<XFP4>(v, sb);
+          if constexpr (XFP4) *reinterpret_cast<uint32_t*>(xs + t * rb + 4 * q) = w.x;
+          else *reinterpret_cast<uint2*>(xs + t * rb + 8 * q) = w;
+          if ((q & 3) == 0) xsc[t * (K >> 5) + (q >> 2)] = (uint8_t)sb;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const uint8_t* xr = (FUSED ? xs : p.Xq) + (int64_t)m * rb + 16 * g;
+  const uint8_t* xsc = FUSED ? xs + M * rb + m * (K >> 5) + g : p.sx + m * 4 + g;
+  const int xstep = FUSED ? 4 : M * 4;
+
   v4f acc = {};
-  const int64_t np = p.K >> 7;
-  for (int64_t k = wid; k < np; k += 8) {
-    const uint4 a = *reinterpret_cast<const uint4*>(wr + k * 64);
-    const int ea = p.sw[(k * p.N + n) * 4 + g];
-    const int eb = p.sx[(k * p.M + m) * 4 + g];
-    const v8i A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-    if constexpr (XFP4) {
-      const uint4 b = *reinterpret_cast<const uint4*>(xr + k * 64);
-      const v8i B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, 0, ea, 0, eb);
-    } else {
-      const uint4 b = *reinterpret_cast<const uint4*>(xr + k * 128);
-      const uint4 c = *reinterpret_cast<const uint4*>(xr + k * 128 + 64);
-      const v8i B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, (int)c.x, (int)c.y, (int)c.z, (int)c.w};
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 0, 0, ea, 0, eb);
+  for (int i = wid; i < npair; i += D * KW) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int pair = i + d * KW;
+      if (pair >= npair) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k = 2 * pair + e;
+        if (k >= np) break;
+        const uint4 w = a[d][e];
+        const v8i A = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+        const int eb = xsc[(int64_t)k * xstep];
+        if constexpr (XFP4) {
+          const uint4 b = *reinterpret_cast<const uint4*>(xr + k * 64);
+          const v8i B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+          acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, 0, ea[d][e], 0, eb);
+        } else {
+          const uint4 b = *reinterpret_cast<const uint4*>(xr + k * 128);
+          const uint4 c = *reinterpret_cast<const uint4*>(xr + k * 128 + 64);
+          const v8i B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, (int)c.x, (int)c.y, (int)c.z, (int)c.w};
+          acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 0, 0, ea[d][e], 0, eb);
+        }
+      }
+      if (pair + D * KW < npair) load(d, pair + D * KW);
     }
   }
-  red[wid][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  __syncthreads();
-  if (wid != 0) return;
-  float s[4] = {};
+  float s[4] = {acc[0], acc[1], acc[2], acc[3]};
+  if constexpr (KW > 1) {
+    red[wave][lane] = make_float4(s[0], s[1], s[2], s[3]);
+    __syncthreads();
+    if (wid != 0) return;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const float4 v = red[w][lane];
-    s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+    for (int w = 1; w < KW; ++w) {
+      const float4 v = red[wave + w][lane];
+      s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+    }
   }
-  mx4_store4(p, tm * 16 + r, tn * 16 + 4 * g, s);
+  mx4_store4(p, r, n0 + 4 * g, s);
+}
+
+// ---------------------------------------------------------------------------
+// Tiled product: BN weight rows x BM tokens per block, a ring of S stages in LDS. A
+// stage holds KS elements of K: weight rows (KS / 2 bytes each), token rows (KS / 2
+// or KS bytes) and the scale bytes of both (4 per row and 128-element panel), moved
+// global -> LDS by LDS-DMA copies (16 bytes a lane). The block's waves form a WN x WM
+// grid, each owning BN / WN x BM / WM outputs as T x T fragments.
+//
+// LDS rows of 64 bytes are paired, so that every 128-byte line has eight 16-byte
+// chunks; chunk q of line i sits at q ^ (i & 7) (rows of 128 bytes: i = r / 2, as for
+// the 8-bit GEMMs), which spreads a fragment's reads over all banks. The swizzle is
+// applied on the global side of the copies.
+//
+// Operands of a fragment's next K step are read from LDS while the matrix cores work
+// on the current one, across the stage boundary too: the barrier that opens a stage
+// stands before the last K step of the one before, whose operands are already in
+// registers, so its slot can be refilled at once.
+//
+// A T = 32 fragment takes 64 elements per MFMA (T = 16: 128); lane l holds row l % T
+// and, with g = l / T, E2M1 elements [32 g, 32 g + 32) or E4M3 elements [16 g, + 16)
+// and [KI / 2 + 16 g, + 16), and the scale byte of block g of the KI elements. A
+// lane's scale word (the panel's four bytes of its row) is shifted by 8 g, so that
+// byte 0 (and for T = 32 byte 2 in the panel's second half) is the one it needs.
+//
+// Rows past N or M are copied as zeros and not stored. With splits > 1 a block takes one
+// contiguous part of its tile's stages and writes fp32 partial sums, which
+// mx4_sum_kernel adds in a fixed order.
+// ---------------------------------------------------------------------------
+// One copy of LANES lanes' 16 bytes (a power of two), exec being all ones before and after.
+template <int LANES>
+__device__ __forceinline__ void dma_lanes(uint32_t lds_addr, uint32_t vo, __amdgpu_buffer_rsrc_t r) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  if constexpr (LANES == 64)
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 : : "s"(lds_addr), "v"(vo), "s"(r) : "memory", "m0");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_mov_b64 exec, %3\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
+        "s_mov_b64 exec, -1"
+        : : "s"(lds_addr), "v"(vo), "s"(r), "s"(((uint64_t)1 << (LANES & 63)) - 1) : "memory", "m0");
+#pragma clang diagnostic pop
+}
+
+struct Mx4TileParams {
+  Mx4Params g;
+  float* part;
+  int tiles_m, tiles_n, stages, splits;
+};
+
+template <int T>
+struct Mx4Mfma;
+template <>
+struct Mx4Mfma<16> {
+  using acc_t = v4f;
+  static constexpr int KI = 128;
+  template <bool XFP4, int OP>
+  static __device__ __forceinline__ acc_t run(v8i a, v8i b, acc_t c, int sa, int sb) {
+    static_assert(OP == 0, "one step per panel");
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, XFP4 ? 4 : 0, 0, sa, 0, sb);
+  }
+};
+template <>
+struct Mx4Mfma<32> {
+  using acc_t = v16f;
+  static constexpr int KI = 64;
+  template <bool XFP4, int OP>
+  static __device__ __forceinline__ acc_t run(v8i a, v8i b, acc_t c, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, XFP4 ? 4 : 0, 2 * OP, sa, 2 * OP, sb);
+  }
+};
+
+template <bool XFP4, int T, int BN, int BM, int WN, int WM, int S, int KS>
+__global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4TileParams p) {
+  using MF = Mx4Mfma<T>;
+  using acc_t = typename MF::acc_t;
+  constexpr int NW = WN * WM;
+  constexpr int KI = MF::KI, NKK = KS / KI, PP = KS / 128;  // K steps, panels per stage
+  constexpr int RA = KS / 2, RB = XFP4 ? KS / 2 : KS;       // bytes per row and stage
+  constexpr int WTN = BN / WN, WTM = BM / WM, FN = WTN / T, FM = WTM / T;
+  constexpr int IA = (BN * RA / 1024 + NW - 1) / NW * NW, IB = (BM * RB / 1024 + NW - 1) / NW * NW;
+  constexpr int NA = IA / NW, NB = IB / NW, GA = (NA + 3) / 4, GB = (NB + 3) / 4;
+  constexpr int CODES = (IA + IB) * 1024, STAGE = CODES + PP * 2048;
+  constexpr int SL = 128 * PP / NW;  // lanes of a wave's scale copy
+  constexpr int NI = NA + NB + 1;    // copies per wave and stage
+  static_assert(RA == 64 || RA == 128, "weight rows of half a line or a line");
+  static_assert(RB == 64 || RB == 128 || RB == 256, "token rows of half a line to two");
+  static_assert(NKK % 2 == 0, "operand buffers alternate within a stage");
+  static_assert(BN * RA % 1024 == 0 && BM * RB % 1024 == 0, "whole copies");
+  static_assert(WTN % T == 0 && WTM % T == 0 && BN <= 256 && BM <= 256, "wave tile");
+  static_assert(SL >= 1 && SL <= 64 && 64 % SL == 0, "one scale copy per wave");
+  static_assert(S >= 2 && (S - 1) * NI <= 63 && S * STAGE <= 160 * 1024, "ring");
+
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+
+  const int64_t N = p.g.N, M = p.g.M, K = p.g.K;
+  // neighbouring tiles on one XCD; groups of up to 8 token tiles share weight tiles
+  const int G8 = gridDim.x & ~7;
+  int b = blockIdx.x;
+  if (b < G8) b = (b & 7) * (G8 >> 3) + (b >> 3);
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int split = b / tiles;
+  b -= split * tiles;
+  const int grp = b / (8 * p.tiles_n), m0 = grp * 8;
+  const int gm = p.tiles_m - m0 < 8 ? p.tiles_m - m0 : 8;
+  b -= m0 * p.tiles_n;
+  const int tm = m0 + b % gm, tn = b / gm;
+  const int ks0 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.stages * split / p.splits));
+  const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)p.stages * (split + 1) / p.splits)) - ks0;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wid % WN, wm = wid / WN;
+  constexpr uint32_t kBig = 0x80000000u;
+  const int64_t ra = K >> 1, rb = XFP4 ? K >> 1 : K;  // bytes per row
+  const uint32_t spw = (uint32_t)(N * 4), spx = (uint32_t)(M * 4);
+  const uint32_t np = (uint32_t)(K >> 7);
+  const __amdgpu_buffer_rsrc_t rw =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.Wq, (short)0, (int)(uint32_t)(N * ra), kBufWord3);
+  const __amdgpu_buffer_rsrc_t rx =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.Xq, (short)0, (int)(uint32_t)(M * rb), kBufWord3);
+  const __amdgpu_buffer_rsrc_t rsw =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.sw, (short)0, (int)(np * spw), kBufWord3);
+  const __amdgpu_buffer_rsrc_t rsx =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.sx, (short)0, (int)(np * spx), kBufWord3);
+
+  // Copies: instruction i of an operand fills LDS lines 8 i .. 8 i + 7; lane l the
+  // physical chunk l % 8 of line 8 i + l / 8.
+  const int ll = lane >> 3, pc = lane & 7;
+  auto place = [&](int i, int rowbytes, int& row, int& chunk) {
+    const int line = i * 8 + ll;
+    if (rowbytes == 256) {
+      row = line >> 1;
+      chunk = ((line & 1) << 3) | (pc ^ (row & 7));
+    } else if (rowbytes == 128) {
+      row = line;
+      chunk = pc ^ ((line >> 1) & 7);
+    } else {
+      const int q = pc ^ (line & 7);
+      row = 2 * line + (q >> 2);
+      chunk = q & 3;
+    }
+  };
+  uint32_t oa[NA], ob[NB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    int r, c;
+    place(wid * NA + i, RA, r, c);
+    const int64_t row = (int64_t)tn * BN + r;
+    oa[i] = ((r < BN && row < N) ? (uint32_t)(row * ra + c * 16) : kBig) - 1024u * (uint32_t)(i % 4);
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    int r, c;
+    place(wid * NB + i, RB, r, c);
+    const int64_t row = (int64_t)tm * BM + r;
+    ob[i] = ((r < BM && row < M) ? (uint32_t)(row * rb + c * 16) : kBig) - 1024u * (uint32_t)(i % 4);
+  }
+  // Scales: the 2 PP kilobytes of a stage (panel, then weights or tokens: four bytes of
+  // each of 256 rows) are split over the waves, SL lanes' 16 bytes each. Words of rows
+  // that are not the tile's belong to rows that are not stored, or are past the array:
+  // zero.
+  const int sp = wid * SL / 64, sl0 = wid * SL % 64;
+  const bool sw_w = (sp & 1) == 0;
+  const uint32_t os = (uint32_t)(((sw_w ? (int64_t)tn * BN : (int64_t)tm * BM) + 4 * (sl0 + lane)) * 4);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+  const uint32_t la0 = lds0 + (uint32_t)(wid * NA) * 1024u;
+  const uint32_t lb0 = lds0 + (uint32_t)(IA + wid * NB) * 1024u;
+  const uint32_t ls0 = lds0 + (uint32_t)CODES + (uint32_t)(wid * SL * 16);
+
+  // K an odd multiple of 128: the second half of the last stage lies past the rows'
+  // ends. Bit i: copy i's lane holds such a chunk.
+  uint32_t past_a = 0, past_b = 0;
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    int r, c;
+    place(wid * NA + i, RA, r, c);
+    past_a |= (c * 32 >= RA ? 1u : 0u) << i;
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    int r, c;
+    place(wid * NB + i, RB, r, c);
+    past_b |= (c * 32 >= RB ? 1u : 0u) << i;
+  }
+  constexpr int NG = GA + GB + 1;  // copy groups of a stage: weights, tokens, scales
+  auto issue_group = [&](int g, int slot, int ks) {
+    const uint32_t so = (uint32_t)(slot * STAGE);
+    if (g == NG - 1) {
+      const uint32_t panel = (uint32_t)(ks * PP + (sp >> 1));
+      const uint32_t vs = panel < np ? os + panel * (sw_w ? spw : spx) : kBig;
+      dma_lanes<SL>(ls0 + so, vs, sw_w ? rsw : rsx);
+      return;
+    }
+    const bool tail = KS == 256 && (ks + 1) * KS > K;
+    const bool isA = g < GA;
+    const uint32_t past = tail ? (isA ? past_a : past_b) : 0u;
+    const int i0 = (isA ? g : g - GA) * 4, n = isA ? NA : NB, cnt = n - i0 < 4 ? n - i0 : 4;
+    const uint32_t base = (isA ? la0 : lb0) + so + (uint32_t)i0 * 1024u;
+    const int soff = ks * (isA ? RA : RB);
+    uint32_t vo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e < n ? i0 + e : 0;
+      vo[e] = isA ? oa[i < NA ? i : 0] : ob[i < NB ? i : 0];
+      if (KS == 256) vo[e] = (past >> i) & 1u ? kBig - 1024u * (uint32_t)(i % 4) : vo[e];
+    }
+    if (cnt == 4) dma_group<4, false>(base, vo, isA ? rw : rx, soff);
+    else if (cnt == 3) dma_group<3, false>(base, vo, isA ? rw : rx, soff);
+    else if (cnt == 2) dma_group<2, false>(base, vo, isA ? rw : rx, soff);
+    else dma_group<1, false>(base, vo, isA ? rw : rx, soff);
+  };
+
+  // Operand reads: byte of chunk c of the wave's first fragment row (rows lr, lr + T,
+  // ... have the same swizzle, and are T rows' bytes apart).
+  const int lr = lane % T, lg = lane / T;
+  auto at = [&](int row0, int c, int rowbytes) {
+    if (rowbytes == 256) return (row0 + lr) * 256 + ((c & 8) << 4) + (((c & 7) ^ (lr & 7)) << 4);
+    if (rowbytes == 128) return (row0 + lr) * 128 + ((c ^ ((lr >> 1) & 7)) << 4);
+    return ((row0 + lr) >> 1) * 128 + ((((lr & 1) * 4 + c) ^ ((lr >> 1) & 7)) << 4);
+  };
+  int xa[NKK], xb[NKK], xb2[NKK];
+#pragma unroll
+  for (int h = 0; h < NKK; ++h) {
+    // chunk of the lane's first 16 bytes: 32 E2M1 elements, 16 E4M3
+    const int ca = h * (KI / 32) + lg, cb = XFP4 ? ca : h * (KI / 16) + lg;
+    xa[h] = at(wn * WTN, ca, RA);
+    xb[h] = IA * 1024 + at(wm * WTM, cb, RB);
+    xb2[h] = XFP4 ? 0 : IA * 1024 + at(wm * WTM, cb + KI / 32, RB);
+  }
+  const int xsa = CODES + (wn * WTN + lr) * 4, xsb = CODES + 1024 + (wm * WTM + lr) * 4, sh = 8 * lg;
+  acc_t acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = acc_t{};
+
+  v8i opa[2][FN], opb[2][FM];
+  int sna[FN], snb[FM], sca[FN], scb[FM];  // scale words: as read, and shifted for use
+  auto load_ops = [&](const uint8_t* st, int h, int buf) {
+    const int panel = h * KI / 128;
+    const bool fresh = h * KI % 128 == 0;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(st + xa[h] + i * T * RA);
+      opa[buf][i] = v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, 0, 0, 0, 0};
+      if (fresh) sna[i] = *reinterpret_cast<const int*>(st + xsa + panel * 2048 + i * T * 4);
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(st + xb[h] + j * T * RB);
+      if constexpr (XFP4) {
+        opb[buf][j] = v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, 0, 0, 0, 0};
+      } else {
+        const uint4 w = *reinterpret_cast<const uint4*>(st + xb2[h] + j * T * RB);
+        opb[buf][j] = v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
+      }
+      if (fresh) snb[j] = *reinterpret_cast<const int*>(st + xsb + panel * 2048 + j * T * 4);
+    }
+  };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < FN; ++i) sca[i] = sna[i] >> sh;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) scb[j] = snb[j] >> sh;
+  };
+  auto multiply_row = [&](int h, int buf, int i) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      if (h * KI % 128 == 0)
+        acc[i][j] = MF::template run<XFP4, 0>(opa[buf][i], opb[buf][j], acc[i][j], sca[i], scb[j]);
+      else if constexpr (T == 32)
+        acc[i][j] = MF::template run<XFP4, 1>(opa[buf][i], opb[buf][j], acc[i][j], sca[i], scb[j]);
+    }
+  };
+  // Stage j opens when its copies have landed and no wave reads stage j - 1 any more;
+  // the S - 2 stages behind it (S - 1 behind the first) may still be in flight. The
+  // last step of stage j - 1 is multiplied after that. Each step is kept apart for the
+  // scheduler, which would otherwise hold a whole stage's operands in registers.
+  int cs = 0, it = 0;
+  // one MFMA, then the reads that one covers
+  auto interleave = [&]() {
+    constexpr int NR = FN + FM * (XFP4 ? 1 : 2), NM = FN * FM;
+#pragma unroll
+    for (int q = 0; q < NM; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, (NR + NM - 1) / NM + 1, 0);
+    }
+  };
+  auto steps = [&](auto refill, auto last) {
+    const int ns = cs + 1 == S ? 0 : cs + 1;
+#pragma unroll
+    for (int h = 0; h < NKK; ++h) {
+      const int buf = h & 1;
+      if (h * KI % 128 == 0) take_scales();
+      if (h + 1 < NKK) {
+        load_ops(smem + cs * STAGE, h + 1, buf ^ 1);
+#pragma unroll
+        for (int i = 0; i < FN; ++i) multiply_row(h, buf, i);
+        interleave();
+      } else {
+        if constexpr (!decltype(last)::value) {
+          if constexpr (decltype(refill)::value) wait_vm<(S - 2) * NI>();
+          else wait_stages<NI, S - 2>(nk - 2 - it);
+          __syncthreads();
+          load_ops(smem + ns * STAGE, 0, buf ^ 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        // the copies of the refill between the products
+#pragma unroll
+        for (int i = 0; i < (FN > NG ? FN : NG); ++i) {
+          if (i < FN) multiply_row(h, buf, i);
+          if constexpr (decltype(refill)::value) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (i < NG) issue_group(i, cs, ks0 + it + S);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    cs = ns;
+  };
+  if (nk > 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (s < nk)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) issue_group(g, s, ks0 + s);
+    wait_stages<NI, S - 1>(nk - 1);
+    __syncthreads();
+    load_ops(smem, 0, 0);
+    for (; it < nk - S; ++it) steps(std::true_type{}, std::false_type{});
+    for (; it < nk - 1; ++it) steps(std::false_type{}, std::false_type{});
+    steps(std::false_type{}, std::true_type{});
+  }
+
+  // Register 4 q + r of a fragment: weight row 8 q + 4 lg + r, token lr.
+  constexpr int NQ = T == 16 ? 1 : 4;
+  const int64_t n0 = (int64_t)tn * BN;
+  const int own = (int)(N - n0 < BN ? N - n0 : BN);
+  if (!p.part && !p.g.out_raw && (p.g.ldy & 7) == 0) {
+    // bf16 outputs through the idle ring, each wave its own part of it (only the last
+    // stage's reads have to be over), so that a lane stores 16 bytes of a token's row.
+    // Rows of 16 bytes more than the wave's channels spread the writes over the banks.
+    constexpr int LD = WTN * 2 + 16, FIT = S * STAGE / NW / (T * LD);
+    constexpr int JC = FIT < FM ? FIT : FM, CPR = WTN / 8;
+    static_assert(JC >= 1, "a token fragment per wave fits the ring");
+    uint8_t* so = smem + wid * (JC * T * LD);
+    uint16_t* Y = static_cast<uint16_t*>(p.g.Y) + n0 + wn * WTN;
+    const int64_t mw = (int64_t)tm * BM + wm * WTM;
+    const int ow = own - wn * WTN;
+    __syncthreads();
+#pragma unroll
+    for (int j0 = 0; j0 < FM; j0 += JC) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = j0; j < FM && j < j0 + JC; ++j)
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const acc_t& v = acc[i][j];
+            *reinterpret_cast<uint2*>(so + (T * (j - j0) + lr) * LD + (T * i + 8 * q + 4 * lg) * 2) =
+                make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
+          }
+#pragma unroll
+      for (int c = lane; c < JC * T * CPR; c += 64) {
+        const int ml = c / CPR, nl = 8 * (c % CPR);
+        const int64_t m = mw + T * j0 + ml;
+        if (m >= M || nl >= ow || T * j0 + ml >= WTM) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(so + ml * LD + nl * 2);
+        uint16_t* dst = Y + m * p.g.ldy + nl;
+        if (nl + 8 <= ow) {
+          *reinterpret_cast<uint4*>(dst) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int e = 0; nl + e < ow; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+    return;
+  }
+  const int64_t n4 = (N + 3) & ~(int64_t)3;
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int64_t m = (int64_t)tm * BM + wm * WTM + T * j + lr;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int nl = wn * WTN + T * i + 8 * q + 4 * lg;
+        if (m >= M || nl >= own) continue;
+        const float a[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (p.part)
+          *reinterpret_cast<float4*>(p.part + ((int64_t)split * M + m) * n4 + n0 + nl) =
+              make_float4(a[0], a[1], a[2], a[3]);
+        else
+          mx4_store4(p.g, m, n0 + nl, a);
+      }
+    }
+}
+
+// Sum of the K splits' partial sums ([splits][M][N up to a multiple of 4]), four
+// channels a thread, in the order of the splits.
+__global__ __launch_bounds__(256) void mx4_sum_kernel(const float* __restrict__ part, int splits,
+                                                      const Mx4Params p) {
+  const int64_t n4 = (p.N + 3) & ~(int64_t)3, q = n4 >> 2;
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= p.M * q) return;
+  const int64_t m = idx / q, n = 4 * (idx - m * q);
+  const float4* s = reinterpret_cast<const float4*>(part) + idx;
+  float a[4] = {};
+  for (int i = 0; i < splits; ++i) {
+    const float4 v = s[(int64_t)i * p.M * q];
+    a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
+  }
+  mx4_store4(p, m, n, a);
+}
+
+template <bool XFP4, int T, int BN, int BM, int WN, int WM, int S, int KS>
+hipError_t launch_tile(const Mx4Params& g, int splits, float* part, hipStream_t st) {
+  Mx4TileParams p;
+  p.g = g;
+  p.part = splits > 1 ? part : nullptr;
+  p.tiles_m = (int)((g.M + BM - 1) / BM);
+  p.tiles_n = (int)((g.N + BN - 1) / BN);
+  p.stages = (int)((g.K + KS - 1) / KS);
+  p.splits = splits;
+  const int64_t blocks = (int64_t)p.tiles_m * p.tiles_n * splits;
+  hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS>), dim3((unsigned)blocks),
+                     dim3(64 * WN * WM), 0, st, p);
+  if (splits > 1) {
+    const int64_t total = g.M * ((g.N + 3) >> 2);
+    hipLaunchKernelGGL(mx4_sum_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, part, splits, g);
+  }
+  return hipGetLastError();
+}
+
+// X: bf16 tokens to quantize in the kernel (stride ldx), or NULL for codes in p.
+template <bool XFP4, bool FUSED, int NW, int KW>
+hipError_t launch_decode(const Mx4Params& p, const uint16_t* X, int64_t ldx, hipStream_t st) {
+  constexpr int rows = 16 * (NW / KW);
+  const size_t lds = FUSED ? (size_t)(XFP4 ? p.M * p.K / 2 : p.M * p.K) + p.M * p.K / 32 : 0;
+  hipLaunchKernelGGL((mx4_decode_kernel<XFP4, FUSED, NW, KW, 4>), dim3((unsigned)((p.N + rows - 1) / rows)),
+                     dim3(64 * NW), lds, st, p, X, ldx);
+  return hipGetLastError();
+}
+
+// Tile configurations and what they cost: us per tile besides its stages, and per stage
+// alone on a CU / with a second block there (measured, one full round of 256 blocks at
+// K = 1792 .. 7168).
+struct Mx4Config {
+  int BN, BM, KS, per_cu;
+  float base, alone, shared;
+  hipError_t (*run)(const Mx4Params&, int, float*, hipStream_t);
+};
+constexpr Mx4Config kFp4Configs[] = {
+    {256, 256, 256, 1, 8.0f, 2.00f, 0.0f, launch_tile<true, 32, 256, 256, 2, 4, 2, 256>},
+    {160, 256, 256, 1, 5.5f, 1.50f, 0.0f, launch_tile<true, 16, 160, 256, 2, 4, 2, 256>},
+    {160, 128, 256, 1, 5.0f, 0.87f, 0.0f, launch_tile<true, 16, 160, 128, 2, 4, 3, 256>},
+    {128, 128, 256, 1, 5.0f, 0.65f, 0.0f, launch_tile<true, 32, 128, 128, 2, 4, 4, 256>},
+    {160, 64, 256, 1, 4.5f, 0.65f, 0.0f, launch_tile<true, 16, 160, 64, 2, 4, 4, 256>},
+    {128, 64, 256, 1, 4.5f, 0.56f, 0.0f, launch_tile<true, 16, 128, 64, 4, 2, 4, 256>},
+    {64, 64, 256, 2, 4.4f, 0.31f, 0.44f, launch_tile<true, 16, 64, 64, 2, 2, 4, 256>},
+    {64, 32, 256, 2, 3.5f, 0.30f, 0.35f, launch_tile<true, 16, 64, 32, 4, 1, 4, 256>},
+};
+constexpr Mx4Config kFp8Configs[] = {
+    {256, 256, 128, 1, 8.0f, 1.42f, 0.0f, launch_tile<false, 32, 256, 256, 2, 4, 3, 128>},
+    {160, 256, 128, 1, 5.0f, 1.02f, 0.0f, launch_tile<false, 32, 160, 256, 1, 8, 3, 128>},
+    {160, 128, 256, 1, 4.0f, 1.40f, 0.0f, launch_tile<false, 16, 160, 128, 2, 4, 2, 256>},
+    {128, 128, 128, 1, 4.8f, 0.50f, 0.0f, launch_tile<false, 32, 128, 128, 2, 4, 4, 128>},
+    {160, 64, 256, 1, 4.8f, 0.68f, 0.0f, launch_tile<false, 16, 160, 64, 2, 4, 3, 256>},
+    {64, 64, 256, 1, 4.8f, 0.38f, 0.0f, launch_tile<false, 16, 64, 64, 2, 2, 3, 256>},
+    {64, 32, 256, 2, 3.8f, 0.31f, 0.42f, launch_tile<false, 16, 64, 32, 4, 1, 4, 256>},
+};
+constexpr int kCUs = 256;
+
+struct Mx4Plan {
+  const Mx4Config* c;  // NULL: the decode kernel on token codes
+  int splits;
+};
+
+// Up to 16 tokens and matrices up to 8192 x 8192 take the decode kernel (7B O
+// projection, 3.8 - 5.0 us against 6.3 - 7.1 on the smallest tiles; beyond, the tiles'
+// deeper copy rings win: 15 against 20 - 32 us on the stacked gate and up). Else the
+// configuration and the number of K splits whose rounds of blocks over the CUs cost
+// least by the table; a split adds a launch and one write and read of its partial sums.
+Mx4Plan make_mx4_plan(int64_t M, int64_t N, int64_t K, bool fp4) {
+  if (M <= 16 && N <= 8192 && K <= 8192) return {nullptr, 1};
+  const Mx4Config* first = fp4 ? kFp4Configs : kFp8Configs;
+  const int n = fp4 ? (int)(sizeof(kFp4Configs) / sizeof(Mx4Config)) : (int)(sizeof(kFp8Configs) / sizeof(Mx4Config));
+  Mx4Plan best{first, 1};
+  float least = 3.0e38f;
+  for (int i = 0; i < n; ++i) {
+    const Mx4Config& c = first[i];
+    const int64_t tiles = ((M + c.BM - 1) / c.BM) * ((N + c.BN - 1) / c.BN);
+    const int64_t stages = (K + c.KS - 1) / c.KS;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (s > 1 && (stages < 4 * s || tiles * s > 2 * kCUs)) break;
+      const int64_t blocks = tiles * s, round = (int64_t)kCUs * c.per_cu;
+      const float step = blocks > kCUs && c.per_cu > 1 ? c.shared : c.alone;
+      float t = (float)((blocks + round - 1) / round) * (c.base + step * (float)((stages + s - 1) / s));
+      if (s > 1) t += 3.5f + (float)s * (float)M * (float)N * 1.0e-6f;
+      if (t < least) {
+        least = t;
+        best = {&c, s};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -200,29 +787,55 @@ hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int64_t R
 
 hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq,
                            const uint8_t* sw, int64_t M, int64_t N, int64_t K, int out_raw, void* Y,
-                           int64_t ldy, void* /*ws*/, hipStream_t st) {
+                           int64_t ldy, void* ws, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
   const Mx4Params p{static_cast<const uint8_t*>(Xq), sx, static_cast<const uint8_t*>(Wq), sw,
                     M, N, K, Y, ldy, out_raw};
-  const dim3 g((unsigned)(((N + 15) / 16) * ((M + 15) / 16))), b(512);
-  if (xfmt == kActMxFp4) hipLaunchKernelGGL(mx4_stream_kernel<true>, g, b, 0, st, p);
-  else hipLaunchKernelGGL(mx4_stream_kernel<false>, g, b, 0, st, p);
-  return hipGetLastError();
+  const bool fp4 = xfmt == kActMxFp4;
+  const Mx4Plan plan = make_mx4_plan(M, N, K, fp4);
+  if (plan.c) return plan.c->run(p, plan.splits, static_cast<float*>(ws), st);
+  return fp4 ? launch_decode<true, false, 8, 8>(p, nullptr, 0, st)
+             : launch_decode<false, false, 8, 8>(p, nullptr, 0, st);
 }
 
-size_t mx4_gemm_ws_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+size_t mx4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int xfmt) {
+  const Mx4Plan plan = make_mx4_plan(M, N, K, xfmt == kActMxFp4);
+  return plan.splits > 1 ? (size_t)plan.splits * (size_t)M * (size_t)((N + 3) & ~(int64_t)3) * 4 : 0;
+}
 
-// The workspace holds the token codes, then their scales (each 256-byte aligned).
+// One launch where the blocks' own quantization of the tokens costs less than a launch
+// for it (2.6 us): up to 16384 values (four tokens of the 7B hidden size: 6.8 against
+// 7.6 us on QKV; eight: 9.4 against 7.9), and for one or two tokens up to what fits the
+// LDS (7B down projection, one token: 10.5 against 13.7 us). Long rows with few blocks
+// split K over 16 waves; many rows (the stacked gate and up) take 32 rows a block, half
+// of K a wave (14.2 us; 20.4 with 16 rows over eight waves).
+bool mx4_one_launch(int64_t M, int64_t K) { return M * K <= 16384 || (M <= 2 && M * K <= 40960); }
+
+template <bool XFP4>
+hipError_t launch_fused(const Mx4Params& p, const uint16_t* X, int64_t ldx, hipStream_t st) {
+  if (p.N > 16 * 1024) return launch_decode<XFP4, true, 4, 2>(p, X, ldx, st);
+  if (p.K >= 8192) return launch_decode<XFP4, true, 16, 16>(p, X, ldx, st);
+  return launch_decode<XFP4, true, 8, 8>(p, X, ldx, st);
+}
+
+// The workspace holds the product's partial sums, the token codes, then their scales
+// (each 256-byte aligned).
 hipError_t launch_mx4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const uint8_t* sw,
                              int64_t M, int64_t N, int64_t K, void* Y, int64_t ldy, void* ws,
                              hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
-  const size_t cb = (size_t)(xfmt == kActMxFp4 ? M * (K >> 1) : M * K);
-  uint8_t* xq = static_cast<uint8_t*>(ws);
-  uint8_t* sx = xq + ((cb + 255) & ~(size_t)255);
+  const bool fp4 = xfmt == kActMxFp4;
+  if (K > 0 && M <= 16 && mx4_one_launch(M, K)) {
+    const Mx4Params p{nullptr, nullptr, static_cast<const uint8_t*>(Wq), sw, M, N, K, Y, ldy, 0};
+    const uint16_t* x = static_cast<const uint16_t*>(X);
+    return fp4 ? launch_fused<true>(p, x, ldx, st) : launch_fused<false>(p, x, ldx, st);
+  }
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  uint8_t* xq = static_cast<uint8_t*>(ws) + up(mx4_gemm_ws_bytes(M, N, K, xfmt));
+  uint8_t* sx = xq + up((size_t)(fp4 ? M * (K >> 1) : M * K));
   const hipError_t e = launch_mx4_quant(X, M, K, ldx, 1, xfmt, xq, sx, st);
   if (e != hipSuccess) return e;
-  return launch_mx4_gemm(xq, sx, xfmt, Wq, sw, M, N, K, 0, Y, ldy, nullptr, st);
+  return launch_mx4_gemm(xq, sx, xfmt, Wq, sw, M, N, K, 0, Y, ldy, ws, st);
 }
 
 }  // namespace qr

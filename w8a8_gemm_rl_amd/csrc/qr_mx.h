@@ -122,6 +122,13 @@ __device__ __forceinline__ uint32_t f32_to_bf16_any(float f) {
   return (u & 0x7fffffffu) > 0x7f800000u ? ((u >> 16) | 0x40u) : f32_to_bf16_rne(f);
 }
 
+// Two fp32 -> packed bf16 (a low), v_cvt_pk_bf16_f32: nearest even, NaN stays NaN.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 h2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), h2));
+}
+
 __device__ __forceinline__ void bf16x8(const uint4 v, float* h) {
   h[0] = bf16_lo(v.x); h[1] = bf16_hi(v.x); h[2] = bf16_lo(v.y); h[3] = bf16_hi(v.y);
   h[4] = bf16_lo(v.z); h[5] = bf16_hi(v.z); h[6] = bf16_lo(v.w); h[7] = bf16_hi(v.w);
