@@ -365,9 +365,11 @@ int qr_mxfp4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq, c
  *   qr_mxfp4_gemm with out = QR_OUT_BF16.
  *
  *   X        [M, ldx] bf16, rows on 16-byte boundaries (read).
- *   workspace  qr_workspace_size("qr_mxfp4_linear", M, N, K, xfmt) bytes (never 0
- *            when M, N, K > 0), 256-byte aligned: the product's, then codes and
- *            scales.
+ *   workspace  qr_workspace_size("qr_mxfp4_linear", M, N, K, xfmt) bytes, 256-byte
+ *            aligned: the product's, then codes and scales. NULL when that is 0:
+ *            a few tokens (M <= 16 with M K <= 16384, or M <= 2 with M K <= 40960)
+ *            run as one launch whose blocks quantize X themselves; the waves'
+ *            partial sums are added in a fixed order.
  */
 int qr_mxfp4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const uint8_t* sw, int64_t M,
                     int64_t N, int64_t K, void* Y, int64_t ldy, void* workspace, size_t ws_bytes,

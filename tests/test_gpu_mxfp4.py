@@ -310,6 +310,20 @@ def test_block_norm_row_lengths(M, K, fmt):
         _check_norm(_norm_inputs(M, K, M + K, True, "token", True), fmt, "layer", 0.75)
 
 
+@pytest.mark.parametrize("shift", [0.0, 3.0, 30.0, 3000.0])
+def test_block_norm_layer_kind_with_a_large_mean(shift):
+    """LayerNorm rows whose mean is up to thousands of deviations: the variance must not lose to
+    cancellation (both routes to it, on the block's output and on the residual stream)."""
+    M, K = 7, 1056
+    g = np.random.default_rng(4)
+    d = _norm_inputs(M, K, 1, True, "none", True)
+    d["Y"] = F.f32_to_bf16_bits((shift + g.standard_normal((M, K))).astype(np.float32))
+    d["H"] = F.f32_to_bf16_bits((shift + g.standard_normal((M, K))).astype(np.float32))
+    _check_norm(d, "int8", "layer", 1.0)
+    d["post_gamma"] = d["post_beta"] = None
+    _check_norm(d, "mxfp8", "layer", 1.0)
+
+
 def test_block_norm_of_k16_rows():
     """Rows of the per-token formats need only 16-element steps."""
     for fmt in ("int8", "fp8", "bf16"):
@@ -506,7 +520,7 @@ def test_binding_refusals_on_device_tensors():
     with pytest.raises(B.QRError):
         B.mxfp4_quantize(torch.zeros((4, 48), device=DEV))
     with pytest.raises(B.QRError):
-        B.mxfp4_linear(x, w, sw, ws=torch.zeros(16, dtype=torch.uint8, device=DEV))
+        B.mxfp4_linear(x.repeat(50, 1), w, sw, ws=torch.zeros(16, dtype=torch.uint8, device=DEV))
     y = torch.empty(4 * 16 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(4, 16)
     with pytest.raises(B.QRError):
         B.mxfp4_linear(x, w, sw, Y=y)

@@ -149,7 +149,10 @@ def test_product_refusals(L):
     li = lambda **kw: _call(L.qr_mxfp4_linear, spec, **kw)  # noqa: E731
     assert li(xfmt=1) == -1 and li(ldx=255) == -1 and li(X=None) == -1 and li(Y=None) == -1
     assert li(ldx=260) == -2 and li(X=ctypes.c_void_p(8)) == -2 and li(K=128 + 64) == -2
-    assert li(ws=None) == -3 and li(wsb=16) == -3 and li(ws=ctypes.c_void_p((1 << 20) + 64)) == -3
+    big = dict(M=100, K=1024, ldx=1024)
+    assert li(ws=None, **big) == -3 and li(wsb=16, **big) == -3
+    assert li(ws=ctypes.c_void_p((1 << 20) + 64), **big) == -3
+    assert li(M=1 << 20, N=1 << 18, ldy=1 << 18, K=128) == -2  # M N = 2^38
 
 
 def test_workspace_sizes(L):
@@ -163,6 +166,9 @@ def test_workspace_sizes(L):
     for x, per in ((MX8, 1.0), (MX4, 0.5)):
         need = ws(b"qr_mxfp4_linear", 33, 512, 1024, x) - ws(b"qr_mxfp4_gemm", 33, 512, 1024, x)
         assert need >= 33 * 1024 * per + 33 * 32
+        # a few tokens are quantized inside the kernel
+        assert ws(b"qr_mxfp4_linear", 1, 512, 18944, x) == 0 and ws(b"qr_mxfp4_linear", 16, 512, 1024, x) == 0
+        assert ws(b"qr_mxfp4_linear", 1, 512, 41088, x) > 0 and ws(b"qr_mxfp4_linear", 17, 512, 128, x) > 0
 
 
 def test_block_norm_refusals(L):

@@ -520,89 +520,86 @@ def linear_fused_noalloc(X, act_mult, Wq, scale_w, qt, Y=None):
 
 
 # ----------------------------------------------------------------------------
-# MXFP4 operators and block norms. Decode calls are a few microseconds, so the
-# marshalling here is kept short: no device switch where the tensors' device is
-# current, scratch from torch's allocator (stream-ordered; a graph's own pool under
-# capture, so captured graphs never share it).
+# MXFP4 operators and block norms. Decode calls are a few microseconds on the GPU, so
+# the marshalling here is kept short (one-token mxfp4_linear: 10.8 us of host time with
+# this module's general helpers, 6.6 with these): the stream as a plain handle, no
+# device switch where the tensors' device is current, scratch from torch's allocator
+# (stream-ordered; a graph's own pool under capture, so captured graphs never share it).
 # ----------------------------------------------------------------------------
 
-def _call(fn, dev, *args):
-    """Call library function `fn` on dev's current stream, dev being current."""
+def _call(fn, idx, *args):
+    """Call library function `fn` on the current stream of device `idx`, made current."""
     f = getattr(_lib or lib(), fn)
-    idx = dev.index
     if idx == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = f(*args, torch._C._cuda_getCurrentRawStream(idx))
     else:
         with torch.cuda.device(idx):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(idx))
     if st != 0:
         _check(fn, st)
 
 
 def _one_device(dev, *ts):
-    """Every given tensor lives on HIP device `dev`."""
+    """Every given tensor lives on HIP device `dev`; returns its index."""
     if dev.type != "cuda":
         raise ValueError("tensors must live on a HIP device")
     for t in ts:
         if t is not None and t.device != dev:
             raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
+    return dev.index
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(t, shape, dtype, dev, name):
-    """A new dense output, or the caller's after a check of its shape and type."""
+def _out(t, like, shape, dtype, name):
+    """A new dense output beside `like`, or the caller's after a check of its shape and type."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if t.shape != torch.Size(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+        return like.new_empty(shape, dtype=dtype)
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
     return t
 
 
-def _panels(rows, K):
-    return ((K + 127) // 128, rows, 4)
-
-
-def _mx_shape(codes, name):
-    """(rows, K, format) of block-wise codes: uint8 holds two E2M1 codes a byte."""
+def _mx_codes(codes, scales, name):
+    """(rows, K, format) of block-wise codes and their scale panels: uint8 holds two E2M1
+    codes a byte."""
     if codes.dim() != 2 or not codes.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-D tensor of codes")
+    R, K = codes.shape
     if codes.dtype == torch.uint8:
-        return codes.shape[0], 2 * codes.shape[1], 3
-    if codes.dtype == torch.float8_e4m3fn:
-        return codes.shape[0], codes.shape[1], 2
-    raise ValueError(f"{name} must be uint8 (MXFP4) or float8_e4m3fn (block-wise FP8) codes")
+        K, fmt = 2 * K, 3
+    elif codes.dtype == torch.float8_e4m3fn:
+        fmt = 2
+    else:
+        raise ValueError(f"{name} must be uint8 (MXFP4) or float8_e4m3fn (block-wise FP8) codes")
+    if scales.dtype != torch.uint8 or scales.shape != ((K + 127) // 128, R, 4) or not scales.is_contiguous():
+        raise ValueError(f"the scales of {name} must be contiguous uint8 panels {((K + 127) // 128, R, 4)}")
+    return R, K, fmt
 
 
-def _mx_scales(s, rows, K, name):
-    if s.dtype != torch.uint8 or s.shape != _panels(rows, K) or not s.is_contiguous():
-        raise ValueError(f"{name} must be contiguous uint8 scale panels of shape {_panels(rows, K)}")
-
-
-def _mx_out(M, K, fmt, codes, scales, dev):
+def _mx_out(like, M, K, fmt, codes, scales):
     """Outputs of a producer with block-wise codes."""
     if fmt == "mxfp4":
-        codes = _out(codes, (M, K // 2), torch.uint8, dev, "codes")
+        codes = _out(codes, like, (M, K // 2), torch.uint8, "codes")
     else:
-        codes = _out(codes, (M, K), torch.float8_e4m3fn, dev, "codes")
-    return codes, _out(scales, _panels(M, K), torch.uint8, dev, "scales")
+        codes = _out(codes, like, (M, K), torch.float8_e4m3fn, "codes")
+    return codes, _out(scales, like, ((K + 127) // 128, M, 4), torch.uint8, "scales")
 
 
 def mxfp4_quantize(A, codes=None, scales=None):
     """MXFP4 of fp32 or bf16 rows A [R, K] -> (codes uint8 [R, K/2], two E2M1 codes a
     byte, E8M0 scales uint8 [ceil(K/128), R, 4])."""
-    dev = A.device
-    _one_device(dev, codes, scales)
-    if A.dtype not in (torch.float32, torch.bfloat16):
+    idx = _one_device(A.device, codes, scales)
+    if A.dtype != torch.float32 and A.dtype != torch.bfloat16:
         raise ValueError("A must be float32 or bfloat16")
     lda = _rows(A, "A")
     R, K = A.shape
     if K % 32:
         raise QRError("qr_mxfp4_quantize", -2, f"K={K} is not a multiple of 32")
-    codes, scales = _mx_out(R, K, "mxfp4", codes, scales, dev)
-    _call("qr_mxfp4_quantize", dev, A.data_ptr(), R, K, lda, int(A.dtype == torch.bfloat16),
+    codes, scales = _mx_out(A, R, K, "mxfp4", codes, scales)
+    _call("qr_mxfp4_quantize", idx, A.data_ptr(), R, K, lda, int(A.dtype == torch.bfloat16),
           codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -610,32 +607,24 @@ def mxfp4_quantize(A, codes=None, scales=None):
 def mx_dequantize(codes, scales, out=None, dtype=torch.bfloat16):
     """The values of MXFP4 (uint8) or block-wise FP8 (float8_e4m3fn) codes, bf16 or fp32
     [R, K]; `out` may have any row stride."""
-    dev = codes.device
-    _one_device(dev, scales, out)
-    R, K, fmt = _mx_shape(codes, "codes")
-    _mx_scales(scales, R, K, "scales")
+    idx = _one_device(codes.device, scales, out)
+    R, K, fmt = _mx_codes(codes, scales, "codes")
     if out is None:
         if dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("dtype must be bfloat16 or float32")
-        out = torch.empty((R, K), dtype=dtype, device=dev)
+        out, ldo = codes.new_empty((R, K), dtype=dtype), K
     elif out.shape != (R, K) or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out must be a bfloat16 or float32 tensor of the codes' rows and K")
-    _call("qr_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), R, K, fmt, out.data_ptr(),
-          _rows(out, "out"), int(out.dtype == torch.bfloat16))
+    else:
+        ldo = _rows(out, "out")
+    _call("qr_mx_dequantize", idx, codes.data_ptr(), scales.data_ptr(), R, K, fmt, out.data_ptr(), ldo,
+          int(out.dtype == torch.bfloat16))
     return out
 
 
-def _mx4_weights(Wq, sw):
-    if Wq.dtype != torch.uint8:
-        raise ValueError("Wq must be uint8 MXFP4 codes")
-    N, K, _ = _mx_shape(Wq, "Wq")
-    _mx_scales(sw, N, K, "sw")
-    return N, K
-
-
-def _mx4_out(Y, M, N, dtype, dev):
+def _mx4_out(Y, like, M, N, dtype):
     if Y is None:
-        return torch.empty((M, N), dtype=dtype, device=dev), N
+        return like.new_empty((M, N), dtype=dtype), N
     if Y.shape != (M, N) or Y.dtype != dtype:
         raise ValueError(f"Y must be {dtype} [{M}, {N}]")
     return Y, max(_rows(Y, "Y"), N)
@@ -644,8 +633,12 @@ def _mx4_out(Y, M, N, dtype, dev):
 _mx4_ws = {}
 
 
-def _mx4_workspace(fn, M, N, K, xfmt, dev, ws):
-    """(workspace tensor or None, bytes) for a call; the sizes are kept per shape."""
+def _mx4_workspace(fn, M, N, K, xfmt, like, ws):
+    """(workspace address or None, bytes, its tensor) of a call; sizes are kept per shape."""
+    if ws is not None:
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+        return ws.data_ptr(), ws.numel() * ws.element_size(), ws
     need = _mx4_ws.get((fn, M, N, K, xfmt))
     if need is None:
         need = lib().qr_workspace_size(fn.encode(), M, N, K, xfmt)
@@ -654,51 +647,50 @@ def _mx4_workspace(fn, M, N, K, xfmt, dev, ws):
         if len(_mx4_ws) > 4096:
             _mx4_ws.clear()
         _mx4_ws[(fn, M, N, K, xfmt)] = need
-    if ws is not None:
-        if not ws.is_contiguous():
-            raise ValueError("ws must be contiguous")
-        return ws, ws.numel() * ws.element_size()
-    return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
+    if need == 0:
+        return None, 0, None
+    ws = like.new_empty(need, dtype=torch.uint8)
+    return ws.data_ptr(), need, ws
 
 
 def mxfp4_gemm(Xq, sx, Wq, sw, out="bf16", Y=None, ws=None):
     """Product of quantized tokens (uint8 MXFP4 or float8_e4m3fn block-wise codes [M, K] with
     their scale panels) with MXFP4 weights Wq [N, K/2]: bf16 Y [M, N] or the fp32 accumulators."""
-    dev = Xq.device
-    _one_device(dev, sx, Wq, sw, Y, ws)
-    M, K, xfmt = _mx_shape(Xq, "Xq")
-    _mx_scales(sx, M, K, "sx")
-    N, Kw = _mx4_weights(Wq, sw)
-    if Kw != K:
-        raise ValueError("Xq and Wq disagree on K")
+    idx = _one_device(Xq.device, sx, Wq, sw, Y, ws)
+    M, K, xfmt = _mx_codes(Xq, sx, "Xq")
+    N, Kw, wfmt = _mx_codes(Wq, sw, "Wq")
+    if wfmt != 3 or Kw != K:
+        raise ValueError("Wq must be uint8 MXFP4 codes of Xq's K")
     if out not in OUT:
         raise ValueError(f"out must be one of {list(OUT)}")
-    Y, ldy = _mx4_out(Y, M, N, torch.bfloat16 if out == "bf16" else torch.float32, dev)
-    ws, wsb = _mx4_workspace("qr_mxfp4_gemm", M, N, K, xfmt, dev, ws)
-    _call("qr_mxfp4_gemm", dev, Xq.data_ptr(), sx.data_ptr(), xfmt, Wq.data_ptr(), sw.data_ptr(), M, N, K,
-          OUT[out], Y.data_ptr(), ldy, _addr(ws), wsb)
+    Y, ldy = _mx4_out(Y, Xq, M, N, torch.bfloat16 if out == "bf16" else torch.float32)
+    wsp, wsb, ws = _mx4_workspace("qr_mxfp4_gemm", M, N, K, xfmt, Xq, ws)
+    _call("qr_mxfp4_gemm", idx, Xq.data_ptr(), sx.data_ptr(), xfmt, Wq.data_ptr(), sw.data_ptr(), M, N, K,
+          OUT[out], Y.data_ptr(), ldy, wsp, wsb)
     return Y
 
 
 def mxfp4_linear(X, Wq, sw, x="fp4", Y=None, ws=None):
     """One rollout linear with MXFP4 weights: bf16 X [M, K] (any row stride) quantized block-wise
     to `x` ("fp4" or "fp8"), product, bf16 Y [M, N]."""
-    dev = X.device
-    _one_device(dev, Wq, sw, Y, ws)
+    idx = _one_device(X.device, Wq, sw, Y, ws)
     if X.dtype != torch.bfloat16:
         raise ValueError("X must be bfloat16")
-    if x not in ("fp4", "fp8"):
+    if x == "fp4":
+        xfmt = 3
+    elif x == "fp8":
+        xfmt = 2
+    else:
         raise ValueError(f"x must be 'fp4' or 'fp8', got {x!r}")
-    xfmt = 3 if x == "fp4" else 2
     ldx = _rows(X, "X")
     M, K = X.shape
-    N, Kw = _mx4_weights(Wq, sw)
-    if Kw != K:
-        raise ValueError("X and Wq disagree on K")
-    Y, ldy = _mx4_out(Y, M, N, torch.bfloat16, dev)
-    ws, wsb = _mx4_workspace("qr_mxfp4_linear", M, N, K, xfmt, dev, ws)
-    _call("qr_mxfp4_linear", dev, X.data_ptr(), ldx, xfmt, Wq.data_ptr(), sw.data_ptr(), M, N, K,
-          Y.data_ptr(), ldy, _addr(ws), wsb)
+    N, Kw, wfmt = _mx_codes(Wq, sw, "Wq")
+    if wfmt != 3 or Kw != K:
+        raise ValueError("Wq must be uint8 MXFP4 codes of X's K")
+    Y, ldy = _mx4_out(Y, X, M, N, torch.bfloat16)
+    wsp, wsb, ws = _mx4_workspace("qr_mxfp4_linear", M, N, K, xfmt, X, ws)
+    _call("qr_mxfp4_linear", idx, X.data_ptr(), ldx, xfmt, Wq.data_ptr(), sw.data_ptr(), M, N, K,
+          Y.data_ptr(), ldy, wsp, wsb)
     return Y
 
 
@@ -710,54 +702,50 @@ def block_norm_quant(Y, H, gamma, fmt, post_gamma=None, gate=None, res_scale=1.0
 
     Y, H bf16 [M, K]; gamma, beta, post_gamma, post_beta fp32 [K]; gate None, fp32 [K] or bf16
     [M, K]. Hout may be H or Y (updated in place)."""
-    dev = Y.device
-    _one_device(dev, H, gamma, post_gamma, gate, beta, post_beta, Hout, codes, scales)
-    if Y.dtype != torch.bfloat16 or H.dtype != torch.bfloat16 or Y.shape != H.shape:
+    idx = _one_device(Y.device, H, gamma, post_gamma, gate, beta, post_beta, Hout, codes, scales)
+    shape = Y.shape
+    if Y.dtype != torch.bfloat16 or H.dtype != torch.bfloat16 or H.shape != shape:
         raise ValueError("Y and H must be bfloat16 of one shape")
     if fmt not in ACT:
         raise ValueError(f"fmt must be one of {list(ACT)}, got {fmt!r}")
     if kind not in NORM:
         raise ValueError(f"kind must be one of {list(NORM)}")
     ldy, ldh = _rows(Y, "Y"), _rows(H, "H")
-    M, K = Y.shape
-    for name, t in (("gamma", gamma), ("post_gamma", post_gamma), ("beta", beta), ("post_beta", post_beta)):
-        if t is None:
-            continue
-        if t.dtype != torch.float32 or t.numel() != K or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor of K entries")
+    M, K = shape
+    for t in (gamma, post_gamma, beta, post_beta):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != K or not t.is_contiguous()):
+            raise ValueError("gains and biases must be contiguous float32 tensors of K entries")
     ldgate = 0
     if gate is not None:
-        if gate.dtype == torch.bfloat16 and gate.shape == Y.shape:
+        if gate.dtype == torch.bfloat16 and gate.shape == shape:
             ldgate = _rows(gate, "gate")
         elif gate.dtype != torch.float32 or gate.shape != (K,) or not gate.is_contiguous():
             raise ValueError("gate must be float32 [K] or bfloat16 [M, K]")
     if Hout is None:
-        Hout, ldo = torch.empty((M, K), dtype=torch.bfloat16, device=dev), K
-    elif Hout.shape != Y.shape or Hout.dtype != torch.bfloat16:
+        Hout, ldo = Y.new_empty(shape), K
+    elif Hout.shape != shape or Hout.dtype != torch.bfloat16:
         raise ValueError("Hout must be bfloat16 of Y's shape")
     else:
         ldo = _rows(Hout, "Hout")
     if fmt == "bf16":
-        codes = _out(codes, (M, K), torch.bfloat16, dev, "codes")
-        scales = None
-    elif fmt in ("int8", "fp8"):
-        codes = _out(codes, (M, K), code_dtype(fmt), dev, "codes")
-        scales = _out(scales, (M,), torch.float32, dev, "scales")
+        codes, scales = _out(codes, Y, (M, K), torch.bfloat16, "codes"), None
+    elif fmt == "int8" or fmt == "fp8":
+        codes = _out(codes, Y, (M, K), code_dtype(fmt), "codes")
+        scales = _out(scales, Y, (M,), torch.float32, "scales")
     else:
         if K % 32:
             raise QRError("qr_block_norm_quant", -2, f"K={K} is not a multiple of 32")
-        codes, scales = _mx_out(M, K, fmt, codes, scales, dev)
-    _call("qr_block_norm_quant", dev, Y.data_ptr(), ldy, H.data_ptr(), ldh, M, K, NORM[kind],
-          _addr(post_gamma), _addr(post_beta), _addr(gate), ldgate, float(res_scale), gamma.data_ptr(),
-          _addr(beta), float(eps), ACT[fmt], Hout.data_ptr(), ldo, codes.data_ptr(), _addr(scales))
+        codes, scales = _mx_out(Y, M, K, fmt, codes, scales)
+    _call("qr_block_norm_quant", idx, Y.data_ptr(), ldy, H.data_ptr(), ldh, M, K, NORM[kind],
+          _addr(post_gamma), _addr(post_beta), _addr(gate), ldgate, res_scale, gamma.data_ptr(),
+          _addr(beta), eps, ACT[fmt], Hout.data_ptr(), ldo, codes.data_ptr(), _addr(scales))
     return Hout, codes, scales
 
 
 def silu_mul_mx(G, U, fmt, codes=None, scales=None):
     """SiLU(G) * U for bf16 [M, N] views (rows contiguous, any row strides), quantized block-wise to
     fmt ("mxfp4" or "mxfp8") -> (codes, scales)."""
-    dev = G.device
-    _one_device(dev, U, codes, scales)
+    idx = _one_device(G.device, U, codes, scales)
     if G.dtype != torch.bfloat16 or U.dtype != torch.bfloat16 or G.shape != U.shape:
         raise ValueError("G and U must be bfloat16 of one shape")
     if fmt not in ("mxfp4", "mxfp8"):
@@ -766,8 +754,8 @@ def silu_mul_mx(G, U, fmt, codes=None, scales=None):
     M, N = G.shape
     if N % 32:
         raise QRError("qr_silu_mul_mx", -2, f"N={N} is not a multiple of 32")
-    codes, scales = _mx_out(M, N, fmt, codes, scales, dev)
-    _call("qr_silu_mul_mx", dev, G.data_ptr(), U.data_ptr(), M, N, ldg, ldu, ACT[fmt], codes.data_ptr(),
+    codes, scales = _mx_out(G, M, N, fmt, codes, scales)
+    _call("qr_silu_mul_mx", idx, G.data_ptr(), U.data_ptr(), M, N, ldg, ldu, ACT[fmt], codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
 

@@ -18,37 +18,48 @@
 namespace qr {
 namespace {
 
-constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
-
-template <int TPR>
-__device__ __forceinline__ double row_sum(double v, double* red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  if constexpr (TPR > 64) {
-    __syncthreads();  // red may still be read from the last reduction
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = red[0];
-#pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) s += red[w];
-    v = s;
-  }
+// Sum / maximum over a wave, every lane getting it: within 16 lanes by lane permutes of
+// the vector ALU, then across the four groups through LDS permutes.
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v += dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v += dpp<0x141>(v);  // row_half_mirror
+  v += dpp<0x140>(v);  // row_mirror
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
   return v;
 }
 
-template <int TPR>
-__device__ __forceinline__ float row_max(float v, double* red) {
-  v = wave_max(v);
-  if constexpr (TPR > 64) {
-    float* redf = reinterpret_cast<float*>(red);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) redf[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float m = redf[0];
+// Sums / maximum over the block, whose waves leave theirs in `red` (not used by another
+// reduction of the kernel, so one barrier each).
+template <int N>
+__device__ __forceinline__ void row_sum(double (&v)[N], double (*red)[16]) {
 #pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) m = fmaxf(m, redf[w]);
-    v = m;
+  for (int n = 0; n < N; ++n) {
+    v[n] = wave_sum(v[n]);
+    if ((threadIdx.x & 63) == 0) red[n][threadIdx.x >> 6] = v[n];
   }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    v[n] = red[n][0];
+    for (uint32_t w = 1; w < blockDim.x >> 6; ++w) v[n] += red[n][w];
+  }
+}
+
+__device__ __forceinline__ float row_max(float v, float* red) {
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = red[0];
+  for (uint32_t w = 1; w < blockDim.x >> 6; ++w) v = fmaxf(v, red[w]);
   return v;
 }
 
@@ -60,42 +71,106 @@ __device__ __forceinline__ void load8(const float* p, int64_t c, float* v) {
 }
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
-  uint32_t h[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = f32_to_bf16_any(v[e]);
-  return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+  return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
 }
 
-// Norm of the row held as v[i][8] (chunk lt + i TPR of thread lt) in place; `live(i)`
-// says which chunks exist.
-template <int KIND, int TPR, int MAXC, typename Live>
-__device__ __forceinline__ void norm_row(float (&v)[MAXC][8], const Live& live, int lt, int64_t K,
-                                         const float* gamma, const float* beta, float eps, double* red) {
+// Eight INT8 codes rint(fl32(v / t)), |v| <= 127 t, inv = fl32(1 / t) finite: v inv is
+// within 2^-15 of fl32(v / t) and rounds to the same integer unless it lies that close to
+// a half; only then (one value in 8000) is the division done. Adding 1.5 2^23 rounds to
+// an integer (ties to even) and leaves it in the low byte.
+__device__ __forceinline__ uint2 int8_codes8(const float* v, float t, float inv) {
+  constexpr float kMagic = 12582912.0f;
+  uint32_t b[8];
+  float far = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = v[e] * inv, m = q + kMagic;
+    far = fmaxf(far, fabsf(q - (m - kMagic)));
+    b[e] = __float_as_uint(m);
+  }
+  if (far > 0.5f - 0x1p-14f)
+    return make_uint2(quant_codes4<kQInt8>(v[0], v[1], v[2], v[3], t),
+                      quant_codes4<kQInt8>(v[4], v[5], v[6], v[7], t));
+  auto pack = [](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    // bytes: 4 .. 7 of the first operand, 0 .. 3 of the second
+    const uint32_t lo = __builtin_amdgcn_perm(a1, a0, 0x0c0c0400u), hi = __builtin_amdgcn_perm(a3, a2, 0x04000c0cu);
+    return lo | hi;
+  };
+  return make_uint2(pack(b[0], b[1], b[2], b[3]), pack(b[4], b[5], b[6], b[7]));
+}
+
+// 1 / sqrt(x) in float64 to 2^-48: the instruction's estimate (2^-24) and a Newton step
+// each way of a last bit's doubt; 0 and infinity as the estimate gives them.
+__device__ __forceinline__ double rsqrt64(double x) {
+  const double y0 = __builtin_amdgcn_rsq(x);
+  double y = y0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double h = 0.5 * y;
+    y = fma(h, fma(-x * y, y, 1.0), y);
+  }
+  return x > 0.0 && x < __builtin_inf() ? y : y0;
+}
+
+// Norm of the row held as v[i][8] (chunk c(i) = lt + i tpr of thread lt) in place;
+// `live(i)` says which chunks exist. inv_k = 1 / K; red: three arrays of 16.
+//
+// LayerNorm's sum of (v - mu)^2 is s2 - mu (2 s1 - K mu) with s1, s2 the sums of v and v^2,
+// all in float64: one pass and one barrier instead of two. The cancellation costs
+// s2 / that of its 53 bits; where it is more than 6 (a mean of eight deviations) the
+// second pass is made.
+template <int KIND, int MAXC, typename Live>
+__device__ __forceinline__ void norm_row(float (&v)[MAXC][8], const Live& live, int lt, int tpr, double inv_k,
+                                         double k, const float* gamma, const float* beta, float eps,
+                                         double (*red)[16]) {
   float mu = 0.0f;
+  double var;
   if constexpr (KIND == 1) {
-    double s1 = 0.0;
+    double s[2] = {0.0, 0.0};
 #pragma unroll
     for (int i = 0; i < MAXC; ++i)
       if (live(i))
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s1 += (double)v[i][e];
-    mu = (float)(row_sum<TPR>(s1, red) / (double)K);
+        for (int e = 0; e < 8; ++e) {
+          const double d = (double)v[i][e];
+          s[0] += d;
+          s[1] = fma(d, d, s[1]);
+        }
+    row_sum<2>(s, red);
+    mu = (float)(s[0] * inv_k);
+    const double m = (double)mu;
+    var = s[1] - m * (2.0 * s[0] - k * m);
+    if (!(var * 64.0 > s[1])) {  // the same for every thread of the block
+      double t[1] = {0.0};
+#pragma unroll
+      for (int i = 0; i < MAXC; ++i)
+        if (live(i))
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const double d = (double)v[i][e] - m;
+            t[0] = fma(d, d, t[0]);
+          }
+      row_sum<1>(t, red + 2);
+      var = t[0];
+    }
+  } else {
+    double s[1] = {0.0};
+#pragma unroll
+    for (int i = 0; i < MAXC; ++i)
+      if (live(i))
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const double d = (double)v[i][e];
+          s[0] = fma(d, d, s[0]);
+        }
+    row_sum<1>(s, red);
+    var = s[0];
   }
-  double s2 = 0.0;
-#pragma unroll
-  for (int i = 0; i < MAXC; ++i)
-    if (live(i))
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double d = KIND == 1 ? (double)v[i][e] - (double)mu : (double)v[i][e];
-        s2 += d * d;
-      }
-  s2 = row_sum<TPR>(s2, red);
-  const float r = (float)(1.0 / sqrt(s2 / (double)K + (double)eps));
+  const float r = (float)rsqrt64(var * inv_k + (double)eps);
 #pragma unroll
   for (int i = 0; i < MAXC; ++i) {
     if (!live(i)) continue;
-    const int64_t c = lt + (int64_t)i * TPR;
+    const int64_t c = lt + (int64_t)i * tpr;
     float g[8];
     load8(gamma, c, g);
 #pragma unroll
@@ -112,42 +187,46 @@ __device__ __forceinline__ void norm_row(float (&v)[MAXC][8], const Live& live, 
   }
 }
 
-// One row per TPR threads, held in registers: K <= 8 MAXC TPR. The residual row is
-// loaded with the block's output, but by the 1024-thread blocks of the longest rows,
-// which have 128 registers a thread, after the post norm.
-template <int KIND, int TPR, int MAXC>
-__global__ __launch_bounds__(block_threads(TPR)) void block_norm_kernel(const BlockNormArgs p) {
-  constexpr int RPB = block_threads(TPR) / TPR;
-  __shared__ double red[16];
-  const int lt = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  const bool valid = row < p.M;
-  const int64_t K = p.K, nch = K >> 3, rr = valid ? row : p.M - 1;
-  const int niter = (int)((nch + TPR - 1) / TPR);
-  const uint4* yr = reinterpret_cast<const uint4*>(p.Y + rr * p.ldy);
-  const uint4* hr = reinterpret_cast<const uint4*>(p.H + rr * p.ldh);
-  auto live = [&](int i) { return valid && i < niter && lt + (int64_t)i * TPR < nch; };
+// One row per block of tpr threads, held in registers: K <= 8 MAXC tpr. The residual row
+// is loaded with the block's output, but with four chunks a thread (up to 1024 threads
+// of 128 registers) after the post norm. Every output row is read by the thread that writes it before it
+// does, so Hout may be an input's rows.
+template <int KIND, int MAXC>
+__global__ __launch_bounds__(1024) void block_norm_kernel(const BlockNormArgs p) {
+  __shared__ double red[6][16];
+  __shared__ float redf[16];
+  const int tpr = (int)blockDim.x, lt = (int)threadIdx.x;
+  // an XCD takes a contiguous range of rows: their scale bytes share lines
+  const uint32_t g8 = gridDim.x & ~7u;
+  const uint32_t blk = blockIdx.x < g8 ? (blockIdx.x & 7u) * (g8 >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+  const int64_t row = p.row0 + blk, K = p.K;
+  const double inv_k = p.inv_k, k = (double)K;
+  const int nch = (int)(K >> 3), niter = (nch + tpr - 1) / tpr;
+  const uint4* yr = reinterpret_cast<const uint4*>(p.Y + row * p.ldy);
+  const uint4* hr = reinterpret_cast<const uint4*>(p.H + row * p.ldh);
+  auto live = [&](int i) { return lt + i * tpr < nch; };
 
-  constexpr bool kLateH = TPR == 1024 && MAXC > 2;
+  constexpr bool kLateH = MAXC > 2;
   uint4 hraw[MAXC];
   float v[MAXC][8];
 #pragma unroll
   for (int i = 0; i < MAXC; ++i) {
     if (i >= niter) continue;
-    const int64_t c = lt + (int64_t)i * TPR, cc = c < nch ? c : nch - 1;
+    const int c = lt + i * tpr, cc = c < nch ? c : nch - 1;
     bf16x8(yr[cc], v[i]);
     if constexpr (!kLateH) hraw[i] = hr[cc];
   }
-  if (p.post_gamma) norm_row<KIND, TPR, MAXC>(v, live, lt, K, p.post_gamma, p.post_beta, p.eps, red);
+  if (p.post_gamma)
+    norm_row<KIND, MAXC>(v, live, lt, tpr, inv_k, k, p.post_gamma, p.post_beta, p.eps, red);
 
 #pragma unroll
   for (int i = 0; i < MAXC; ++i) {
     if (!live(i)) continue;
-    const int64_t c = lt + (int64_t)i * TPR;
+    const int c = lt + i * tpr;
     if (p.gate) {
       float g[8];
       if (p.gate_rows)
-        bf16x8(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.gate) + rr * p.ldgate)[c], g);
+        bf16x8(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.gate) + row * p.ldgate)[c], g);
       else
         load8(static_cast<const float*>(p.gate), c, g);
 #pragma unroll
@@ -159,18 +238,18 @@ __global__ __launch_bounds__(block_threads(TPR)) void block_norm_kernel(const Bl
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] = h[e] * p.res + v[i][e];
     const uint4 o = pack8(v[i]);
-    reinterpret_cast<uint4*>(p.Hout + rr * p.ldo)[c] = o;
+    reinterpret_cast<uint4*>(p.Hout + row * p.ldo)[c] = o;
     bf16x8(o, v[i]);
   }
 
-  norm_row<KIND, TPR, MAXC>(v, live, lt, K, p.gamma, p.beta, p.eps, red);
+  norm_row<KIND, MAXC>(v, live, lt, tpr, inv_k, k, p.gamma, p.beta, p.eps, red + 3);
 
   if (p.fmt == kActMxFp4 || p.fmt == kActMxFp8) {
     // every lane takes part in the block maxima
 #pragma unroll
     for (int i = 0; i < MAXC; ++i) {
       if (i >= niter) continue;
-      const int64_t c = lt + (int64_t)i * TPR;
+      const int64_t c = lt + i * tpr;
       const bool on = live(i);
       if (!on)
 #pragma unroll
@@ -184,9 +263,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void block_norm_kernel(const Bl
   if (p.fmt == kActBf16) {
 #pragma unroll
     for (int i = 0; i < MAXC; ++i)
-      if (live(i))
-        reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.codes) + row * K)[lt + (int64_t)i * TPR] =
-            pack8(v[i]);
+      if (live(i)) reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.codes) + row * K)[lt + i * tpr] = pack8(v[i]);
     return;
   }
   float amax = 0.0f;
@@ -195,17 +272,18 @@ __global__ __launch_bounds__(block_threads(TPR)) void block_norm_kernel(const Bl
     if (live(i))
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[i][e]));
-  amax = row_max<TPR>(amax, red);
-  if (!valid) return;
+  amax = row_max(amax, redf);
   const bool i8 = p.fmt == kActInt8;
-  const float t = amax / (i8 ? qmax<kQInt8>() : qmax<kQFp8>());
+  const float t = amax / (i8 ? qmax<kQInt8>() : qmax<kQFp8>()), inv = 1.0f / t;
   if (lt == 0) static_cast<float*>(p.scales)[row] = t;
 #pragma unroll
   for (int i = 0; i < MAXC; ++i) {
     if (!live(i)) continue;
     uint2 q = make_uint2(0u, 0u);
     if (t != 0.0f) {
-      if (i8) {
+      if (i8 && inv < 3.0e38f) {
+        q = int8_codes8(v[i], t, inv);
+      } else if (i8) {
         q.x = quant_codes4<kQInt8>(v[i][0], v[i][1], v[i][2], v[i][3], t);
         q.y = quant_codes4<kQInt8>(v[i][4], v[i][5], v[i][6], v[i][7], t);
       } else {
@@ -213,65 +291,107 @@ __global__ __launch_bounds__(block_threads(TPR)) void block_norm_kernel(const Bl
         q.y = quant_codes4<kQFp8>(v[i][4], v[i][5], v[i][6], v[i][7], t);
       }
     }
-    reinterpret_cast<uint2*>(p.codes + row * K)[lt + (int64_t)i * TPR] = q;
+    reinterpret_cast<uint2*>(p.codes + row * K)[lt + i * tpr] = q;
   }
 }
 
-// Eight outputs per lane: a = fl32(g u / (1 + exp(-g))) in float64, block-wise codes.
+// g u / (1 + exp(-g)) in float64, relative error below 2^-40 (so its fp32 rounding is the
+// exact value's unless that lies as close to a rounding boundary). With x = -g log2(e)
+// (off by at most 2^-43), n = rint(x), exp(-g) = 2^n 2^f, |f| <= 1/2, 2^f by its Taylor
+// polynomial of degree 10 (remainder (ln 2 / 2)^11 / 11! < 2^-42); the quotient by the
+// reciprocal instruction (relative error at most 2^-23) and a Newton step (2^-46). g is
+// clamped to +-700 for the exponential, where the value is g u or rounds to zero. Of the
+// order of half the operations of the library's exp and an IEEE division.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const double x = (double)__builtin_amdgcn_fmed3f(g, -700.0f, 700.0f) * -1.4426950408889634;
+  const double n = rint(x), f = x - n;
+  double p = 7.054911620801121e-09;  // ln(2)^k / k!, k = 10 .. 0
+  p = fma(p, f, 1.0178086009239696e-07);
+  p = fma(p, f, 1.3215486790144305e-06);
+  p = fma(p, f, 1.5252733804059838e-05);
+  p = fma(p, f, 0.00015403530393381606);
+  p = fma(p, f, 0.0013333558146428441);
+  p = fma(p, f, 0.009618129107628477);
+  p = fma(p, f, 0.055504108664821576);
+  p = fma(p, f, 0.2402265069591007);
+  p = fma(p, f, 0.6931471805599453);
+  p = fma(p, f, 1.0);
+  const double d = 1.0 + ldexp(p, (int)n);
+  double r = __builtin_amdgcn_rcp(d);
+  r = fma(r, fma(-d, r, 1.0), r);
+  return (float)(((double)g * (double)u) * r);
+}
+
+// Rows [row0, row0 + w.rows), two chunks of eight outputs a thread, block-wise codes.
 template <bool FP4>
 __global__ __launch_bounds__(256) void silu_mx_kernel(const uint16_t* __restrict__ G,
                                                       const uint16_t* __restrict__ U, int64_t M,
                                                       int64_t N, int64_t ldg, int64_t ldu,
                                                       uint8_t* __restrict__ codes,
-                                                      uint8_t* __restrict__ scales) {
-  const int64_t cpr = ((N + 127) >> 7) << 4;
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = idx / cpr, c = idx - row * cpr;
-  const bool live = row < M && 8 * c < N;
-  float v[8] = {};
-  if (live) {
-    float g[8], u[8];
-    bf16x8(*reinterpret_cast<const uint4*>(G + row * ldg + 8 * c), g);
-    bf16x8(*reinterpret_cast<const uint4*>(U + row * ldu + 8 * c), u);
+                                                      uint8_t* __restrict__ scales, int64_t row0,
+                                                      ChunkWalk w) {
+  constexpr int NU = 2;
+  const uint32_t total = w.rows * w.cpr, i0 = w.first(NU), nch = (uint32_t)(N >> 3);
+  uint4 g[NU], u[NU];
+  int64_t row[NU];
+  uint32_t c[NU];
+  bool live[NU];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double gd = g[e];
-      v[e] = (float)((gd * (double)u[e]) / (1.0 + exp(-gd)));
+  for (int j = 0; j < NU; ++j) {
+    const uint32_t i = i0 + j * 256u, r = w.row(i);
+    row[j] = row0 + r;
+    c[j] = i - r * w.cpr;
+    live[j] = i < total && c[j] < nch;
+    g[j] = u[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (live[j]) {
+      g[j] = *reinterpret_cast<const uint4*>(G + row[j] * ldg + 8 * c[j]);
+      u[j] = *reinterpret_cast<const uint4*>(U + row[j] * ldu + 8 * c[j]);
     }
   }
-  mx_store_row8<FP4>(v, live, row, M, c, N, codes, scales);
+#pragma unroll
+  for (int j = 0; j < NU; ++j) {
+    float a[8], b[8];
+    bf16x8(g[j], a);
+    bf16x8(u[j], b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = silu_mul(a[e], b[e]);
+    mx_store_row8<FP4>(a, live[j], row[j], M, c[j], N, codes, scales);
+  }
 }
 
-template <int TPR, int MAXC>
-void launch_rows(const BlockNormArgs& p, int kind, hipStream_t st) {
-  constexpr int NT = block_threads(TPR), RPB = NT / TPR;
-  const dim3 g((unsigned)((p.M + RPB - 1) / RPB)), b(NT);
-  if (kind == 0) hipLaunchKernelGGL((block_norm_kernel<0, TPR, MAXC>), g, b, 0, st, p);
-  else hipLaunchKernelGGL((block_norm_kernel<1, TPR, MAXC>), g, b, 0, st, p);
+template <int MAXC>
+void launch_rows(BlockNormArgs p, int kind, hipStream_t st) {
+  constexpr int64_t kBlocks = (int64_t)1 << 21;  // per launch
+  const int nch = (int)(p.K >> 3), threads = ((nch + MAXC - 1) / MAXC + 63) & ~63;
+  p.inv_k = 1.0 / (double)p.K;
+  for (p.row0 = 0; p.row0 < p.M; p.row0 += kBlocks) {
+    const int64_t blocks = p.M - p.row0 < kBlocks ? p.M - p.row0 : kBlocks;
+    const dim3 g((unsigned)blocks), b(threads);
+    if (kind == 0) hipLaunchKernelGGL((block_norm_kernel<0, MAXC>), g, b, 0, st, p);
+    else hipLaunchKernelGGL((block_norm_kernel<1, MAXC>), g, b, 0, st, p);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNormArgs& p, int kind, hipStream_t st) {
   if (p.M == 0 || p.K == 0) return hipSuccess;
-  if (p.K <= 2048) launch_rows<64, 4>(p, kind, st);
-  else if (p.K <= 4096) launch_rows<256, 2>(p, kind, st);
-  else if (p.K <= 8192) launch_rows<512, 2>(p, kind, st);
-  else if (p.K <= 16384) launch_rows<1024, 2>(p, kind, st);
-  else launch_rows<1024, 4>(p, kind, st);
+  const int64_t nch = p.K >> 3;
+  if (nch <= 1024 && p.M <= 512) launch_rows<1>(p, kind, st);
+  else if (nch <= 2048 && (p.M < 2048 || nch < 256)) launch_rows<2>(p, kind, st);
+  else launch_rows<4>(p, kind, st);
   return hipGetLastError();
 }
 
 hipError_t launch_silu_mx(const void* G, const void* U, int64_t M, int64_t N, int64_t ldg, int64_t ldu,
                           int fmt, void* codes, uint8_t* scales, hipStream_t st) {
-  const int64_t total = M * (((N + 127) >> 7) << 4);
-  if (total == 0) return hipSuccess;
-  const dim3 gr((unsigned)((total + 255) / 256)), b(256);
   const uint16_t *g = static_cast<const uint16_t*>(G), *u = static_cast<const uint16_t*>(U);
   uint8_t* q = static_cast<uint8_t*>(codes);
-  if (fmt == kActMxFp4) hipLaunchKernelGGL(silu_mx_kernel<true>, gr, b, 0, st, g, u, M, N, ldg, ldu, q, scales);
-  else hipLaunchKernelGGL(silu_mx_kernel<false>, gr, b, 0, st, g, u, M, N, ldg, ldu, q, scales);
-  return hipGetLastError();
+  const dim3 b(256);
+  return chunk_launches(M, ((N + 127) >> 7) << 4, 2, [&](int64_t r, ChunkWalk w, dim3 gr) {
+    if (fmt == kActMxFp4) hipLaunchKernelGGL(silu_mx_kernel<true>, gr, b, 0, st, g, u, M, N, ldg, ldu, q, scales, r, w);
+    else hipLaunchKernelGGL(silu_mx_kernel<false>, gr, b, 0, st, g, u, M, N, ldg, ldu, q, scales, r, w);
+  });
 }
 
 }  // namespace qr

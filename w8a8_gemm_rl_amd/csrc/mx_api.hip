@@ -85,6 +85,7 @@ size_t mx4_workspace(const char* fn, int64_t M, int64_t N, int64_t K, int xfmt) 
   if (M == 0 || N == 0) return 0;
   const size_t gemm = mx4_gemm_ws_bytes(M, N, K, xfmt);
   if (std::strcmp(fn, "qr_mxfp4_gemm") == 0) return gemm;
+  if (mx4_one_launch(M, K)) return 0;
   return align256(gemm) + align256((size_t)(M * code_row_bytes(K, xfmt))) +
          align256((size_t)scale_bytes(M, K));
 }

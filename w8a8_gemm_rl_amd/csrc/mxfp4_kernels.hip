@@ -23,73 +23,102 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-// One chunk of eight values per lane, four lanes a block; 256 chunks per block of
-// threads, rows padded to whole 16-chunk panels so that lanes keep their place.
+// Rows [row0, row0 + w.rows) of A, two chunks of eight values a thread, four lanes a
+// block of 32; rows padded to whole 16-chunk panels so that lanes keep their place in a
+// block (pad chunks hold zeros). One pass, bound by memory; the weights are read once and
+// not again soon, hence the non-temporal loads.
 template <bool FP4, bool BF16>
 __global__ __launch_bounds__(256) void mx4_quant_kernel(const void* __restrict__ A, int64_t R,
                                                         int64_t K, int64_t lda,
                                                         uint8_t* __restrict__ codes,
-                                                        uint8_t* __restrict__ scales) {
-  const int64_t cpr = ((K + 127) >> 7) << 4;  // chunks per row, padded
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = idx / cpr, c = idx - row * cpr;
-  const bool live = row < R && 8 * c < K;
-  float v[8] = {};
-  if (live) {
+                                                        uint8_t* __restrict__ scales, int64_t row0,
+                                                        ChunkWalk w) {
+  constexpr int U = 2;
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  const uint32_t total = w.rows * w.cpr, i0 = w.first(U), nch = (uint32_t)(K >> 3);
+  float v[U][8];
+  int64_t row[U];
+  uint32_t c[U];
+  bool live[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = i0 + u * 256u, r = w.row(i);
+    row[u] = row0 + r;
+    c[u] = i - r * w.cpr;
+    live[u] = i < total && c[u] < nch;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
+    if (!live[u]) continue;
     if constexpr (BF16) {
-      bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A) + row * lda + 8 * c), v);
+      bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A) + row[u] * lda + 8 * c[u]), v[u]);
     } else {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(A) + row * lda + 8 * c);
-      const float4 a = p[0], b = p[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      const f4* p = reinterpret_cast<const f4*>(static_cast<const float*>(A) + row[u] * lda + 8 * c[u]);
+      const f4 a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[u][e] = a[e];
+        v[u][4 + e] = b[e];
+      }
     }
   }
-  mx_store_row8<FP4>(v, live, row, R, c, K, codes, scales);
+#pragma unroll
+  for (int u = 0; u < U; ++u) mx_store_row8<FP4>(v[u], live[u], row[u], R, c[u], K, codes, scales);
 }
 
-// Eight values per lane from their codes and the block's scale byte.
+// Eight values from their codes (q: four or eight bytes) and their block's scale byte.
+template <bool FP4>
+__device__ __forceinline__ void mx_values8(const uint2 q, uint32_t sb, float* v) {
+  const float s = mx_scale_value(sb);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (FP4) {
+      // |v| = m / 2 for codes 0 and 1, else (1 + m / 2) 2^(ex - 1)
+      const uint32_t x = (q.x >> (4 * e)) & 15u, ex = (x >> 1) & 3u, m = x & 1u;
+      const uint32_t mag = ex == 0u ? (m ? 0x3f000000u : 0u) : ((ex + 126u) << 23) | (m << 22);
+      v[e] = __uint_as_float(mag | ((x & 8u) << 28)) * s;
+    } else {
+      const uint32_t x = (e < 4 ? q.x >> (8 * e) : q.y >> (8 * (e - 4))) & 255u;
+      const uint32_t ex = (x >> 3) & 15u, m = x & 7u;
+      const float mag = ex == 0u ? (float)m * 0x1p-9f : __uint_as_float(((ex + 120u) << 23) | (m << 20));
+      v[e] = ((x & 127u) == 127u ? __uint_as_float(0x7fc00000u) : ((x & 128u) ? -mag : mag)) * s;
+    }
+  }
+}
+
+// Values of rows [row0, row0 + w.rows), four chunks of eight a thread.
 template <bool FP4, bool BF16>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scales,
                                                          int64_t R, int64_t K, void* __restrict__ out,
-                                                         int64_t ldo) {
-  const int64_t cpr = K >> 3;
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= R * cpr) return;
-  const int64_t row = idx / cpr, c = idx - row * cpr;
-  const int64_t b = c >> 2;
-  const float s = mx_scale_value(scales[((b >> 2) * R + row) * 4 + (b & 3)]);
-  float v[8];
-  if constexpr (FP4) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + row * (K >> 1) + 4 * c);
+                                                         int64_t ldo, int64_t row0, ChunkWalk w) {
+  constexpr int U = 4;
+  const uint32_t total = w.rows * w.cpr, i0 = w.first(U);
+  uint2 q[U];
+  uint32_t sb[U], c[U];
+  int64_t row[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // |v| = m / 2 for codes 0 and 1, else (1 + m / 2) 2^(e - 1)
-      const uint32_t q = (w >> (4 * e)) & 15u, ex = (q >> 1) & 3u, m = q & 1u;
-      const uint32_t mag = ex == 0u ? (m ? 0x3f000000u : 0u) : ((ex + 126u) << 23) | (m << 22);
-      v[e] = __uint_as_float(mag | ((q & 8u) << 28)) * s;
-    }
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(codes + row * K + 8 * c);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t q = (e < 4 ? w.x >> (8 * e) : w.y >> (8 * (e - 4))) & 255u;
-      const uint32_t ex = (q >> 3) & 15u, m = q & 7u;
-      const float mag = ex == 0u ? (float)m * 0x1p-9f : __uint_as_float(((ex + 120u) << 23) | (m << 20));
-      v[e] = ((q & 127u) == 127u ? __uint_as_float(0x7fc00000u) : ((q & 128u) ? -mag : mag)) * s;
-    }
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = i0 + u * 256u, ii = i < total ? i : total - 1, r = w.row(ii);
+    row[u] = row0 + r;
+    c[u] = ii - r * w.cpr;
+    q[u].y = 0u;
+    if constexpr (FP4) q[u].x = *reinterpret_cast<const uint32_t*>(codes + row[u] * (K >> 1) + 4 * c[u]);
+    else q[u] = *reinterpret_cast<const uint2*>(codes + row[u] * K + 8 * c[u]);
+    sb[u] = scales[((int64_t)(c[u] >> 4) * R + row[u]) * 4 + ((c[u] >> 2) & 3u)];
   }
-  if constexpr (BF16) {
-    uint32_t h[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = f32_to_bf16_any(v[e]);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * ldo + 8 * c) =
-        make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
-  } else {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * ldo + 8 * c);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  for (int u = 0; u < U; ++u) {
+    if (i0 + u * 256u >= total) break;
+    float v[8];
+    mx_values8<FP4>(q[u], sb[u], v);
+    if constexpr (BF16) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row[u] * ldo + 8 * c[u]) =
+          make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+    } else {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row[u] * ldo + 8 * c[u]);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
@@ -173,13 +202,13 @@ __global__ __launch_bounds__(64 * NW) void mx4_decode_kernel(const Mx4Params p,
       uint4 x[XC];
 #pragma unroll
       for (int u = 0; u < XC; ++u) {
-        const int c = c0 + u * 64 * NW, t = c / cpr;
+        const int c = c0 + u * 64 * NW, t = M == 1 ? 0 : c / cpr;
         x[u] = make_uint4(0u, 0u, 0u, 0u);
         if (c < total) x[u] = *reinterpret_cast<const uint4*>(X + t * ldx + 8 * (c - t * cpr));
       }
 #pragma unroll
       for (int u = 0; u < XC; ++u) {
-        const int c = c0 + u * 64 * NW, t = c / cpr, q = c - t * cpr;
+        const int c = c0 + u * 64 * NW, t = M == 1 ? 0 : c / cpr, q = c - t * cpr;
         float v[8];
         bf16x8(x[u], v);
         const uint32_t sb = mx_block_scale<XFP4>(v);
@@ -605,7 +634,9 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
                 make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
           }
 #pragma unroll
-      for (int c = lane; c < JC * T * CPR; c += 64) {
+      for (int k = 0; k < (JC * T * CPR + 63) / 64; ++k) {
+        const int c = lane + 64 * k;
+        if (JC * T * CPR % 64 != 0 && c >= JC * T * CPR) break;
         const int ml = c / CPR, nl = 8 * (c % CPR);
         const int64_t m = mw + T * j0 + ml;
         if (m >= M || nl >= ow || T * j0 + ml >= WTM) continue;
@@ -755,34 +786,31 @@ Mx4Plan make_mx4_plan(int64_t M, int64_t N, int64_t K, bool fp4) {
 
 hipError_t launch_mx4_quant(const void* A, int64_t R, int64_t K, int64_t lda, int bf16, int fmt,
                             void* codes, uint8_t* scales, hipStream_t st) {
-  const int64_t total = R * (((K + 127) >> 7) << 4);
-  if (total == 0) return hipSuccess;
-  const dim3 g((unsigned)((total + 255) / 256)), b(256);
   uint8_t* q = static_cast<uint8_t*>(codes);
-  if (fmt == kActMxFp4) {
-    if (bf16) hipLaunchKernelGGL((mx4_quant_kernel<true, true>), g, b, 0, st, A, R, K, lda, q, scales);
-    else hipLaunchKernelGGL((mx4_quant_kernel<true, false>), g, b, 0, st, A, R, K, lda, q, scales);
-  } else {
-    if (bf16) hipLaunchKernelGGL((mx4_quant_kernel<false, true>), g, b, 0, st, A, R, K, lda, q, scales);
-    else hipLaunchKernelGGL((mx4_quant_kernel<false, false>), g, b, 0, st, A, R, K, lda, q, scales);
-  }
-  return hipGetLastError();
+  const dim3 b(256);
+  return chunk_launches(R, ((K + 127) >> 7) << 4, 2, [&](int64_t r, ChunkWalk w, dim3 g) {
+    if (fmt == kActMxFp4) {
+      if (bf16) hipLaunchKernelGGL((mx4_quant_kernel<true, true>), g, b, 0, st, A, R, K, lda, q, scales, r, w);
+      else hipLaunchKernelGGL((mx4_quant_kernel<true, false>), g, b, 0, st, A, R, K, lda, q, scales, r, w);
+    } else {  // bf16 tokens of a product
+      hipLaunchKernelGGL((mx4_quant_kernel<false, true>), g, b, 0, st, A, R, K, lda, q, scales, r, w);
+    }
+  });
 }
 
 hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int fmt,
                              void* out, int64_t ldo, int bf16, hipStream_t st) {
-  const int64_t total = R * (K >> 3);
-  if (total == 0) return hipSuccess;
-  const dim3 g((unsigned)((total + 255) / 256)), b(256);
   const uint8_t* q = static_cast<const uint8_t*>(codes);
-  if (fmt == kActMxFp4) {
-    if (bf16) hipLaunchKernelGGL((mx_dequant_kernel<true, true>), g, b, 0, st, q, scales, R, K, out, ldo);
-    else hipLaunchKernelGGL((mx_dequant_kernel<true, false>), g, b, 0, st, q, scales, R, K, out, ldo);
-  } else {
-    if (bf16) hipLaunchKernelGGL((mx_dequant_kernel<false, true>), g, b, 0, st, q, scales, R, K, out, ldo);
-    else hipLaunchKernelGGL((mx_dequant_kernel<false, false>), g, b, 0, st, q, scales, R, K, out, ldo);
-  }
-  return hipGetLastError();
+  const dim3 b(256);
+  return chunk_launches(R, K >> 3, 4, [&](int64_t r, ChunkWalk w, dim3 g) {
+    if (fmt == kActMxFp4) {
+      if (bf16) hipLaunchKernelGGL((mx_dequant_kernel<true, true>), g, b, 0, st, q, scales, R, K, out, ldo, r, w);
+      else hipLaunchKernelGGL((mx_dequant_kernel<true, false>), g, b, 0, st, q, scales, R, K, out, ldo, r, w);
+    } else {
+      if (bf16) hipLaunchKernelGGL((mx_dequant_kernel<false, true>), g, b, 0, st, q, scales, R, K, out, ldo, r, w);
+      else hipLaunchKernelGGL((mx_dequant_kernel<false, false>), g, b, 0, st, q, scales, R, K, out, ldo, r, w);
+    }
+  });
 }
 
 hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq,
@@ -809,7 +837,9 @@ size_t mx4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int xfmt) {
 // LDS (7B down projection, one token: 10.5 against 13.7 us). Long rows with few blocks
 // split K over 16 waves; many rows (the stacked gate and up) take 32 rows a block, half
 // of K a wave (14.2 us; 20.4 with 16 rows over eight waves).
-bool mx4_one_launch(int64_t M, int64_t K) { return M * K <= 16384 || (M <= 2 && M * K <= 40960); }
+bool mx4_one_launch(int64_t M, int64_t K) {
+  return K > 0 && M <= 16 && (M * K <= 16384 || (M <= 2 && M * K <= 40960));
+}
 
 template <bool XFP4>
 hipError_t launch_fused(const Mx4Params& p, const uint16_t* X, int64_t ldx, hipStream_t st) {
@@ -825,7 +855,7 @@ hipError_t launch_mx4_linear(const void* X, int64_t ldx, int xfmt, const void* W
                              hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
   const bool fp4 = xfmt == kActMxFp4;
-  if (K > 0 && M <= 16 && mx4_one_launch(M, K)) {
+  if (mx4_one_launch(M, K)) {
     const Mx4Params p{nullptr, nullptr, static_cast<const uint8_t*>(Wq), sw, M, N, K, Y, ldy, 0};
     const uint16_t* x = static_cast<const uint16_t*>(X);
     return fp4 ? launch_fused<true>(p, x, ldx, st) : launch_fused<false>(p, x, ldx, st);

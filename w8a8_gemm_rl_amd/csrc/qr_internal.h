@@ -47,6 +47,7 @@ hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const vo
 hipError_t launch_mx4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const uint8_t* sw,
                              int64_t M, int64_t N, int64_t K, void* Y, int64_t ldy, void* ws,
                              hipStream_t st);
+bool mx4_one_launch(int64_t M, int64_t K);  // qr_mxfp4_linear needs no workspace
 // Workspace of qr_mxfp4_gemm / qr_mxfp4_linear; (size_t)-1 for invalid sizes.
 size_t mx4_workspace(const char* fn, int64_t M, int64_t N, int64_t K, int xfmt);
 
@@ -58,6 +59,8 @@ struct BlockNormArgs {
   uint8_t* codes;
   void* scales;
   int64_t ldy, ldh, ldgate, ldo, M, K;
+  int64_t row0 = 0;    // first row of the launch
+  double inv_k = 0.0;  // 1 / K
   float res, eps;
   int fmt;
   bool gate_rows;

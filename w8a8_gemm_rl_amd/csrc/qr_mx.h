@@ -116,6 +116,40 @@ __device__ __forceinline__ void mx_store_row8(const float* v, bool live, int64_t
   if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + ((c >> 4) * R + row) * 4) = w;
 }
 
+// Elementwise passes over rows of 16-byte-aligned chunks of eight values: a block of 256
+// threads takes U * 256 consecutive chunks (lane order = chunk order, a thread's chunks
+// 256 apart), rows counting `cpr` chunks. Blocks are numbered so that an XCD takes a
+// contiguous range: neighbouring rows' scale bytes share lines.
+struct ChunkWalk {
+  uint32_t rows, cpr;     // rows of this launch, chunks per row; rows * cpr < 2^31
+  uint32_t magic, shift;  // i / cpr = mulhi(i, magic) >> shift for i < 2^31
+  // With 2^(s-1) < cpr <= 2^s, magic = floor(2^(31+s) / cpr) + 1 exceeds 2^(31+s) / cpr by
+  // at most 1, so i magic / 2^(31+s) exceeds i / cpr by less than 1 / cpr.
+  static ChunkWalk of(int64_t rows, int64_t cpr) {  // cpr >= 2
+    uint32_t s = 1;
+    while (((int64_t)1 << s) < cpr) ++s;
+    return {(uint32_t)rows, (uint32_t)cpr, (uint32_t)(((uint64_t)1 << (31 + s)) / (uint64_t)cpr + 1), s - 1};
+  }
+  __device__ __forceinline__ uint32_t row(uint32_t i) const { return __umulhi(i, magic) >> shift; }
+  __device__ __forceinline__ uint32_t first(int u) const {
+    const uint32_t g8 = gridDim.x & ~7u, b = blockIdx.x;
+    const uint32_t blk = b < g8 ? (b & 7u) * (g8 >> 3) + (b >> 3) : b;
+    return (blk * (uint32_t)u) * 256u + threadIdx.x;
+  }
+};
+
+// Host: launches `launch(row0, walk, grid)` over row ranges of at most 2^30 chunks.
+template <typename F>
+hipError_t chunk_launches(int64_t rows, int64_t cpr, int u, const F& launch) {
+  if (rows == 0 || cpr == 0) return hipSuccess;
+  const int64_t step = ((int64_t)1 << 30) / cpr > 0 ? ((int64_t)1 << 30) / cpr : 1;
+  for (int64_t r = 0; r < rows; r += step) {
+    const int64_t n = rows - r < step ? rows - r : step;
+    launch(r, ChunkWalk::of(n, cpr), dim3((unsigned)((n * cpr + u * 256 - 1) / (u * 256))));
+  }
+  return hipGetLastError();
+}
+
 // fp32 -> bf16 bits, round to nearest even; NaN stays NaN.
 __device__ __forceinline__ uint32_t f32_to_bf16_any(float f) {
   const uint32_t u = __float_as_uint(f);
