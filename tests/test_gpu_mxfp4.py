@@ -166,9 +166,63 @@ def test_gemm_against_exact_block_sums(M, N, K, fmt):
     assert torch.equal(lin, again)
 
 
+def _random_operand(rows, K, fmt, seed):
+    """Device codes and scale panels drawn directly (every code, a range of scales), and their
+    float64 values by table: for products too large for the host."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    draw = lambda hi, *shape: torch.randint(0, hi, shape, dtype=torch.uint8, device=DEV, generator=g)  # noqa: E731
+    s = 118 + draw(12, K // 128, rows, 4)
+    if fmt == "mxfp4":
+        codes = draw(256, rows, K // 2)
+        table = torch.from_numpy(O.e2m1_decode(np.arange(16))).to(DEV)
+        v = table[torch.stack((codes & 15, codes >> 4), dim=2).view(rows, K).int()]
+    else:
+        codes = draw(256, rows, K)
+        codes = torch.where((codes & 127) == 127, torch.zeros_like(codes), codes)  # no NaN codes
+        v = torch.from_numpy(np.nan_to_num(O.e4m3fn_decode(np.arange(256)))).to(DEV)[codes.int()]
+        codes = codes.view(torch.float8_e4m3fn)
+    X = s.permute(1, 0, 2).reshape(rows, K // 32).double() - 127.0
+    v = v.view(rows, -1, 32) * torch.exp2(X)[:, :, None]
+    return codes, s, v.view(rows, K)
+
+
+# One shape or more for each tile configuration of the planner, without and with a split of K,
+# odd numbers of 128-element panels, odd and even row strides among them.
+CONFIGS = [(1200, 9000, 384), (300, 30000, 1152), (300, 30000, 9344), (700, 9000, 640), (130, 20001, 384), (512, 3584, 18944),
+           (1326, 2334, 896), (256, 3584, 18944), (1030, 3584, 1408), (1636, 1345, 1280), (1856, 131, 14592),
+           (2325, 819, 384), (3776, 41, 14976), (2756, 67, 7552), (128, 4608, 3584), (52, 9542, 6784),
+           (258, 689, 9984), (298, 285, 11904), (24, 426, 5504), (20, 20000, 2944), (1024, 5120, 27648),
+           (2, 30000, 640), (1, 50000, 384), (1, 3584, 18944), (2, 100, 20480), (1, 7, 40960), (1, 24, 41088),
+           (16, 8192, 8192), (5, 3584, 3584)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K", CONFIGS)
+def test_gemm_every_configuration(M, N, K, fmt):
+    xc, xs, x = _random_operand(M, K, fmt, M + N)
+    wc, ws, w = _random_operand(N, K, "mxfp4", K)
+    y = B.mxfp4_gemm(xc, xs, wc, ws)
+    raw = B.mxfp4_gemm(xc, xs, wc, ws, out="raw")
+    exact, size = x @ w.t(), x.abs() @ w.abs().t()
+    rel = (K / 32 + 64) * 2.0 ** -23 + (2.0 ** -12 if fmt == "mxfp8" else 0.0)
+    assert bool(((raw.double() - exact).abs() <= rel * size).all())
+    assert torch.equal(y, raw.to(torch.bfloat16))
+    assert torch.equal(B.mxfp4_gemm(xc, xs, wc, ws), y)
+    # the linear on bf16 tokens that quantize to some codes: its own quantization, then the same
+    # bound, and half a bf16 step (2^-8) of the value
+    X = B.mx_dequantize(xc, xs)
+    qc, qs = (B.mxfp4_quantize(X) if fmt == "mxfp4" else B.mx_quantize(X))
+    v = B.mx_dequantize(qc, qs, dtype=torch.float32).double()
+    lin = B.mxfp4_linear(X, wc, ws, x="fp4" if fmt == "mxfp4" else "fp8").double()
+    exact, size = v @ w.t(), v.abs() @ w.abs().t()
+    assert bool(((lin - exact).abs() <= rel * size + 2.0 ** -8 * (exact.abs() + rel * size)).all())
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("M,N,K,pad", [(1, 130, 384, 6), (9, 64, 384, 1), (40, 130, 256, 6), (70, 131, 256, 5),
-                                       (260, 264, 512, 8), (200, 1030, 384, 2), (600, 520, 256, 3)])
+                                       (260, 264, 512, 8), (200, 1030, 384, 2), (600, 520, 256, 3), (1200, 9000, 384, 4),
+                                       (1200, 9000, 384, 3), (700, 9001, 640, 1), (300, 515, 8320, 1)])
 def test_gemm_strided_tokens_and_outputs(M, N, K, pad, fmt):
     """Outputs in wider rows (strides that are and are not multiples of 8 and 4) leave the padding
     alone and hold the packed call's values; tokens in wider rows too."""

@@ -610,17 +610,47 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
   constexpr int NQ = T == 16 ? 1 : 4;
   const int64_t n0 = (int64_t)tn * BN;
   const int own = (int)(N - n0 < BN ? N - n0 : BN);
-  if (!p.part && !p.g.out_raw && (p.g.ldy & 7) == 0) {
+  if (!p.part && !p.g.out_raw) {
     // bf16 outputs through the idle ring, each wave its own part of it (only the last
-    // stage's reads have to be over), so that a lane stores 16 bytes of a token's row.
-    // Rows of 16 bytes more than the wave's channels spread the writes over the banks.
+    // stage's reads have to be over), so that a wave's stores run along a token's row:
+    // 16 bytes a lane, or 4 or 2 where the row stride (and so the rows' alignment) is no
+    // multiple of 8 or 2 channels. Rows of 16 bytes more than the wave's channels spread
+    // the writes over the banks.
     constexpr int LD = WTN * 2 + 16, FIT = S * STAGE / NW / (T * LD);
-    constexpr int JC = FIT < FM ? FIT : FM, CPR = WTN / 8;
+    constexpr int JC = FIT < FM ? FIT : FM;
     static_assert(JC >= 1, "a token fragment per wave fits the ring");
     uint8_t* so = smem + wid * (JC * T * LD);
     uint16_t* Y = static_cast<uint16_t*>(p.g.Y) + n0 + wn * WTN;
-    const int64_t mw = (int64_t)tm * BM + wm * WTM;
+    const int64_t mw = (int64_t)tm * BM + wm * WTM, ldy = p.g.ldy;
     const int ow = own - wn * WTN;
+    auto rows_out = [&](int j0, auto vec) {
+      constexpr int V = decltype(vec)::value, CPR = WTN / V, PIECES = JC * T * CPR;
+#pragma unroll V == 8 ? (PIECES + 63) / 64 : 4
+      for (int k = 0; k < (PIECES + 63) / 64; ++k) {
+        const int c = lane + 64 * k, ml = c / CPR, nl = V * (c % CPR);
+        const int64_t m = mw + T * j0 + ml;
+        if ((PIECES % 64 != 0 && c >= PIECES) || m >= M || nl >= ow || T * j0 + ml >= WTM) continue;
+        const uint8_t* src = so + ml * LD + nl * 2;
+        uint16_t* dst = Y + m * ldy + nl;
+        if constexpr (V == 8) {
+          typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+          const u4 v = *reinterpret_cast<const u4*>(src);
+          if (nl + 8 > ow) {
+            for (int e = 0; nl + e < ow; ++e) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+          } else if (p.nt_out) {
+            __builtin_nontemporal_store(v, reinterpret_cast<u4*>(dst));
+          } else {
+            *reinterpret_cast<u4*>(dst) = v;
+          }
+        } else if constexpr (V == 2) {
+          const uint32_t v = *reinterpret_cast<const uint32_t*>(src);
+          if (nl + 2 > ow) dst[0] = (uint16_t)v;
+          else *reinterpret_cast<uint32_t*>(dst) = v;
+        } else {
+          dst[0] = *reinterpret_cast<const uint16_t*>(src);
+        }
+      }
+    };
     __syncthreads();
 #pragma unroll
     for (int j0 = 0; j0 < FM; j0 += JC) {
@@ -634,25 +664,9 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
             *reinterpret_cast<uint2*>(so + (T * (j - j0) + lr) * LD + (T * i + 8 * q + 4 * lg) * 2) =
                 make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
           }
-#pragma unroll
-      for (int k = 0; k < (JC * T * CPR + 63) / 64; ++k) {
-        const int c = lane + 64 * k;
-        if (JC * T * CPR % 64 != 0 && c >= JC * T * CPR) break;
-        const int ml = c / CPR, nl = 8 * (c % CPR);
-        const int64_t m = mw + T * j0 + ml;
-        if (m >= M || nl >= ow || T * j0 + ml >= WTM) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(so + ml * LD + nl * 2);
-        uint16_t* dst = Y + m * p.g.ldy + nl;
-        if (nl + 8 <= ow) {
-          typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-          const u4 t = {v.x, v.y, v.z, v.w};
-          if (p.nt_out) __builtin_nontemporal_store(t, reinterpret_cast<u4*>(dst));
-          else *reinterpret_cast<u4*>(dst) = t;
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          for (int e = 0; nl + e < ow; ++e) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-        }
-      }
+      if ((ldy & 7) == 0) rows_out(j0, std::integral_constant<int, 8>{});
+      else if ((ldy & 1) == 0) rows_out(j0, std::integral_constant<int, 2>{});
+      else rows_out(j0, std::integral_constant<int, 1>{});
     }
     return;
   }
@@ -739,7 +753,7 @@ constexpr Mx4Config kFp4Configs[] = {
     {160, 128, 256, 1, 5.0f, 0.87f, 0.0f, launch_tile<true, 16, 160, 128, 2, 4, 3, 256>},
     {128, 128, 256, 1, 5.0f, 0.65f, 0.0f, launch_tile<true, 32, 128, 128, 2, 4, 4, 256>},
     {160, 64, 256, 1, 4.5f, 0.65f, 0.0f, launch_tile<true, 16, 160, 64, 2, 4, 4, 256>},
-    {128, 64, 256, 1, 4.5f, 0.56f, 0.0f, launch_tile<true, 16, 128, 64, 4, 2, 4, 256>},
+    {128, 64, 256, 1, 4.0f, 0.45f, 0.0f, launch_tile<true, 16, 128, 64, 4, 2, 4, 256>},
     {64, 64, 256, 2, 4.4f, 0.31f, 0.44f, launch_tile<true, 16, 64, 64, 2, 2, 4, 256>},
     {64, 32, 256, 2, 3.5f, 0.30f, 0.35f, launch_tile<true, 16, 64, 32, 4, 1, 4, 256>},
 };
@@ -749,7 +763,7 @@ constexpr Mx4Config kFp8Configs[] = {
     {160, 128, 256, 1, 4.0f, 1.40f, 0.0f, launch_tile<false, 16, 160, 128, 2, 4, 2, 256>},
     {128, 128, 128, 1, 4.8f, 0.50f, 0.0f, launch_tile<false, 32, 128, 128, 2, 4, 4, 128>},
     {160, 64, 256, 1, 4.8f, 0.68f, 0.0f, launch_tile<false, 16, 160, 64, 2, 4, 3, 256>},
-    {64, 64, 256, 1, 4.8f, 0.38f, 0.0f, launch_tile<false, 16, 64, 64, 2, 2, 3, 256>},
+    {64, 64, 256, 1, 4.0f, 0.38f, 0.0f, launch_tile<false, 16, 64, 64, 2, 2, 3, 256>},
     {64, 32, 256, 2, 3.8f, 0.31f, 0.42f, launch_tile<false, 16, 64, 32, 4, 1, 4, 256>},
 };
 constexpr int kCUs = 256;
