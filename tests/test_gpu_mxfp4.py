@@ -194,7 +194,8 @@ CONFIGS = [(1200, 9000, 384), (300, 30000, 1152), (300, 30000, 9344), (700, 9000
            (2325, 819, 384), (3776, 41, 14976), (2756, 67, 7552), (128, 4608, 3584), (52, 9542, 6784),
            (258, 689, 9984), (298, 285, 11904), (24, 426, 5504), (20, 20000, 2944), (1024, 5120, 27648),
            (2, 30000, 640), (1, 50000, 384), (1, 3584, 18944), (2, 100, 20480), (1, 7, 40960), (1, 24, 41088),
-           (16, 8192, 8192), (5, 3584, 3584)]
+           (16, 8192, 8192), (5, 3584, 3584),
+           (1, 5120, 27648), (2, 7168, 5120)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])

@@ -549,6 +549,11 @@ def _one_device(dev, *ts):
     return dev.index
 
 
+def _ld(t, name):
+    """Row stride of a 2-D tensor with contiguous rows."""
+    return t.shape[-1] or 1 if t.is_contiguous() else _rows(t, name)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -594,7 +599,7 @@ def mxfp4_quantize(A, codes=None, scales=None):
     idx = _one_device(A.device, codes, scales)
     if A.dtype != torch.float32 and A.dtype != torch.bfloat16:
         raise ValueError("A must be float32 or bfloat16")
-    lda = _rows(A, "A")
+    lda = _ld(A, "A")
     R, K = A.shape
     if K % 32:
         raise QRError("qr_mxfp4_quantize", -2, f"K={K} is not a multiple of 32")
@@ -616,7 +621,7 @@ def mx_dequantize(codes, scales, out=None, dtype=torch.bfloat16):
     elif out.shape != (R, K) or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out must be a bfloat16 or float32 tensor of the codes' rows and K")
     else:
-        ldo = _rows(out, "out")
+        ldo = _ld(out, "out")
     _call("qr_mx_dequantize", idx, codes.data_ptr(), scales.data_ptr(), R, K, fmt, out.data_ptr(), ldo,
           int(out.dtype == torch.bfloat16))
     return out
@@ -627,7 +632,7 @@ def _mx4_out(Y, like, M, N, dtype):
         return like.new_empty((M, N), dtype=dtype), N
     if Y.shape != (M, N) or Y.dtype != dtype:
         raise ValueError(f"Y must be {dtype} [{M}, {N}]")
-    return Y, max(_rows(Y, "Y"), N)
+    return Y, max(_ld(Y, "Y"), N)
 
 
 _mx4_ws = {}
@@ -682,7 +687,7 @@ def mxfp4_linear(X, Wq, sw, x="fp4", Y=None, ws=None):
         xfmt = 2
     else:
         raise ValueError(f"x must be 'fp4' or 'fp8', got {x!r}")
-    ldx = _rows(X, "X")
+    ldx = _ld(X, "X")
     M, K = X.shape
     N, Kw, wfmt = _mx_codes(Wq, sw, "Wq")
     if wfmt != 3 or Kw != K:
@@ -710,7 +715,7 @@ def block_norm_quant(Y, H, gamma, fmt, post_gamma=None, gate=None, res_scale=1.0
         raise ValueError(f"fmt must be one of {list(ACT)}, got {fmt!r}")
     if kind not in NORM:
         raise ValueError(f"kind must be one of {list(NORM)}")
-    ldy, ldh = _rows(Y, "Y"), _rows(H, "H")
+    ldy, ldh = _ld(Y, "Y"), _ld(H, "H")
     M, K = shape
     for t in (gamma, post_gamma, beta, post_beta):
         if t is not None and (t.dtype != torch.float32 or t.numel() != K or not t.is_contiguous()):
@@ -718,7 +723,7 @@ def block_norm_quant(Y, H, gamma, fmt, post_gamma=None, gate=None, res_scale=1.0
     ldgate = 0
     if gate is not None:
         if gate.dtype == torch.bfloat16 and gate.shape == shape:
-            ldgate = _rows(gate, "gate")
+            ldgate = _ld(gate, "gate")
         elif gate.dtype != torch.float32 or gate.shape != (K,) or not gate.is_contiguous():
             raise ValueError("gate must be float32 [K] or bfloat16 [M, K]")
     if Hout is None:
@@ -726,7 +731,7 @@ def block_norm_quant(Y, H, gamma, fmt, post_gamma=None, gate=None, res_scale=1.0
     elif Hout.shape != shape or Hout.dtype != torch.bfloat16:
         raise ValueError("Hout must be bfloat16 of Y's shape")
     else:
-        ldo = _rows(Hout, "Hout")
+        ldo = _ld(Hout, "Hout")
     if fmt == "bf16":
         codes, scales = _out(codes, Y, (M, K), torch.bfloat16, "codes"), None
     elif fmt == "int8" or fmt == "fp8":
@@ -750,7 +755,7 @@ def silu_mul_mx(G, U, fmt, codes=None, scales=None):
         raise ValueError("G and U must be bfloat16 of one shape")
     if fmt not in ("mxfp4", "mxfp8"):
         raise ValueError(f"fmt must be 'mxfp4' or 'mxfp8', got {fmt!r}")
-    ldg, ldu = _rows(G, "G"), _rows(U, "U")
+    ldg, ldu = _ld(G, "G"), _ld(U, "U")
     M, N = G.shape
     if N % 32:
         raise QRError("qr_silu_mul_mx", -2, f"N={N} is not a multiple of 32")

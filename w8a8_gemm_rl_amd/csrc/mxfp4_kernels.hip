@@ -730,11 +730,11 @@ hipError_t launch_tile(const Mx4Params& g, int splits, float* part, hipStream_t 
 }
 
 // X: bf16 tokens to quantize in the kernel (stride ldx), or NULL for codes in p.
-template <bool XFP4, bool FUSED, int NW, int KW>
+template <bool XFP4, bool FUSED, int NW, int KW, int D>
 hipError_t launch_decode(const Mx4Params& p, const uint16_t* X, int64_t ldx, hipStream_t st) {
   constexpr int rows = 16 * (NW / KW);
   const size_t lds = FUSED ? (size_t)(XFP4 ? p.M * p.K / 2 : p.M * p.K) + p.M * p.K / 32 : 0;
-  hipLaunchKernelGGL((mx4_decode_kernel<XFP4, FUSED, NW, KW, 4>), dim3((unsigned)((p.N + rows - 1) / rows)),
+  hipLaunchKernelGGL((mx4_decode_kernel<XFP4, FUSED, NW, KW, D>), dim3((unsigned)((p.N + rows - 1) / rows)),
                      dim3(64 * NW), lds, st, p, X, ldx);
   return hipGetLastError();
 }
@@ -843,8 +843,8 @@ hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const vo
   const bool fp4 = xfmt == kActMxFp4;
   const Mx4Plan plan = make_mx4_plan(M, N, K, fp4);
   if (plan.c) return plan.c->run(p, plan.splits, static_cast<float*>(ws), st);
-  return fp4 ? launch_decode<true, false, 8, 8>(p, nullptr, 0, st)
-             : launch_decode<false, false, 8, 8>(p, nullptr, 0, st);
+  return fp4 ? launch_decode<true, false, 8, 8, 4>(p, nullptr, 0, st)
+             : launch_decode<false, false, 8, 8, 4>(p, nullptr, 0, st);
 }
 
 size_t mx4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int xfmt) {
@@ -855,18 +855,22 @@ size_t mx4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int xfmt) {
 // One launch where the blocks' own quantization of the tokens costs less than a launch
 // for it (2.6 us): up to 16384 values (four tokens of the 7B hidden size: 6.8 against
 // 7.6 us on QKV; eight: 9.4 against 7.9), and for one or two tokens up to what fits the
-// LDS (7B down projection, one token: 10.5 against 13.7 us). Long rows with few blocks
-// split K over 16 waves; many rows (the stacked gate and up) take 32 rows a block, half
-// of K a wave (14.2 us; 20.4 with 16 rows over eight waves).
+// LDS (7B down projection, one token: 10.5 against 13.7 us).
 bool mx4_one_launch(int64_t M, int64_t K) {
   return K > 0 && M <= 16 && (M * K <= 16384 || (M <= 2 && M * K <= 40960));
 }
 
+// Many rows (the stacked gate and up) take 32 rows a block, half of K a wave (14.3 us; 17.1
+// with 16 rows over eight waves). Long rows whose 16-row tiles all find a CU split K over
+// 16 waves (7B down projection 10.4 against 11.3 us over eight; the 32B one, 320 tiles,
+// 24.0 against 20.5). Rows up to 4096 need no more than two pairs a wave in flight (7B QKV
+// 5.7 against 6.0 us).
 template <bool XFP4>
 hipError_t launch_fused(const Mx4Params& p, const uint16_t* X, int64_t ldx, hipStream_t st) {
-  if (p.N > 16 * 1024) return launch_decode<XFP4, true, 4, 2>(p, X, ldx, st);
-  if (p.K >= 8192) return launch_decode<XFP4, true, 16, 16>(p, X, ldx, st);
-  return launch_decode<XFP4, true, 8, 8>(p, X, ldx, st);
+  if (p.N > 16384) return launch_decode<XFP4, true, 4, 2, 4>(p, X, ldx, st);
+  if (p.K >= 8192 && p.N <= 16 * kCUs) return launch_decode<XFP4, true, 16, 16, 4>(p, X, ldx, st);
+  if (p.K <= 4096) return launch_decode<XFP4, true, 8, 8, 2>(p, X, ldx, st);
+  return launch_decode<XFP4, true, 8, 8, 4>(p, X, ldx, st);
 }
 
 // The workspace holds the product's partial sums, the token codes, then their scales
