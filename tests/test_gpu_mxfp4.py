@@ -582,3 +582,16 @@ def test_binding_refusals_on_device_tensors():
     buf = torch.zeros((4, 160), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(B.QRError):  # rows that overlap H's without being H's
         B.block_norm_quant(x, buf[:, :128], torch.ones(128, device=DEV), "mxfp4", Hout=buf[:, 32:])
+
+
+def test_outputs_whose_rows_share_memory_are_refused():
+    x = torch.zeros((4, 128), dtype=torch.bfloat16, device=DEV)
+    w, sw = B.mxfp4_quantize(torch.zeros((16, 128), device=DEV))
+    xq, sx = B.mxfp4_quantize(x)
+    row = torch.zeros((1, 16), dtype=torch.bfloat16, device=DEV)
+    for f in (lambda: B.mxfp4_linear(x, w, sw, Y=row.expand(4, 16)),
+              lambda: B.mxfp4_gemm(xq, sx, w, sw, Y=row.expand(4, 16)),
+              lambda: B.mx_dequantize(w, sw, out=torch.zeros((1, 128), device=DEV).expand(16, 128)),
+              lambda: B.block_norm_quant(x, x, torch.ones(128, device=DEV), "mxfp4", Hout=x[:1].expand(4, 128))):
+        with pytest.raises(B.QRError, match="ld[yo]=0|row stride"):
+            f()

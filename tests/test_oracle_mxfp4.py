@@ -222,3 +222,16 @@ def test_binding_refuses_host_tensors_and_bad_types():
               lambda: B.block_norm_quant(x, x, torch.ones(128), "mxfp4")):
         with pytest.raises(ValueError, match="HIP device"):
             f()
+
+
+def test_binding_passes_the_row_stride_of_an_output_as_it_is():
+    """A stride below N (an expanded row) reaches the library, which refuses it."""
+    import torch
+    from w8a8_gemm_rl_amd import binding as B
+
+    like = torch.zeros((1,), dtype=torch.bfloat16)
+    y = torch.zeros((1, 16), dtype=torch.bfloat16)
+    assert B._mx4_out(y.expand(4, 16), like, 4, 16, torch.bfloat16)[1] == 0
+    assert B._mx4_out(y, like, 1, 16, torch.bfloat16)[1] == 16
+    assert B._mx4_out(torch.zeros((4, 20), dtype=torch.bfloat16)[:, :16], like, 4, 16, torch.bfloat16)[1] == 20
+    assert B._mx4_out(torch.zeros((3, 0), dtype=torch.bfloat16), like, 3, 0, torch.bfloat16)[1] >= 0

@@ -632,7 +632,7 @@ def _mx4_out(Y, like, M, N, dtype):
         return like.new_empty((M, N), dtype=dtype), N
     if Y.shape != (M, N) or Y.dtype != dtype:
         raise ValueError(f"Y must be {dtype} [{M}, {N}]")
-    return Y, max(_ld(Y, "Y"), N)
+    return Y, _ld(Y, "Y")
 
 
 _mx4_ws = {}
