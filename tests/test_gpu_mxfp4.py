@@ -595,3 +595,14 @@ def test_outputs_whose_rows_share_memory_are_refused():
               lambda: B.block_norm_quant(x, x, torch.ones(128, device=DEV), "mxfp4", Hout=x[:1].expand(4, 128))):
         with pytest.raises(B.QRError, match="ld[yo]=0|row stride"):
             f()
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_block_norm_scales_of_rows_of_no_values_are_zero(fmt, kind):
+    for M in (3, 700):
+        z = torch.zeros((M, 0), dtype=torch.bfloat16, device=DEV)
+        s = torch.full((M,), 5.0, device=DEV)
+        h, q, _ = B.block_norm_quant(z, z, torch.ones(0, device=DEV), fmt, kind=kind, scales=s)
+        torch.cuda.synchronize()
+        assert h.shape == (M, 0) and q.shape == (M, 0) and bool((s == 0).all())

@@ -362,7 +362,8 @@ __global__ __launch_bounds__(256) void silu_mx_kernel(const uint16_t* __restrict
 template <int MAXC>
 void launch_rows(BlockNormArgs p, int kind, hipStream_t st) {
   constexpr int64_t kBlocks = (int64_t)1 << 21;  // per launch
-  const int nch = (int)(p.K >> 3), threads = ((nch + MAXC - 1) / MAXC + 63) & ~63;
+  const int nch = (int)(p.K >> 3), waves = ((nch + MAXC - 1) / MAXC + 63) >> 6;
+  const int threads = 64 * (waves > 0 ? waves : 1);
   p.inv_k = 1.0 / (double)p.K;
   for (p.row0 = 0; p.row0 < p.M; p.row0 += kBlocks) {
     const int64_t blocks = p.M - p.row0 < kBlocks ? p.M - p.row0 : kBlocks;
@@ -375,7 +376,8 @@ void launch_rows(BlockNormArgs p, int kind, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNormArgs& p, int kind, hipStream_t st) {
-  if (p.M == 0 || p.K == 0) return hipSuccess;
+  const bool per_token = p.fmt == kActInt8 || p.fmt == kActFp8;  // rows of no values have scale 0
+  if (p.M == 0 || (p.K == 0 && !per_token)) return hipSuccess;
   const int64_t nch = p.K >> 3;
   if (nch <= 1024 && p.M <= 512) launch_rows<1>(p, kind, st);
   else if (nch <= 2048 && (p.M < 2048 || nch < 256)) launch_rows<2>(p, kind, st);
