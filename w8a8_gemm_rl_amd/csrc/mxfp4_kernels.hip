@@ -664,9 +664,12 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
             *reinterpret_cast<uint2*>(so + (T * (j - j0) + lr) * LD + (T * i + 8 * q + 4 * lg) * 2) =
                 make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
           }
+      // lanes read what others of the wave wrote: LDS accesses of a wave are in order
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if ((ldy & 7) == 0) rows_out(j0, std::integral_constant<int, 8>{});
       else if ((ldy & 1) == 0) rows_out(j0, std::integral_constant<int, 2>{});
       else rows_out(j0, std::integral_constant<int, 1>{});
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     return;
   }
