@@ -530,7 +530,7 @@ def linear_fused_noalloc(X, act_mult, Wq, scale_w, qt, Y=None):
 def _call(fn, idx, *args):
     """Call library function `fn` on the current stream of device `idx`, made current."""
     f = getattr(_lib or lib(), fn)
-    if idx == torch.cuda.current_device():
+    if idx == torch._C._cuda_getDevice():
         st = f(*args, torch._C._cuda_getCurrentRawStream(idx))
     else:
         with torch.cuda.device(idx):
