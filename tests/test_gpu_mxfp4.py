@@ -458,6 +458,60 @@ def test_silu_mul_mx(M, N, fmt):
     assert np.array_equal(codes_np(q), _bytes(codes, fmt))
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_silu_mul_mx_of_every_gate_value(fmt):
+    """All 65536 bf16 gates in a block each, beside ordinary ones: codes and scales of the float64
+    form, NaN blocks where it is not finite."""
+    g = np.random.default_rng(4)
+    G = F.f32_to_bf16_bits(g.standard_normal((512, 4096), dtype=np.float32))
+    U = F.f32_to_bf16_bits(g.standard_normal((512, 4096), dtype=np.float32) * np.float32(3.0))
+    G[:, 5::32] = np.arange(65536, dtype=np.uint16).reshape(512, 128)
+    with np.errstate(all="ignore"):
+        a = O.silu_mul(G, U)
+    bad = ~np.isfinite(a.reshape(512, 128, 32)).all(axis=2)
+    codes, X, _ = _quant(np.where(np.repeat(bad, 32, axis=1), np.float32(0), a), fmt)
+    q, s = B.silu_mul_mx(to_dev_bf16(G), to_dev_bf16(U), fmt)
+    torch.cuda.synchronize()
+    assert 200 < bad.sum() < 1000
+    assert np.array_equal(_rowmajor(s, 512, 4096), np.where(bad, 255, X + 127).astype(np.uint8))
+    # codes of a value that the NaN block's zero stands for: zero, of either sign
+    got, want = codes_np(q), _bytes(codes, fmt)
+    ok = ~np.repeat(bad, 16 if fmt == "mxfp4" else 32, axis=1)
+    assert np.array_equal(got[ok], want[ok]) and not got[~ok].any()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_silu_mul_mx_of_values_on_code_boundaries(fmt):
+    """Gates so large that fl32(SiLU(g) u) = g u: products on, and a bf16 step beside, the midpoints
+    between codes and the tops where the scale changes; and blocks below 2^-100."""
+    top, mids = (6.0, [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) if fmt == "mxfp4" else \
+        (448.0, [2.0 ** -10, 3 * 2.0 ** -10, 1.0625, 17.0, 31.0, 232.0, 432.0])
+
+    def step(v, d):  # the bf16 number d steps further from zero
+        return F.bf16_bits_to_f32((F.f32_to_bf16_bits(v).astype(np.int32) + d).astype(np.uint16))
+
+    rows = []
+    for x in (-109, -3, 0, 9):
+        for sign in (1.0, -1.0):
+            v = np.float32(sign) * np.float32(mids)
+            b = np.zeros(64, np.float32)
+            b[:21] = np.concatenate([v, step(v, 1), step(v, -1)])
+            b[31] = top
+            b[32:53], b[63:] = b[:21], step(np.float32([top]), 1)  # the next scale
+            rows.append(b * np.float32(2.0 ** x))
+    v = np.stack(rows)
+    G = np.full(v.shape, 32.0, np.float32)
+    Gb, Ub = F.f32_to_bf16_bits(G), F.f32_to_bf16_bits(v / np.float32(32.0))
+    assert np.array_equal(F.bf16_bits_to_f32(Ub) * np.float32(32.0), v)
+    a = O.silu_mul(Gb, Ub)
+    assert np.array_equal(a, v)
+    codes, X, _ = _quant(a, fmt)
+    q, s = B.silu_mul_mx(to_dev_bf16(Gb), to_dev_bf16(Ub), fmt)
+    torch.cuda.synchronize()
+    assert np.array_equal(_rowmajor(s, *v.shape), (X + 127).astype(np.uint8))
+    assert np.array_equal(codes_np(q), _bytes(codes, fmt))
+
+
 # ---------------------------------------------------------------------------- together
 
 class Layer:

@@ -322,7 +322,22 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return (float)(((double)g * (double)u) * r);
 }
 
-// Rows [row0, row0 + w.rows), two chunks of eight outputs a thread, block-wise codes.
+// The same in fp32 for g >= -80, off by less than 2^-21.3 of it where nothing underflows
+// (the sigmoid by at most 2^-22.4, the largest error over all bf16 g; two products):
+// exp(-g) = 2^(-g c) (1 - g d) with c the 15 leading bits of log2(e), so that g c is exact,
+// and d = (log2(e) - c) ln 2, |g d| < 2^-11.3.
+__device__ __forceinline__ float silu_mul_fast(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(g * -1.44268798828125f) * fmaf(g, -4.888495152e-06f, 1.0f);
+  return (g * __builtin_amdgcn_rcpf(1.0f + e)) * u;
+}
+
+// Rows [row0, row0 + w.rows), eight outputs a thread, block-wise codes: those of silu_mul's
+// values. Rounding to codes is monotone, and so is the scale in the block's maximum: where
+// the values times 1 - 2^-19 and times 1 + 2^-19 give the same codes and scale, so does
+// silu_mul's value, which the fp32 form comes closer to than 2^-20 (2^-21.3, and the
+// roundings to fp32 of that value and of the product with the factor). Else (one wave in 60
+// for E4M3 codes), or if a block is not finite or its maximum below 2^-100, or a g < -80, the
+// wave evaluates silu_mul.
 template <bool FP4>
 __global__ __launch_bounds__(256) void silu_mx_kernel(const uint16_t* __restrict__ G,
                                                       const uint16_t* __restrict__ U, int64_t M,
@@ -330,33 +345,38 @@ __global__ __launch_bounds__(256) void silu_mx_kernel(const uint16_t* __restrict
                                                       uint8_t* __restrict__ codes,
                                                       uint8_t* __restrict__ scales, int64_t row0,
                                                       ChunkWalk w) {
-  constexpr int NU = 2;
-  const uint32_t total = w.rows * w.cpr, i0 = w.first(NU), nch = (uint32_t)(N >> 3);
-  uint4 g[NU], u[NU];
-  int64_t row[NU];
-  uint32_t c[NU];
-  bool live[NU];
-#pragma unroll
-  for (int j = 0; j < NU; ++j) {
-    const uint32_t i = i0 + j * 256u, r = w.row(i);
-    row[j] = row0 + r;
-    c[j] = i - r * w.cpr;
-    live[j] = i < total && c[j] < nch;
-    g[j] = u[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (live[j]) {
-      g[j] = *reinterpret_cast<const uint4*>(G + row[j] * ldg + 8 * c[j]);
-      u[j] = *reinterpret_cast<const uint4*>(U + row[j] * ldu + 8 * c[j]);
-    }
+  constexpr float kLow = 1.0f - 0x1p-19f, kHigh = 1.0f + 0x1p-19f;
+  const uint32_t i = w.first(1), r = w.row(i), c = i - r * w.cpr;
+  const int64_t row = row0 + r;
+  const bool live = i < w.rows * w.cpr && c < (uint32_t)(N >> 3);
+  uint4 g = make_uint4(0u, 0u, 0u, 0u), u = g;
+  if (live) {
+    g = *reinterpret_cast<const uint4*>(G + row * ldg + 8 * c);
+    u = *reinterpret_cast<const uint4*>(U + row * ldu + 8 * c);
   }
+  float a[8], b[8], t[8], least = 0.0f;
+  bf16x8(g, a);
+  bf16x8(u, b);
 #pragma unroll
-  for (int j = 0; j < NU; ++j) {
-    float a[8], b[8];
-    bf16x8(g[j], a);
-    bf16x8(u[j], b);
+  for (int e = 0; e < 8; ++e) {
+    t[e] = silu_mul_fast(a[e], b[e]);
+    least = fminf(least, a[e]);
+  }
+  const uint32_t m = mx_block_max(t);  // a NaN or an infinity is above every number
+  const float amax = __uint_as_float(m);
+  uint32_t sb = mx_scale_byte<FP4>(__float_as_uint(amax * kHigh));
+  const float inv = mx_inv_scale(sb);
+  uint2 q = mx_codes8_times<FP4>(t, inv * kLow);
+  const uint2 high = mx_codes8_times<FP4>(t, inv * kHigh);
+  const bool sure = m >= 0x0d800000u && m < 0x7f000000u && least >= -80.0f && q.x == high.x && q.y == high.y &&
+                    sb == mx_scale_byte<FP4>(__float_as_uint(amax * kLow));
+  if (__builtin_amdgcn_ballot_w64(live && !sure) != 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) a[e] = silu_mul(a[e], b[e]);
-    mx_store_row8<FP4>(a, live[j], row[j], M, c[j], N, codes, scales);
+    sb = mx_block_scale<FP4>(a);
+    q = mx_codes8<FP4>(a, sb);
   }
+  mx_store_codes8<FP4>(q, live ? sb : 0u, live, row, M, c, N, codes, scales);
 }
 
 template <int MAXC>
@@ -390,7 +410,7 @@ hipError_t launch_silu_mx(const void* G, const void* U, int64_t M, int64_t N, in
   const uint16_t *g = static_cast<const uint16_t*>(G), *u = static_cast<const uint16_t*>(U);
   uint8_t* q = static_cast<uint8_t*>(codes);
   const dim3 b(256);
-  return chunk_launches(M, ((N + 127) >> 7) << 4, 2, [&](int64_t r, ChunkWalk w, dim3 gr) {
+  return chunk_launches(M, ((N + 127) >> 7) << 4, 1, [&](int64_t r, ChunkWalk w, dim3 gr) {
     if (fmt == kActMxFp4) hipLaunchKernelGGL(silu_mx_kernel<true>, gr, b, 0, st, g, u, M, N, ldg, ldu, q, scales, r, w);
     else hipLaunchKernelGGL(silu_mx_kernel<false>, gr, b, 0, st, g, u, M, N, ldg, ldu, q, scales, r, w);
   });

@@ -71,24 +71,25 @@ __device__ __forceinline__ uint32_t abs_bits_max8(const float* v) {
   return m;
 }
 
-// Scale byte of the 32-element block that lanes 4 j .. 4 j + 3 hold, eight values
-// each (every lane of the four gets it). Integer maximum of the sign-cleared bits:
+// Bits of max |v| and the scale byte of the 32-element block that lanes 4 j .. 4 j + 3
+// hold, eight values each (every lane of the four gets them). Integer maximum of the sign-cleared bits:
 // the order of non-negative floats, with NaN above infinity above every number.
-template <bool FP4>
-__device__ __forceinline__ uint32_t mx_block_scale(const float* v) {
+__device__ __forceinline__ uint32_t mx_block_max(const float* v) {
   uint32_t m = abs_bits_max8(v);
   uint32_t o = (uint32_t)__shfl_xor((int)m, 1, 64);
   m = o > m ? o : m;
   o = (uint32_t)__shfl_xor((int)m, 2, 64);
-  m = o > m ? o : m;
-  return mx_scale_byte<FP4>(m);
+  return o > m ? o : m;
 }
 
-// Codes of eight values of a block with scale byte sb (zero codes in a NaN block).
 template <bool FP4>
-__device__ __forceinline__ uint2 mx_codes8(const float* v, uint32_t sb) {
-  if (sb == 255u) return make_uint2(0u, 0u);
-  const float inv = mx_inv_scale(sb);
+__device__ __forceinline__ uint32_t mx_block_scale(const float* v) {
+  return mx_scale_byte<FP4>(mx_block_max(v));
+}
+
+// Codes of eight values times inv.
+template <bool FP4>
+__device__ __forceinline__ uint2 mx_codes8_times(const float* v, float inv) {
   float t[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) t[e] = v[e] * inv;
@@ -96,24 +97,37 @@ __device__ __forceinline__ uint2 mx_codes8(const float* v, uint32_t sb) {
   else return mx_fp8_codes8(t);
 }
 
-// Stores the codes and scale bytes of a row's values when every lane holds eight
-// consecutive ones: chunk c (values 8 c .. 8 c + 7) of row `row`, c ascending with
+// Codes of eight values of a block with scale byte sb (zero codes in a NaN block).
+template <bool FP4>
+__device__ __forceinline__ uint2 mx_codes8(const float* v, uint32_t sb) {
+  if (sb == 255u) return make_uint2(0u, 0u);
+  return mx_codes8_times<FP4>(v, mx_inv_scale(sb));
+}
+
+// Stores the codes and scale bytes of a row when every lane holds those of eight
+// consecutive values: chunk c (values 8 c .. 8 c + 7) of row `row`, c ascending with
 // the lane and c % 16 == lane % 16. `live` lanes hold values (whole blocks of 32),
 // the others zeros. A panel's four scale bytes are stored as one word; the bytes of a
 // last panel that no block owns come out zero.
 template <bool FP4>
-__device__ __forceinline__ void mx_store_row8(const float* v, bool live, int64_t row, int64_t R,
-                                              int64_t c, int64_t K, uint8_t* codes, uint8_t* scales) {
-  const uint32_t sb = mx_block_scale<FP4>(v);
+__device__ __forceinline__ void mx_store_codes8(uint2 q, uint32_t sb, bool live, int64_t row, int64_t R,
+                                                int64_t c, int64_t K, uint8_t* codes, uint8_t* scales) {
   const int lane = threadIdx.x & 63;
   uint32_t w = sb << (8 * ((lane >> 2) & 3));
   w |= (uint32_t)__shfl_xor((int)w, 4, 64);
   w |= (uint32_t)__shfl_xor((int)w, 8, 64);
   if (!live) return;
-  const uint2 q = mx_codes8<FP4>(v, sb);
   if constexpr (FP4) *reinterpret_cast<uint32_t*>(codes + row * (K >> 1) + 4 * c) = q.x;
   else *reinterpret_cast<uint2*>(codes + row * K + 8 * c) = q;
   if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + ((c >> 4) * R + row) * 4) = w;
+}
+
+// The same from the lanes' values.
+template <bool FP4>
+__device__ __forceinline__ void mx_store_row8(const float* v, bool live, int64_t row, int64_t R,
+                                              int64_t c, int64_t K, uint8_t* codes, uint8_t* scales) {
+  const uint32_t sb = mx_block_scale<FP4>(v);
+  mx_store_codes8<FP4>(mx_codes8<FP4>(v, sb), sb, live, row, R, c, K, codes, scales);
 }
 
 // Elementwise passes over rows of 16-byte-aligned chunks of eight values: a block of 256
