@@ -327,7 +327,8 @@ int qr_mxfp4_quantize(const void* A, int64_t R, int64_t K, int64_t lda, int src_
 /*
  * qr_mx_dequantize -- the values that block-wise codes stand for,
  *   out[r, k] = element(codes[r, k]) * 2^X(r, k / 32)
- * (exact in bf16 and fp32 up to overflow to infinity; scale byte 255 gives NaN).
+ * (exact in fp32 and bf16 up to overflow to infinity, but for bf16 below 2^-133, which
+ * E4M3 elements with X < -124 can reach: nearest even; scale byte 255 gives NaN).
  *
  *   fmt      QR_ACT_MXFP4 (codes [R, K/2]) or QR_ACT_MXFP8 (codes [R, K]).
  *   out      [R, ldo] bf16 (out_bf16 = 1) or fp32 (written), rows on 16-byte
@@ -414,10 +415,11 @@ int qr_block_norm_quant(const void* Y, int64_t ldy, const void* H, int64_t ldh, 
                         int fmt, void* Hout, int64_t ldo, void* codes, void* scales, void* stream);
 
 /*
- * qr_silu_mul_mx -- the input of an MXFP4 down projection: SiLU(gate) * up as
- * qr_silu_mul_quant evaluates it, quantized block-wise to fmt (QR_ACT_MXFP4 or
- * QR_ACT_MXFP8). The block scales are powers of two, so there is no act_mult: a
- * UAQ factor belongs into the weights of the other side.
+ * qr_silu_mul_mx -- the input of an MXFP4 down projection: SiLU(gate) * up,
+ *   a = fl32(g u / (1 + exp(-g))), relative error below 2^-40 before that rounding,
+ * quantized block-wise to fmt (QR_ACT_MXFP4 or QR_ACT_MXFP8). A block whose a is not
+ * finite is a NaN block. The block scales are powers of two, so there is no act_mult:
+ * a UAQ factor belongs into the weights of the other side.
  *
  *   G, U     [M, ldg] / [M, ldu] bf16 (read), strides multiples of 8.
  *   N        multiple of 32. codes [M, N/2] or [M, N], scales

@@ -522,7 +522,7 @@ def linear_fused_noalloc(X, act_mult, Wq, scale_w, qt, Y=None):
 # ----------------------------------------------------------------------------
 # MXFP4 operators and block norms. Decode calls are a few microseconds on the GPU, so
 # the marshalling here is kept short (one-token mxfp4_linear: 10.8 us of host time with
-# this module's general helpers, 6.6 with these): the stream as a plain handle, no
+# this module's general helpers, 7 with these): the stream as a plain handle, no
 # device switch where the tensors' device is current, scratch from torch's allocator
 # (stream-ordered; a graph's own pool under capture, so captured graphs never share it).
 # ----------------------------------------------------------------------------

@@ -4,12 +4,13 @@
 //
 //   Y[m,n] = sum_b 2^(Xx[m,b] + Xw[n,b]) sum_{k in block b} x[m,k] w[n,k]
 //
-// runs on v_mfma_scale_f32_16x16x128_f8f6f4 with weights on operand A (E2M1) and
-// tokens on operand B (E2M1 or E4M3). Operand layouts (measured): lane l holds row
-// l % 16; with g = l / 16, E2M1: elements [32 g, 32 g + 32) of the 128, 16 bytes;
-// E4M3: elements [16 g, 16 g + 16) and [64 + 16 g, 64 + 16 g + 16); in both the
-// lane's scale byte is that of block g. Register i of the result is weight row
-// 4 g + i, token l % 16.
+// runs on v_mfma_scale_f32_16x16x128_f8f6f4 and v_mfma_scale_f32_32x32x64_f8f6f4 with
+// weights on operand A (E2M1) and tokens on operand B (E2M1 or E4M3). Operand layouts of
+// the T x T x KI instruction (measured): lane l holds row l % T; with g = l / T, E2M1:
+// elements [32 g, 32 g + 32) of the KI, 16 bytes; E4M3: elements [16 g, 16 g + 16) and
+// [KI / 2 + 16 g, KI / 2 + 16 g + 16); in both the lane's scale byte is that of block g.
+// Register 4 q + r of the result is weight row 8 q + 4 g + r, token l % T. On operands that
+// stay in registers E2M1 x E2M1 reaches 6.6 - 7.1 PFLOP/s, E2M1 x E4M3 4.0.
 #include <type_traits>
 
 #include "qr_copy.h"
@@ -147,7 +148,9 @@ __device__ __forceinline__ void mx4_store4(const Mx4Params& p, int64_t m, int64_
   }
 }
 
-// Few tokens: a weight stream. A block owns 16 weight rows and up to 16 tokens; its NW
+// Few tokens: a weight stream, bound by the time to get it going and then by memory (one
+// token, fused: 7B QKV, 8.8 MB of weights and scales, 5.7 us; 7B down, 36 MB, 10.4 us, 3.5
+// TB/s; an empty kernel 2.6 us). A block owns 16 weight rows and up to 16 tokens; its NW
 // waves take the 256-element pairs of panels of K in turn (a row's pair is one 128-byte
 // line), weights straight from memory to registers with D pairs a wave in flight, and
 // the waves' partial sums are added in a fixed order. FUSED: the block first quantizes
@@ -286,6 +289,16 @@ __global__ __launch_bounds__(64 * NW) void mx4_decode_kernel(const Mx4Params p,
 // Rows past N or M are copied as zeros and not stored. With splits > 1 a block takes one
 // contiguous part of its tile's stages and writes fp32 partial sums, which
 // mx4_sum_kernel adds in a fixed order.
+//
+// Stacked 7B gate and up, 75 MB of codes and scales in and out at 33 E4M3 tokens: 15.4 us,
+// 4.9 TB/s, what a copy reaches. At 256 E2M1 tokens 93 MB take 26 us: 237 tiles of
+// 160 x 256, one round. The 32B gate at 4096 E2M1 tokens: 295 - 310 us, 3.8 - 3.9 PFLOP/s.
+// There, on 256 x 256 tiles, 20 stages in seven rounds, the products alone take 160 us (the
+// clock falls to 1.93 GHz), a fragment's LDS reads alone 164, the copies alone 193 (20 bytes
+// a clock and CU; 127 from the L2), any two together 205, all three 250; filling the ring
+// and storing the outputs add 35 - 50. Measured slower there: a third operand buffer with
+// refills a step earlier, 64-byte rows with deeper rings, four waves of 128 x 128, wave
+// priorities, non-temporal weight copies, other groupings of tiles.
 // ---------------------------------------------------------------------------
 // One copy of LANES lanes' 16 bytes (a power of two), exec being all ones before and after.
 template <int LANES>
@@ -687,7 +700,8 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
 }
 
 // Sum of the K splits' partial sums ([splits][M][N up to a multiple of 4]), four
-// channels a thread, in the order of the splits.
+// channels a thread, in the order of the splits: 3 us and the partial sums' write and read,
+// which the planner counts.
 __global__ __launch_bounds__(256) void mx4_sum_kernel(const float* __restrict__ part, int splits,
                                                       const Mx4Params p) {
   const int64_t n4 = (p.N + 3) & ~(int64_t)3, q = n4 >> 2;
