@@ -660,3 +660,75 @@ def test_block_norm_scales_of_rows_of_no_values_are_zero(fmt, kind):
         h, q, _ = B.block_norm_quant(z, z, torch.ones(0, device=DEV), fmt, kind=kind, scales=s)
         torch.cuda.synchronize()
         assert h.shape == (M, 0) and q.shape == (M, 0) and bool((s == 0).all())
+
+
+# ---------------------------------------------------------------------------- sizes past 32 bits and one launch
+
+def _rows_in_zeros(R, K, at, seed):
+    """bf16 [R, K] of zeros but for the rows `at`, and those rows."""
+    rows = to_dev_bf16(_acts(len(at), K, seed))
+    A = torch.zeros((R, K), dtype=torch.bfloat16, device=DEV)
+    A[torch.tensor(at, device=DEV)] = rows
+    return A, rows
+
+
+def test_quantize_and_dequantize_in_several_launches():
+    """2^30 chunks of eight values and some rows more: 17 GB of tokens, codes past 2^32 bytes."""
+    K, R = 8192, (1 << 20) + 5
+    at = [0, 7, (1 << 19) + 1, (1 << 20) - 1, 1 << 20, R - 1]
+    A, rows = _rows_in_zeros(R, K, at, 3)
+    q, s = B.mxfp4_quantize(A)
+    q0, s0 = B.mxfp4_quantize(rows)
+    i = torch.tensor(at, device=DEV)
+    assert torch.equal(q[i], q0) and torch.equal(s[:, i], s0)
+    rest = torch.ones(R, dtype=torch.bool, device=DEV)
+    rest[i] = False
+    assert not bool((q.view(torch.int64).any(1) & rest).any()) and not bool((s.any(2).any(0) & rest).any())
+    A.fill_(1.0)
+    B.mx_dequantize(q, s, out=A)
+    assert torch.equal(A[i], B.mx_dequantize(q0, s0))
+    assert not bool((A.view(torch.int64).any(1) & rest).any())
+
+
+def test_silu_in_several_launches():
+    N, M = 8192, (1 << 20) + 3
+    at = [1, (1 << 20) - 1, 1 << 20, M - 1]
+    G, rows = _rows_in_zeros(M, N, at, 5)
+    q, s = B.silu_mul_mx(G, G, "mxfp4")
+    q0, s0 = B.silu_mul_mx(rows, rows, "mxfp4")
+    i = torch.tensor(at, device=DEV)
+    assert torch.equal(q[i], q0) and torch.equal(s[:, i], s0)
+    rest = torch.ones(M, dtype=torch.bool, device=DEV)
+    rest[i] = False
+    assert not bool((q.view(torch.int64).any(1) & rest).any())
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mxfp4"])
+def test_block_norm_in_several_launches(fmt):
+    """2^21 rows a launch, and three more."""
+    M, K = (1 << 21) + 3, 64
+    g = torch.Generator(device=DEV).manual_seed(2)
+    Y = torch.randn((M, K), dtype=torch.float32, device=DEV, generator=g).bfloat16()
+    gamma = torch.rand(K, device=DEV, generator=g) + 0.5
+    h, q, s = B.block_norm_quant(Y, Y, gamma, fmt, gamma)
+    for lo in (0, (1 << 21) - 40, M - 60):
+        y = Y[lo:lo + 60].contiguous()
+        h0, q0, s0 = B.block_norm_quant(y, y, gamma, fmt, gamma)
+        assert torch.equal(h[lo:lo + 60], h0) and torch.equal(q[lo:lo + 60], q0)
+        assert torch.equal(s[lo:lo + 60] if fmt == "int8" else s[:, lo:lo + 60], s0)
+
+
+def test_gemm_output_past_32_bit_offsets():
+    """5.6 GB of output; rows and columns at its ends against float64. bf16 rounding 2^-8, and four
+    exact block sums added in fp32."""
+    M, N, K = 70001, 40000, 128
+    x = to_dev_bf16(_acts(M, K, 8))
+    w = to_dev_f32(I.weights(N, K, 0.02, seed=9))
+    (xq, sx), (wq, sw) = B.mxfp4_quantize(x), B.mxfp4_quantize(w)
+    Y = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV)
+    B.mxfp4_gemm(xq, sx, wq, sw, Y=Y)
+    xv, wv = (B.mx_dequantize(c, e, dtype=torch.float32).double() for c, e in ((xq, sx), (wq, sw)))
+    for a in (slice(0, 40), slice(35000, 35040), slice(M - 40, M)):
+        for b in (slice(0, 50), slice(N - 50, N)):
+            want, mag = xv[a] @ wv[b].t(), xv[a].abs() @ wv[b].abs().t()
+            assert bool(((Y[a, b].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * mag).all())
