@@ -732,3 +732,27 @@ def test_gemm_output_past_32_bit_offsets():
         for b in (slice(0, 50), slice(N - 50, N)):
             want, mag = xv[a] @ wv[b].t(), xv[a].abs() @ wv[b].abs().t()
             assert bool(((Y[a, b].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * mag).all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K,pad", [(2100, 9000, 512, 0), (2100, 9001, 640, 7), (1030, 37888, 256, 0), (530, 37890, 1280, 2),
+                                       (2600, 4608, 3584, 0), (8200, 4608, 128, 8), (300, 70000, 384, 1),
+                                       (4200, 30000, 256, 0)])
+def test_gemm_of_several_rounds_of_tiles(M, N, K, pad, fmt):
+    """More tiles than CUs, so that blocks take several, with whole and partial last stages and
+    tiles; every output against float64."""
+    x = to_dev_bf16(_acts(M, K, M + K))
+    xq, sx = B.mxfp4_quantize(x) if fmt == "mxfp4" else B.block_norm_quant(
+        x, x, torch.ones(K, device=DEV), "mxfp8")[1:]
+    wq, sw = B.mxfp4_quantize(to_dev_f32(I.weights(N, K, 0.02, seed=K)))
+    raw = torch.full((M, N), 7.0, device=DEV)
+    wide = torch.full((M, N + pad), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.mxfp4_gemm(xq, sx, wq, sw, out="raw", Y=raw)
+    B.mxfp4_gemm(xq, sx, wq, sw, Y=wide[:, :N])
+    xv, wv = (B.mx_dequantize(c, e, dtype=torch.float32).double() for c, e in ((xq, sx), (wq, sw)))
+    rel = (K / 32 + 64) * 2.0 ** -23 + (2.0 ** -12 if fmt == "mxfp8" else 0.0)
+    for m in range(0, M, 1024):
+        a = slice(m, min(m + 1024, M))
+        assert bool(((raw[a].double() - xv[a] @ wv.t()).abs() <= rel * (xv[a].abs() @ wv.abs().t()) + 1e-30).all())
+    assert torch.equal(wide[:, :N], raw.bfloat16())
+    assert bool((wide[:, N:] == 7.0).all())

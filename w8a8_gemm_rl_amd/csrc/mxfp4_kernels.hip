@@ -292,11 +292,11 @@ __global__ __launch_bounds__(64 * NW) void mx4_decode_kernel(const Mx4Params p,
 //
 // Stacked 7B gate and up, 75 MB of codes and scales in and out at 33 E4M3 tokens: 15.4 us,
 // 4.9 TB/s, what a copy reaches. At 256 E2M1 tokens 93 MB take 26 us: 237 tiles of
-// 160 x 256, one round. The 32B gate at 4096 E2M1 tokens: 295 - 310 us, 3.8 - 3.9 PFLOP/s.
+// 160 x 256, one round. The 32B gate at 4096 E2M1 tokens: 275 - 285 us, 4.1 - 4.2 PFLOP/s.
 // There, on 256 x 256 tiles, 20 stages in seven rounds, the products alone take 160 us (the
 // clock falls to 1.93 GHz), a fragment's LDS reads alone 164, the copies alone 193 (20 bytes
 // a clock and CU; 127 from the L2), any two together 205, all three 250; filling the ring
-// and storing the outputs add 35 - 50. Measured slower there: a third operand buffer with
+// and storing the outputs add 25 - 35. Measured slower there: a third operand buffer with
 // refills a step earlier, 64-byte rows with deeper rings, four waves of 128 x 128, wave
 // priorities, non-temporal weight copies, other groupings of tiles.
 // ---------------------------------------------------------------------------
@@ -317,6 +317,8 @@ __device__ __forceinline__ void dma_lanes(uint32_t lds_addr, uint32_t vo, __amdg
         : : "s"(lds_addr), "v"(vo), "s"(r), "s"(((uint64_t)1 << (LANES & 63)) - 1) : "memory", "m0");
 #pragma clang diagnostic pop
 }
+
+constexpr int kCUs = 256;
 
 struct Mx4TileParams {
   Mx4Params g;
@@ -347,7 +349,15 @@ struct Mx4Mfma<32> {
   }
 };
 
-template <bool XFP4, int T, int BN, int BM, int WN, int WM, int S, int KS>
+// Whether a slot of the ring can hold a token fragment of each wave's outputs.
+template <bool XFP4, int T, int BN, int BM, int WN, int WM, int KS>
+struct Mx4Ahead {
+  static constexpr int NW = WN * WM, RA = KS / 2, RB = XFP4 ? KS / 2 : KS;
+  static constexpr int IA = (BN * RA / 1024 + NW - 1) / NW * NW, IB = (BM * RB / 1024 + NW - 1) / NW * NW;
+  static constexpr bool value = (IA + IB) * 1024 + KS / 128 * 2048 >= NW * T * (BN / WN * 2 + 16);
+};
+
+template <bool XFP4, int T, int BN, int BM, int WN, int WM, int S, int KS, bool AHEAD>
 __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4TileParams p) {
   using MF = Mx4Mfma<T>;
   using acc_t = typename MF::acc_t;
@@ -371,17 +381,20 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
 
   const int64_t N = p.g.N, M = p.g.M, K = p.g.K;
-  // neighbouring tiles on one XCD; groups of up to 8 token tiles share weight tiles
-  const int G8 = gridDim.x & ~7;
-  int b = blockIdx.x;
-  if (b < G8) b = (b & 7) * (G8 >> 3) + (b >> 3);
-  const int tiles = p.tiles_m * p.tiles_n;
-  const int split = b / tiles;
-  b -= split * tiles;
-  const int grp = b / (8 * p.tiles_n), m0 = grp * 8;
-  const int gm = p.tiles_m - m0 < 8 ? p.tiles_m - m0 : 8;
-  b -= m0 * p.tiles_n;
-  const int tm = m0 + b % gm, tn = b / gm;
+  // An XCD takes one contiguous part of the tiles, each of its blocks every `step`-th of
+  // that; groups of up to 8 token tiles share weight tiles.
+  const int tiles = p.tiles_m * p.tiles_n, total = tiles * p.splits, xcd = blockIdx.x & 7;
+  const int end = (int)((int64_t)total * (xcd + 1) / 8), step = gridDim.x >> 3;
+  int cur = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+  if (cur >= end) return;
+  const int split = cur / tiles;  // blocks of several tiles: one split
+  auto locate = [&](int b, int& tm, int& tn) {
+    b -= split * tiles;
+    const int m0 = b / (8 * p.tiles_n) * 8, gm = p.tiles_m - m0 < 8 ? p.tiles_m - m0 : 8;
+    b -= m0 * p.tiles_n;
+    tm = __builtin_amdgcn_readfirstlane(m0 + b % gm);
+    tn = __builtin_amdgcn_readfirstlane(b / gm);
+  };
   const int ks0 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.stages * split / p.splits));
   const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)p.stages * (split + 1) / p.splits)) - ks0;
 
@@ -392,14 +405,19 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
   const int64_t ra = K >> 1, rb = XFP4 ? K >> 1 : K;  // bytes per row
   const uint32_t spw = (uint32_t)(N * 4), spx = (uint32_t)(M * 4);
   const uint32_t np = (uint32_t)(K >> 7);
-  const __amdgpu_buffer_rsrc_t rw =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.Wq, (short)0, (int)(uint32_t)(N * ra), kBufWord3);
-  const __amdgpu_buffer_rsrc_t rx =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.Xq, (short)0, (int)(uint32_t)(M * rb), kBufWord3);
-  const __amdgpu_buffer_rsrc_t rsw =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.sw, (short)0, (int)(np * spw), kBufWord3);
-  const __amdgpu_buffer_rsrc_t rsx =
-      __builtin_amdgcn_make_buffer_rsrc((void*)p.g.sx, (short)0, (int)(np * spx), kBufWord3);
+  // What the copies read: buffers that begin at the tile's first rows and end with the
+  // arrays, so that rows past them come as zeros.
+  __amdgpu_buffer_rsrc_t rw, rx, rs;
+  const bool sw_w = (wid * SL / 64 & 1) == 0;  // the wave copies weights' scales
+  auto copy_from = [&](int tm, int tn) {
+    auto part = [](const uint8_t* a, int64_t from, int64_t bytes) {
+      return __builtin_amdgcn_make_buffer_rsrc((void*)(a + from), (short)0, (int)(uint32_t)(bytes - from), kBufWord3);
+    };
+    rw = part(p.g.Wq, tn * BN * ra, N * ra);
+    rx = part(p.g.Xq, tm * BM * rb, M * rb);
+    if (sw_w) rs = part(p.g.sw, tn * BN * 4, (int64_t)np * spw);
+    else rs = part(p.g.sx, tm * BM * 4, (int64_t)np * spx);
+  };
 
   // Copies: instruction i of an operand fills LDS lines 8 i .. 8 i + 7; lane l the
   // physical chunk l % 8 of line 8 i + l / 8.
@@ -423,23 +441,20 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
   for (int i = 0; i < NA; ++i) {
     int r, c;
     place(wid * NA + i, RA, r, c);
-    const int64_t row = (int64_t)tn * BN + r;
-    oa[i] = ((r < BN && row < N) ? (uint32_t)(row * ra + c * 16) : kBig) - 1024u * (uint32_t)(i % 4);
+    oa[i] = (r < BN ? (uint32_t)(r * ra + c * 16) : kBig) - 1024u * (uint32_t)(i % 4);
   }
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
     int r, c;
     place(wid * NB + i, RB, r, c);
-    const int64_t row = (int64_t)tm * BM + r;
-    ob[i] = ((r < BM && row < M) ? (uint32_t)(row * rb + c * 16) : kBig) - 1024u * (uint32_t)(i % 4);
+    ob[i] = (r < BM ? (uint32_t)(r * rb + c * 16) : kBig) - 1024u * (uint32_t)(i % 4);
   }
   // Scales: the 2 PP kilobytes of a stage (panel, then weights or tokens: four bytes of
   // each of 256 rows) are split over the waves, SL lanes' 16 bytes each. Words of rows
   // that are not the tile's belong to rows that are not stored, or are past the array:
   // zero.
   const int sp = wid * SL / 64, sl0 = wid * SL % 64;
-  const bool sw_w = (sp & 1) == 0;
-  const uint32_t os = (uint32_t)(((sw_w ? (int64_t)tn * BN : (int64_t)tm * BM) + 4 * (sl0 + lane)) * 4);
+  const uint32_t os = (uint32_t)(16 * (sl0 + lane));
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
   const uint32_t la0 = lds0 + (uint32_t)(wid * NA) * 1024u;
   const uint32_t lb0 = lds0 + (uint32_t)(IA + wid * NB) * 1024u;
@@ -466,7 +481,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
     if (g == NG - 1) {
       const uint32_t panel = (uint32_t)(ks * PP + (sp >> 1));
       const uint32_t vs = panel < np ? os + panel * (sw_w ? spw : spx) : kBig;
-      dma_lanes<SL>(ls0 + so, vs, sw_w ? rsw : rsx);
+      dma_lanes<SL>(ls0 + so, vs, rs);
       return;
     }
     const bool tail = KS == 256 && (ks + 1) * KS > K;
@@ -489,47 +504,37 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
   };
 
   // Operand reads: byte of chunk c of the wave's first fragment row (rows lr, lr + T,
-  // ... have the same swizzle, and are T rows' bytes apart).
+  // ... have the same swizzle, and are T rows' bytes apart). Chunks of one lane differ from
+  // its first, lg, in higher bits only: their bytes are the first's, those bits flipped.
   const int lr = lane % T, lg = lane / T;
   auto at = [&](int row0, int c, int rowbytes) {
     if (rowbytes == 256) return (row0 + lr) * 256 + ((c & 8) << 4) + (((c & 7) ^ (lr & 7)) << 4);
     if (rowbytes == 128) return (row0 + lr) * 128 + ((c ^ ((lr >> 1) & 7)) << 4);
     return ((row0 + lr) >> 1) * 128 + ((((lr & 1) * 4 + c) ^ ((lr >> 1) & 7)) << 4);
   };
-  int xa[NKK], xb[NKK], xb2[NKK];
-#pragma unroll
-  for (int h = 0; h < NKK; ++h) {
-    // chunk of the lane's first 16 bytes: 32 E2M1 elements, 16 E4M3
-    const int ca = h * (KI / 32) + lg, cb = XFP4 ? ca : h * (KI / 16) + lg;
-    xa[h] = at(wn * WTN, ca, RA);
-    xb[h] = IA * 1024 + at(wm * WTM, cb, RB);
-    xb2[h] = XFP4 ? 0 : IA * 1024 + at(wm * WTM, cb + KI / 32, RB);
-  }
+  const int xa0 = at(wn * WTN, lg, RA), xb0 = IA * 1024 + at(wm * WTM, lg, RB);
   const int xsa = CODES + (wn * WTN + lr) * 4, xsb = CODES + 1024 + (wm * WTM + lr) * 4, sh = 8 * lg;
   acc_t acc[FN][FM];
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = acc_t{};
-
   v8i opa[2][FN], opb[2][FM];
   int sna[FN], snb[FM], sca[FN], scb[FM];  // scale words: as read, and shifted for use
   auto load_ops = [&](const uint8_t* st, int h, int buf) {
     const int panel = h * KI / 128;
+    // chunk of the lane's first 16 bytes: 32 E2M1 elements, 16 E4M3
+    const int xa = xa0 ^ (h * (KI / 32) << 4), xb = xb0 ^ (h * (XFP4 ? KI / 32 : KI / 16) << 4);
     const bool fresh = h * KI % 128 == 0;
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(st + xa[h] + i * T * RA);
+      const uint4 u = *reinterpret_cast<const uint4*>(st + xa + i * T * RA);
       opa[buf][i] = v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, 0, 0, 0, 0};
       if (fresh) sna[i] = *reinterpret_cast<const int*>(st + xsa + panel * 2048 + i * T * 4);
     }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      const uint4 u = *reinterpret_cast<const uint4*>(st + xb[h] + j * T * RB);
+      const uint4 u = *reinterpret_cast<const uint4*>(st + xb + j * T * RB);
       if constexpr (XFP4) {
         opb[buf][j] = v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, 0, 0, 0, 0};
       } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(st + xb2[h] + j * T * RB);
+        const uint4 w = *reinterpret_cast<const uint4*>(st + (xb ^ (KI / 32 << 4)) + j * T * RB);
         opb[buf][j] = v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
       }
       if (fresh) snb[j] = *reinterpret_cast<const int*>(st + xsb + panel * 2048 + j * T * 4);
@@ -554,7 +559,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
   // the S - 2 stages behind it (S - 1 behind the first) may still be in flight. The
   // last step of stage j - 1 is multiplied after that. Each step is kept apart for the
   // scheduler, which would otherwise hold a whole stage's operands in registers.
-  int cs = 0, it = 0;
+  int cs = 0, it = 0, kc = 0;  // kc: stage that the next refill copies
   // one MFMA, then the reads that one covers
   auto interleave = [&]() {
     constexpr int NR = FN + FM * (XFP4 ? 1 : 2), NM = FN * FM;
@@ -589,114 +594,170 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void mx4_tile_kernel(const Mx4Tile
           if (i < FN) multiply_row(h, buf, i);
           if constexpr (decltype(refill)::value) {
             __builtin_amdgcn_sched_barrier(0);
-            if (i < NG) issue_group(i, cs, ks0 + it + S);
+            if (i < NG) issue_group(i, cs, kc);
             __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (decltype(refill)::value) ++kc;
     cs = ns;
   };
-  if (nk > 0) {
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-      if (s < nk)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) issue_group(g, s, ks0 + s);
-    wait_stages<NI, S - 1>(nk - 1);
-    __syncthreads();
-    load_ops(smem, 0, 0);
-    for (; it < nk - S; ++it) steps(std::true_type{}, std::false_type{});
-    for (; it < nk - 1; ++it) steps(std::false_type{}, std::false_type{});
-    steps(std::false_type{}, std::true_type{});
-  }
-
   // Register 4 q + r of a fragment: weight row 8 q + 4 lg + r, token lr.
   constexpr int NQ = T == 16 ? 1 : 4;
-  const int64_t n0 = (int64_t)tn * BN;
-  const int own = (int)(N - n0 < BN ? N - n0 : BN);
-  if (!p.part && !p.g.out_raw) {
-    // bf16 outputs through the idle ring, each wave its own part of it (only the last
-    // stage's reads have to be over), so that a wave's stores run along a token's row:
-    // 16 bytes a lane, or 4 or 2 where the row stride (and so the rows' alignment) is no
-    // multiple of 8 or 2 channels. Rows of 16 bytes more than the wave's channels spread
-    // the writes over the banks.
-    constexpr int LD = WTN * 2 + 16, FIT = S * STAGE / NW / (T * LD);
-    constexpr int JC = FIT < FM ? FIT : FM;
-    static_assert(JC >= 1, "a token fragment per wave fits the ring");
-    uint8_t* so = smem + wid * (JC * T * LD);
-    uint16_t* Y = static_cast<uint16_t*>(p.g.Y) + n0 + wn * WTN;
-    const int64_t mw = (int64_t)tm * BM + wm * WTM, ldy = p.g.ldy;
-    const int ow = own - wn * WTN;
-    auto rows_out = [&](int j0, auto vec) {
-      constexpr int V = decltype(vec)::value, CPR = WTN / V, PIECES = JC * T * CPR;
+  // bf16 outputs go through the ring, each wave its own part, so that a wave's stores run
+  // along a token's row: 16 bytes a lane, or 4 or 2 where the row stride (and so the rows'
+  // alignment) is no multiple of 8 or 2 channels. Rows of 16 bytes more than the wave's
+  // channels spread the writes over the banks. With AHEAD a slot holds it, and the copies of
+  // the block's next tile run meanwhile.
+  constexpr int LD = WTN * 2 + 16;
+  constexpr int FIT = (AHEAD ? 1 : S) * STAGE / NW / (T * LD), JC = FIT < FM ? FIT : FM;
+  static_assert(JC >= 1, "a token fragment per wave fits");
+  const int64_t n4 = (N + 3) & ~(int64_t)3;
+  auto store = [&](int tm, int tn, uint8_t* stage) {
+    int sl = lane;
+    if constexpr (AHEAD) {  // what follows is not to occupy registers during the products
+      asm volatile("" : "+v"(sl));
+      sl &= 63;
+    }
+    const int lr = sl % T, lg = sl / T;
+    const int64_t n0 = (int64_t)tn * BN;
+    const int own = (int)(N - n0 < BN ? N - n0 : BN);
+    if (!p.part && !p.g.out_raw) {
+      uint8_t* so = stage + wid * (JC * T * LD);
+      uint16_t* Y = static_cast<uint16_t*>(p.g.Y) + n0 + wn * WTN;
+      const int64_t mw = (int64_t)tm * BM + wm * WTM, ldy = p.g.ldy;
+      const int ow = own - wn * WTN;
+      auto rows_out = [&](int j0, auto vec, auto nt) {
+        constexpr int V = decltype(vec)::value, CPR = WTN / V, PIECES = JC * T * CPR;
+        constexpr bool kWhole = 64 % CPR == 0;  // lanes keep their channels, rows go up in steps
+        uint16_t* const first = Y + (mw + T * j0) * ldy + (kWhole ? (sl / CPR) * ldy : 0);
 #pragma unroll V == 8 ? (PIECES + 63) / 64 : 4
-      for (int k = 0; k < (PIECES + 63) / 64; ++k) {
-        const int c = lane + 64 * k, ml = c / CPR, nl = V * (c % CPR);
-        const int64_t m = mw + T * j0 + ml;
-        if ((PIECES % 64 != 0 && c >= PIECES) || m >= M || nl >= ow || T * j0 + ml >= WTM) continue;
-        const uint8_t* src = so + ml * LD + nl * 2;
-        uint16_t* dst = Y + m * ldy + nl;
-        if constexpr (V == 8) {
-          typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-          const u4 v = *reinterpret_cast<const u4*>(src);
-          if (nl + 8 > ow) {
-            for (int e = 0; nl + e < ow; ++e) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-          } else if (p.nt_out) {
-            __builtin_nontemporal_store(v, reinterpret_cast<u4*>(dst));
+        for (int k = 0; k < (PIECES + 63) / 64; ++k) {
+          const int c = sl + 64 * k, ml = c / CPR, nl = V * (c % CPR);
+          const int64_t m = mw + T * j0 + ml;
+          if ((PIECES % 64 != 0 && c >= PIECES) || m >= M || nl >= ow || T * j0 + ml >= WTM) continue;
+          const uint8_t* src = so + ml * LD + nl * 2;
+          uint16_t* dst = first + (kWhole ? k * (64 / CPR) : ml) * ldy + nl;
+          if constexpr (V == 8) {
+            typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+            const u4 v = *reinterpret_cast<const u4*>(src);
+            if (nl + 8 > ow) {
+              for (int e = 0; nl + e < ow; ++e) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            } else if constexpr (decltype(nt)::value) {
+              __builtin_nontemporal_store(v, reinterpret_cast<u4*>(dst));
+            } else {
+              *reinterpret_cast<u4*>(dst) = v;
+            }
+          } else if constexpr (V == 2) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(src);
+            if (nl + 2 > ow) dst[0] = (uint16_t)v;
+            else *reinterpret_cast<uint32_t*>(dst) = v;
           } else {
-            *reinterpret_cast<u4*>(dst) = v;
+            dst[0] = *reinterpret_cast<const uint16_t*>(src);
           }
-        } else if constexpr (V == 2) {
-          const uint32_t v = *reinterpret_cast<const uint32_t*>(src);
-          if (nl + 2 > ow) dst[0] = (uint16_t)v;
-          else *reinterpret_cast<uint32_t*>(dst) = v;
+        }
+      };
+#pragma unroll
+      for (int j0 = 0; j0 < FM; j0 += JC) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = j0; j < FM && j < j0 + JC; ++j)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const acc_t& v = acc[i][j];
+              *reinterpret_cast<uint2*>(so + (T * (j - j0) + lr) * LD + (T * i + 8 * q + 4 * lg) * 2) =
+                  make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
+            }
+        // lanes read what others of the wave wrote: LDS accesses of a wave are in order
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        // (the branch on nt_out around the loop: around the store the two are merged, without nt)
+        if ((ldy & 7) != 0) {
+          if ((ldy & 1) == 0) rows_out(j0, std::integral_constant<int, 2>{}, std::false_type{});
+          else rows_out(j0, std::integral_constant<int, 1>{}, std::false_type{});
+        } else if (p.nt_out) {
+          rows_out(j0, std::integral_constant<int, 8>{}, std::true_type{});
         } else {
-          dst[0] = *reinterpret_cast<const uint16_t*>(src);
+          rows_out(j0, std::integral_constant<int, 8>{}, std::false_type{});
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        const int64_t m = (int64_t)tm * BM + wm * WTM + T * j + lr;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const int nl = wn * WTN + T * i + 8 * q + 4 * lg;
+          if (m >= M || nl >= own) continue;
+          const float a[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if (p.part)
+            *reinterpret_cast<float4*>(p.part + ((int64_t)split * M + m) * n4 + n0 + nl) =
+                make_float4(a[0], a[1], a[2], a[3]);
+          else
+            mx4_store4(p.g, m, n0 + nl, a);
         }
       }
-    };
+  };
+
+  // The block's tiles. Copies run S stages ahead, and with AHEAD (nk >= S then) into the next
+  // tile: its first S - 1 stages are on their way, or there, while this one's last is
+  // multiplied and its outputs are stored from the slot of that last stage.
+  int tm, tn;
+  locate(cur, tm, tn);
+  copy_from(tm, tn);
+  kc = ks0;
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < nk) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) issue_group(g, s, kc);
+      ++kc;
+    }
+  if (nk > 0) wait_stages<NI, S - 1>(nk - 1);
+  __syncthreads();
+  for (;;) {
+    const int next = cur + step;
+    const bool more = AHEAD && next < end;
+    int tm2 = 0, tn2 = 0;
+    if (more) locate(next, tm2, tn2);
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = acc_t{};
+    uint8_t* last_slot = smem;
+    if (nk > 0) {
+      load_ops(smem + cs * STAGE, 0, 0);
+      it = 0;
+      const int refills = more ? nk - 1 : nk - S;
+      for (; it < refills; ++it) {
+        if (AHEAD && it == nk - S) {
+          copy_from(tm2, tn2);
+          kc = 0;
+        }
+        steps(std::true_type{}, std::false_type{});
+      }
+      for (; it < nk - 1; ++it) steps(std::false_type{}, std::false_type{});
+      last_slot = smem + cs * STAGE;
+      steps(std::false_type{}, std::true_type{});
+    }
+    if (more) wait_vm<(S - 2) * NI>();  // the next tile's first stage
+    __syncthreads();
+    store(tm, tn, AHEAD ? last_slot : smem);
+    if (!more) break;
     __syncthreads();
 #pragma unroll
-    for (int j0 = 0; j0 < FM; j0 += JC) {
-#pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = j0; j < FM && j < j0 + JC; ++j)
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const acc_t& v = acc[i][j];
-            *reinterpret_cast<uint2*>(so + (T * (j - j0) + lr) * LD + (T * i + 8 * q + 4 * lg) * 2) =
-                make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
-          }
-      // lanes read what others of the wave wrote: LDS accesses of a wave are in order
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if ((ldy & 7) == 0) rows_out(j0, std::integral_constant<int, 8>{});
-      else if ((ldy & 1) == 0) rows_out(j0, std::integral_constant<int, 2>{});
-      else rows_out(j0, std::integral_constant<int, 1>{});
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    return;
+    for (int g = 0; g < NG; ++g) issue_group(g, cs == 0 ? S - 1 : cs - 1, kc);
+    ++kc;
+    cur = next;
+    tm = tm2;
+    tn = tn2;
   }
-  const int64_t n4 = (N + 3) & ~(int64_t)3;
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int64_t m = (int64_t)tm * BM + wm * WTM + T * j + lr;
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int nl = wn * WTN + T * i + 8 * q + 4 * lg;
-        if (m >= M || nl >= own) continue;
-        const float a[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        if (p.part)
-          *reinterpret_cast<float4*>(p.part + ((int64_t)split * M + m) * n4 + n0 + nl) =
-              make_float4(a[0], a[1], a[2], a[3]);
-        else
-          mx4_store4(p.g, m, n0 + nl, a);
-      }
-    }
 }
 
 // Sum of the K splits' partial sums ([splits][M][N up to a multiple of 4]), four
@@ -718,7 +779,7 @@ __global__ __launch_bounds__(256) void mx4_sum_kernel(const float* __restrict__ 
 }
 
 template <bool XFP4, int T, int BN, int BM, int WN, int WM, int S, int KS>
-hipError_t launch_tile(const Mx4Params& g, int splits, float* part, hipStream_t st) {
+hipError_t launch_tile(const Mx4Params& g, int splits, int per_cu, float* part, hipStream_t st) {
   Mx4TileParams p;
   p.g = g;
   p.part = splits > 1 ? part : nullptr;
@@ -726,12 +787,26 @@ hipError_t launch_tile(const Mx4Params& g, int splits, float* part, hipStream_t 
   p.tiles_n = (int)((g.N + BN - 1) / BN);
   p.stages = (int)((g.K + KS - 1) / KS);
   p.splits = splits;
-  // Outputs beyond the L2s' 32 MB leave them to the operands (32B gate at 4096 tokens
-  // 298 against 317 us; the 19 MB of the 7B gate and up at 256 tokens 26.9 against 26.4).
-  p.nt_out = 2 * g.M * g.N > ((int64_t)32 << 20);
-  const int64_t blocks = (int64_t)p.tiles_m * p.tiles_n * splits;
-  hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS>), dim3((unsigned)blocks),
-                     dim3(64 * WN * WM), 0, st, p);
+  // Outputs past half the 256 MB of the memory-side cache leave it to the operands: 2048 and
+  // 4096 tokens of the stacked 7B gate and up (155 and 310 MB) 140 and 272 us against 152 and
+  // 305, the 32B gate at 4096 275 against 299; 1024 tokens (78 MB) 87 against 83.
+  p.nt_out = 2 * g.M * g.N > ((int64_t)128 << 20);
+  // A block takes one tile, or, where they fill more than one round and copies can run
+  // ahead, every so many-th of its XCD's (stacked 7B gate and up at 512, 1024 and 2048 tokens
+  // 42.4, 80 and 153 us against 44.8, 84.8 and 156; 8192 tokens of 7B QKV 78 against 83). Past
+  // five rounds that gains nothing (32B gate at 4096, seven rounds: 309 against 306).
+  const int64_t need = ((int64_t)p.tiles_m * p.tiles_n * splits + 7) / 8 * 8;
+  const int64_t round = kCUs * per_cu;
+  bool ahead = false;
+  if constexpr (Mx4Ahead<XFP4, T, BN, BM, WN, WM, KS>::value) {
+    ahead = splits == 1 && p.stages >= S && need > round && need <= 5 * round;
+    if (ahead)
+      hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS, true>), dim3((unsigned)round),
+                         dim3(64 * WN * WM), 0, st, p);
+  }
+  if (!ahead)
+    hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS, false>), dim3((unsigned)need),
+                       dim3(64 * WN * WM), 0, st, p);
   if (splits > 1) {
     const int64_t total = g.M * ((g.N + 3) >> 2);
     hipLaunchKernelGGL(mx4_sum_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, part, splits, g);
@@ -755,7 +830,7 @@ hipError_t launch_decode(const Mx4Params& p, const uint16_t* X, int64_t ldx, hip
 struct Mx4Config {
   int BN, BM, KS, per_cu;
   float base, alone, shared;
-  hipError_t (*run)(const Mx4Params&, int, float*, hipStream_t);
+  hipError_t (*run)(const Mx4Params&, int, int, float*, hipStream_t);
 };
 constexpr Mx4Config kFp4Configs[] = {
     {256, 256, 256, 1, 8.0f, 2.00f, 0.0f, launch_tile<true, 32, 256, 256, 2, 4, 2, 256>},
@@ -776,7 +851,6 @@ constexpr Mx4Config kFp8Configs[] = {
     {64, 64, 256, 1, 4.0f, 0.38f, 0.0f, launch_tile<false, 16, 64, 64, 2, 2, 3, 256>},
     {64, 32, 256, 2, 3.8f, 0.31f, 0.42f, launch_tile<false, 16, 64, 32, 4, 1, 4, 256>},
 };
-constexpr int kCUs = 256;
 
 struct Mx4Plan {
   const Mx4Config* c;  // NULL: the decode kernel on token codes
@@ -852,7 +926,7 @@ hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const vo
                     M, N, K, Y, ldy, out_raw};
   const bool fp4 = xfmt == kActMxFp4;
   const Mx4Plan plan = make_mx4_plan(M, N, K, fp4);
-  if (plan.c) return plan.c->run(p, plan.splits, static_cast<float*>(ws), st);
+  if (plan.c) return plan.c->run(p, plan.splits, plan.c->per_cu, static_cast<float*>(ws), st);
   return fp4 ? launch_decode<true, false, 8, 8, 4>(p, nullptr, 0, st)
              : launch_decode<false, false, 8, 8, 4>(p, nullptr, 0, st);
 }
