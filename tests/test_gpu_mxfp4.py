@@ -756,3 +756,19 @@ def test_gemm_of_several_rounds_of_tiles(M, N, K, pad, fmt):
         assert bool(((raw[a].double() - xv[a] @ wv.t()).abs() <= rel * (xv[a].abs() @ wv.abs().t()) + 1e-30).all())
     assert torch.equal(wide[:, :N], raw.bfloat16())
     assert bool((wide[:, N:] == 7.0).all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_dequantize_past_the_l2s(fmt, out):
+    """36 MB of values and more, in rows of a wider buffer: those of the rows in small calls."""
+    R, K = 5003, 3616
+    x = to_dev_bf16(_acts(R, K, 12))
+    q, s = B.mxfp4_quantize(x) if fmt == "mxfp4" else B.block_norm_quant(x, x, torch.ones(K, device=DEV), "mxfp8")[1:]
+    wide = torch.full((R, K + 32), 7.0, dtype=out, device=DEV)
+    B.mx_dequantize(q, s, out=wide[:, :K])
+    for lo in range(0, R, 500):
+        hi = min(lo + 500, R)
+        part = B.mx_dequantize(q[lo:hi].contiguous(), s[:, lo:hi].contiguous(), dtype=out)
+        assert torch.equal(wide[lo:hi, :K], part)
+    assert bool((wide[:, K:] == 7.0).all())
