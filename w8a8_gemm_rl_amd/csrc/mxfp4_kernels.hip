@@ -299,8 +299,7 @@ __global__ __launch_bounds__(64 * NW) void mx4_decode_kernel(const Mx4Params p,
 // Stacked 7B gate and up, 75 MB of codes and scales in and out at 33 E4M3 tokens: 15.4 us,
 // 4.9 TB/s, what a copy reaches. At 256 E2M1 tokens 93 MB take 26 us: 237 tiles of
 // 160 x 256, one round. The 32B gate at 4096 E2M1 tokens: 275 - 300 us, 3.9 - 4.2 PFLOP/s
-// (boxes differ, and the clock falls as it goes on).
-// There, on 256 x 256 tiles, 20 stages in seven rounds, the products alone take 160 us (the
+// (cards differ, and their clock under load). There, on 256 x 256 tiles, 20 stages in seven rounds, the products alone take 160 us (the
 // clock falls to 1.93 GHz), a fragment's LDS reads alone 164, the copies alone 193 (20 bytes
 // a clock and CU; 127 from the L2), any two together 205, all three 250; filling the ring
 // and storing the outputs add 25 - 35. Measured slower there: a third operand buffer with
@@ -923,8 +922,8 @@ hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int64_t R
   auto by_size = [&](auto fp4, auto to_bf16) {
     return nt ? run(fp4, to_bf16, std::true_type{}) : run(fp4, to_bf16, std::false_type{});
   };
-  if (fmt == kActMxFp4) return bf16 ? by_size(std::true_type{}, std::true_type{}) : by_size(std::true_type{}, std::false_type{});
-  return bf16 ? by_size(std::false_type{}, std::true_type{}) : by_size(std::false_type{}, std::false_type{});
+  auto by_type = [&](auto fp4) { return bf16 ? by_size(fp4, std::true_type{}) : by_size(fp4, std::false_type{}); };
+  return fmt == kActMxFp4 ? by_type(std::true_type{}) : by_type(std::false_type{});
 }
 
 hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq,
