@@ -128,6 +128,7 @@ struct MxDmaParams {
   int tiles_m, nks, rn;
 };
 
+// (s_nop 0: the wait state between a write of M0 and the copies that read it; qr_copy.h.)
 template <int CNT>
 __device__ __forceinline__ void mx_dma16(uint32_t lds, const uint32_t* vo,
                                          __amdgpu_buffer_rsrc_t r, int soff) {
@@ -135,22 +136,22 @@ __device__ __forceinline__ void mx_dma16(uint32_t lds, const uint32_t* vo,
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
   if constexpr (CNT == 1)
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(lds), "v"(vo[0]), "s"(r), "s"(soff) : "memory", "m0");
   else if constexpr (CNT == 2)
-    asm volatile("s_mov_b32 m0, %0\n\t"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                  "buffer_load_dwordx4 %1, %3, %4 offen lds\n\t"
                  "buffer_load_dwordx4 %2, %3, %4 offen offset:1024 lds"
                  :: "s"(lds), "v"(vo[0]), "v"(vo[1]), "s"(r), "s"(soff) : "memory", "m0");
   else if constexpr (CNT == 3)
-    asm volatile("s_mov_b32 m0, %0\n\t"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                  "buffer_load_dwordx4 %1, %4, %5 offen lds\n\t"
                  "buffer_load_dwordx4 %2, %4, %5 offen offset:1024 lds\n\t"
                  "buffer_load_dwordx4 %3, %4, %5 offen offset:2048 lds"
                  :: "s"(lds), "v"(vo[0]), "v"(vo[1]), "v"(vo[2]), "s"(r), "s"(soff)
                  : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %0\n\t"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                  "buffer_load_dwordx4 %1, %5, %6 offen lds\n\t"
                  "buffer_load_dwordx4 %2, %5, %6 offen offset:1024 lds\n\t"
                  "buffer_load_dwordx4 %3, %5, %6 offen offset:2048 lds\n\t"

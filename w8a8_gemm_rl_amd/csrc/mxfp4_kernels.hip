@@ -307,12 +307,14 @@ __global__ __launch_bounds__(64 * NW) void mx4_decode_kernel(const Mx4Params p,
 // priorities, non-temporal weight copies, other groupings of tiles.
 // ---------------------------------------------------------------------------
 // One copy of LANES lanes' 16 bytes (a power of two), exec being all ones before and after.
+// The wait state between the write of M0 and the copy (qr_copy.h) is an s_nop, or the write
+// of exec.
 template <int LANES>
 __device__ __forceinline__ void dma_lanes(uint32_t lds_addr, uint32_t vo, __amdgpu_buffer_rsrc_t r) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
   if constexpr (LANES == 64)
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  : : "s"(lds_addr), "v"(vo), "s"(r) : "memory", "m0");
   else
     asm volatile(

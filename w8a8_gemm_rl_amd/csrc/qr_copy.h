@@ -7,6 +7,11 @@
 // (offsets 0, 1 KB, 2 KB, 3 KB; the per-lane global offsets are pre-biased by
 // minus the instruction offset). Offsets past the buffer resource's
 // num_records read as zero, which is how rows outside a matrix are copied.
+//
+// gfx9 parts want one wait state between a scalar write of M0 and an LDS-DMA
+// copy that reads it, or the copy may take the M0 of before and land in
+// another slot. The compiler provides it for its own code but adds nothing
+// inside inline asm, hence the s_nop 0 (one issue slot a group of copies).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -26,26 +31,26 @@ __device__ __forceinline__ void dma_group(uint32_t lds_addr, const uint32_t* vo,
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
   if constexpr (CNT == 1 && !NT)
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  : : "s"(lds_addr), "v"(vo[0]), "s"(r), "s"(soff) : "memory", "m0");
   else if constexpr (CNT == 1)
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
                  : : "s"(lds_addr), "v"(vo[0]), "s"(r), "s"(soff) : "memory", "m0");
   else if constexpr (CNT == 2 && !NT)
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
         "buffer_load_dwordx4 %1, %3, %4 offen lds\n\t"
         "buffer_load_dwordx4 %2, %3, %4 offen offset:1024 lds"
         : : "s"(lds_addr), "v"(vo[0]), "v"(vo[1]), "s"(r), "s"(soff) : "memory", "m0");
   else if constexpr (CNT == 2)
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
         "buffer_load_dwordx4 %1, %3, %4 offen nt lds\n\t"
         "buffer_load_dwordx4 %2, %3, %4 offen offset:1024 nt lds"
         : : "s"(lds_addr), "v"(vo[0]), "v"(vo[1]), "s"(r), "s"(soff) : "memory", "m0");
   else if constexpr (CNT == 3 && !NT)
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
         "buffer_load_dwordx4 %1, %4, %5 offen lds\n\t"
         "buffer_load_dwordx4 %2, %4, %5 offen offset:1024 lds\n\t"
         "buffer_load_dwordx4 %3, %4, %5 offen offset:2048 lds"
@@ -53,7 +58,7 @@ __device__ __forceinline__ void dma_group(uint32_t lds_addr, const uint32_t* vo,
         : "memory", "m0");
   else if constexpr (CNT == 3)
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
         "buffer_load_dwordx4 %1, %4, %5 offen nt lds\n\t"
         "buffer_load_dwordx4 %2, %4, %5 offen offset:1024 nt lds\n\t"
         "buffer_load_dwordx4 %3, %4, %5 offen offset:2048 nt lds"
@@ -61,7 +66,7 @@ __device__ __forceinline__ void dma_group(uint32_t lds_addr, const uint32_t* vo,
         : "memory", "m0");
   else if constexpr (!NT)
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
         "buffer_load_dwordx4 %1, %5, %6 offen lds\n\t"
         "buffer_load_dwordx4 %2, %5, %6 offen offset:1024 lds\n\t"
         "buffer_load_dwordx4 %3, %5, %6 offen offset:2048 lds\n\t"
@@ -70,7 +75,7 @@ __device__ __forceinline__ void dma_group(uint32_t lds_addr, const uint32_t* vo,
         : "memory", "m0");
   else
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
         "buffer_load_dwordx4 %1, %5, %6 offen nt lds\n\t"
         "buffer_load_dwordx4 %2, %5, %6 offen offset:1024 nt lds\n\t"
         "buffer_load_dwordx4 %3, %5, %6 offen offset:2048 nt lds\n\t"

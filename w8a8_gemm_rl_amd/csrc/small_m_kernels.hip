@@ -171,7 +171,8 @@ __global__ __launch_bounds__(kNW * 64) void small_m_linear_kernel(const SmallPar
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
       // one wave instruction: 64 lanes x 16 bytes to LDS at M0 + 16 lane
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+      // (s_nop 0: the wait state that M0 wants; qr_copy.h)
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                    : : "s"(m0), "v"(off), "s"(rx) : "memory", "m0");
 #pragma clang diagnostic pop
     }
