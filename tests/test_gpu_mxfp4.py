@@ -651,6 +651,20 @@ def test_outputs_whose_rows_share_memory_are_refused():
             f()
 
 
+@pytest.mark.parametrize("M", [2, 9])
+def test_block_norm_refuses_an_expanded_token_gate(M):
+    """One bf16 row as every token's gate; the same values in rows of their own, and as fp32 per
+    channel, are taken and agree."""
+    d = _norm_inputs(M, 352, 6, True, "none")
+    row = to_dev_bf16(F.f32_to_bf16_bits(np.random.default_rng(1).uniform(0, 1, 352).astype(np.float32)))
+    args = (_dev(d["Y"]), _dev(d["H"]), _dev(d["gamma"]), "mxfp4", _dev(d["post_gamma"]))
+    with pytest.raises(B.QRError, match="row stride"):
+        B.block_norm_quant(*args, gate=row.expand(M, 352))
+    want = B.block_norm_quant(*args, gate=row.float())
+    for gate in (row.expand(M, 352).contiguous(), torch.cat([row, row]).expand(M, 704).contiguous()[:, 352:]):
+        assert all(torch.equal(a, b) for a, b in zip(B.block_norm_quant(*args, gate=gate), want))
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("fmt", ["int8", "fp8"])
 def test_block_norm_scales_of_rows_of_no_values_are_zero(fmt, kind):

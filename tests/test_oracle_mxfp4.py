@@ -235,3 +235,23 @@ def test_binding_passes_the_row_stride_of_an_output_as_it_is():
     assert B._mx4_out(y, like, 1, 16, torch.bfloat16)[1] == 16
     assert B._mx4_out(torch.zeros((4, 20), dtype=torch.bfloat16)[:, :16], like, 4, 16, torch.bfloat16)[1] == 20
     assert B._mx4_out(torch.zeros((3, 0), dtype=torch.bfloat16), like, 3, 0, torch.bfloat16)[1] >= 0
+
+
+def test_gate_row_strides():
+    """A gate per channel is fp32 [K], stride 0 in the library; rows of a bf16 gate that are one row
+    expanded, whose stride is 0 as well, must not reach it as that."""
+    import torch
+    from w8a8_gemm_rl_amd import binding as B
+
+    shape = torch.Size((4, 64))
+    row = torch.zeros(64, dtype=torch.bfloat16)
+    assert B._gate_ld(torch.zeros(64), shape) == 0
+    assert B._gate_ld(torch.zeros(shape, dtype=torch.bfloat16), shape) == 64
+    assert B._gate_ld(torch.zeros((4, 80), dtype=torch.bfloat16)[:, :64], shape) == 80
+    assert B._gate_ld(row.expand(1, 64), torch.Size((1, 64))) == 64
+    for gate in (row.expand(4, 64), row.view(1, 64).expand(4, 64), torch.zeros(256, dtype=torch.bfloat16).as_strided((4, 64), (32, 1))):
+        with pytest.raises(B.QRError, match="row stride"):
+            B._gate_ld(gate, shape)
+    for gate in (row, torch.zeros(shape), torch.zeros(128)[::2], torch.zeros(1).expand(64), torch.zeros((64, 4), dtype=torch.bfloat16).t()):
+        with pytest.raises(ValueError):
+            B._gate_ld(gate, shape)

@@ -699,6 +699,20 @@ def mxfp4_linear(X, Wq, sw, x="fp4", Y=None, ws=None):
     return Y
 
 
+def _gate_ld(gate, shape):
+    """Row stride of a gate: 0 says one fp32 value per channel, else rows of bf16 [M, K]. Rows
+    that are one row expanded have stride 0 too: refused here like those of Y and H in the
+    library, which would take them for the fp32 gate."""
+    if gate.dtype == torch.bfloat16 and gate.shape == shape:
+        ld = _ld(gate, "gate")
+        if ld < shape[1]:
+            raise QRError("qr_block_norm_quant", -1, f"a row stride below K={shape[1]} (gate)")
+        return ld
+    if gate.dtype != torch.float32 or gate.shape != shape[1:] or not gate.is_contiguous():
+        raise ValueError("gate must be float32 [K] or bfloat16 [M, K]")
+    return 0
+
+
 def block_norm_quant(Y, H, gamma, fmt, post_gamma=None, gate=None, res_scale=1.0, beta=None,
                      post_beta=None, eps=1e-6, kind="rms", Hout=None, codes=None, scales=None):
     """The step between two blocks: Hout = bf16(res_scale * H + gate * post_norm(Y)), and
@@ -706,7 +720,7 @@ def block_norm_quant(Y, H, gamma, fmt, post_gamma=None, gate=None, res_scale=1.0
     (Hout, codes, scales); scales is None for "bf16".
 
     Y, H bf16 [M, K]; gamma, beta, post_gamma, post_beta fp32 [K]; gate None, fp32 [K] or bf16
-    [M, K]. Hout may be H or Y (updated in place)."""
+    [M, K] (rows of their own, not one expanded). Hout may be H or Y (updated in place)."""
     idx = _one_device(Y.device, H, gamma, post_gamma, gate, beta, post_beta, Hout, codes, scales)
     shape = Y.shape
     if Y.dtype != torch.bfloat16 or H.dtype != torch.bfloat16 or H.shape != shape:
@@ -720,12 +734,7 @@ def block_norm_quant(Y, H, gamma, fmt, post_gamma=None, gate=None, res_scale=1.0
     for t in (gamma, post_gamma, beta, post_beta):
         if t is not None and (t.dtype != torch.float32 or t.numel() != K or not t.is_contiguous()):
             raise ValueError("gains and biases must be contiguous float32 tensors of K entries")
-    ldgate = 0
-    if gate is not None:
-        if gate.dtype == torch.bfloat16 and gate.shape == shape:
-            ldgate = _ld(gate, "gate")
-        elif gate.dtype != torch.float32 or gate.shape != (K,) or not gate.is_contiguous():
-            raise ValueError("gate must be float32 [K] or bfloat16 [M, K]")
+    ldgate = 0 if gate is None else _gate_ld(gate, shape)
     if Hout is None:
         Hout, ldo = Y.new_empty(shape), K
     elif Hout.shape != shape or Hout.dtype != torch.bfloat16:
