@@ -379,6 +379,45 @@ def test_block_norm_layer_kind_with_a_large_mean(shift):
     _check_norm(d, "mxfp8", "layer", 1.0)
 
 
+def _rows_with_tied_means(M, K, seed):
+    """bf16 rows around 1.875 whose mean is an odd multiple of 2^-24, half way between two fp32
+    numbers: K - 2 multiples of 2^-7 and two small elements, last, that bring the sum to K times it."""
+    g = np.random.default_rng(seed)
+    j = (K & -K).bit_length() - 1
+    c, u = K >> j, 24 - j  # K = c 2^j; sums counted in 2^-u
+    v = np.float64(1.875) + g.integers(-4, 5, (M, K)) * 2.0 ** -7
+    for row in v:
+        n = int(row[:-2].sum() * 2 ** u)
+        m = -(-n // c) | 1
+        m += 2 * int(g.integers(0, (1 << 14) // c))
+        rest = c * m - n
+        assert 0 <= rest < 1 << 15 and 1 << 24 < m < 1 << 25
+        row[-2], row[-1] = (rest >> 7) * 2.0 ** (7 - u), (rest & 127) * 2.0 ** -u
+    bits = F.f32_to_bf16_bits(v.astype(np.float32))
+    assert np.array_equal(F.bf16_bits_to_f32(bits), v)
+    mean = v.sum(axis=1) * 2.0 ** 24 / K
+    assert np.all(mean == np.rint(mean)) and np.all(mean % 2 == 1)
+    return bits
+
+
+@pytest.mark.parametrize("M", [64, 4096])
+@pytest.mark.parametrize("K", [96, 784, 1232, 1456, 3584, 14336 + 784])
+def test_block_norm_layer_kind_with_a_mean_half_way_between_two_floats(K, M):
+    """The mean is rounded to fp32 once, from the sum's quotient by K: ties to even. (A product with
+    fl64(1 / K) falls beside the tie for K of some odd factors: 49, 77, 91.) The last elements get no
+    gain, so the scale is a deviation of at most 2^-4 over Q and shows one step of the mean, 2^-23."""
+    M = M if K < 4096 else min(M, 256)
+    bits = _rows_with_tied_means(M, K, K)
+    gamma = np.ones(K, np.float32)
+    gamma[-2:] = 0.0
+    zero = np.zeros((M, K), np.uint16)
+    d = dict(Y=bits, H=zero, gamma=gamma, post_gamma=None, beta=None, post_beta=None, gate=None)
+    _check_norm(d, "int8", "layer", 1.0)
+    q, s = B.norm_quant(_dev(bits), _dev(gamma), "int8", kind="layer")
+    _, q2, s2 = B.block_norm_quant(_dev(bits), _dev(zero), _dev(gamma), "int8", kind="layer")
+    assert torch.equal(s, s2) and torch.equal(q, q2)
+
+
 def test_block_norm_of_k16_rows():
     """Rows of the per-token formats need only 16-element steps."""
     for fmt in ("int8", "fp8", "bf16"):

@@ -119,6 +119,11 @@ __device__ __forceinline__ double rsqrt64(double x) {
 // all in float64: one pass and one barrier instead of two. The cancellation costs
 // s2 / that of its 53 bits; where it is more than 6 (a mean of eight deviations) the
 // second pass is made.
+//
+// The mean's quotient by K is a product with fl64(1 / K) and one correction by its remainder
+// (exact in an fma): a mean that float64 holds comes out as it is. One row in a hundred has a
+// mean half way between two fp32 numbers (short sums over a K with few odd factors), and the
+// product alone falls beside it for K of some odd factors, to be rounded to the wrong one.
 template <int KIND, int MAXC, typename Live>
 __device__ __forceinline__ void norm_row(float (&v)[MAXC][8], const Live& live, int lt, int tpr, double inv_k,
                                          double k, const float* gamma, const float* beta, float eps,
@@ -137,7 +142,8 @@ __device__ __forceinline__ void norm_row(float (&v)[MAXC][8], const Live& live, 
           s[1] = fma(d, d, s[1]);
         }
     row_sum<2>(s, red);
-    mu = (float)(s[0] * inv_k);
+    const double q = s[0] * inv_k;
+    mu = (float)fma(fma(-q, k, s[0]), inv_k, q);
     const double m = (double)mu;
     var = s[1] - m * (2.0 * s[0] - k * m);
     if (!(var * 64.0 > s[1])) {  // the same for every thread of the block
