@@ -390,8 +390,10 @@ int qr_mxfp4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const 
  *   codes, scales = z in format fmt: the per-token formats as qr_norm_quant, the
  *   block formats as qr_mxfp4_quantize / qr_mx_quantize of the fp32 z, QR_ACT_BF16
  *   bf16_rne(z) (for qr_linear_fused and qr_mxfp4_linear).
- * Both norms are of kind `norm` with the arithmetic of qr_norm_quant: codes and
- * scales are bit for bit those of qr_norm_quant(Hout, gamma, beta).
+ * Both norms are of kind `norm` with qr_norm_quant's roundings: codes and scales
+ * are those of qr_norm_quant(Hout, gamma, beta) unless a statistic's exact value (r, or
+ * a mean that float64 does not hold) lies within about 2^-45 (relative) of an fp32
+ * rounding boundary, where the order of the sums decides, as there.
  *
  *   Y, H     [M, ldy], [M, ldh] bf16: block output and residual stream (read).
  *   post_gamma, post_beta  NULL or [K] fp32 (post_beta only with post_gamma).

@@ -436,6 +436,25 @@ def test_block_norm_codes_are_those_of_the_norm_alone(fmt, kind):
     assert np.array_equal(codes_np(q), codes_np(q2)) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("K", [64, 784, 1056])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_block_norm_of_many_rows_differs_from_the_norm_alone_by_a_rounding_at_most(kind, K):
+    """131072 rows. r is another fp32 number only where 1 / sqrt lies within 2^-45 (relative) of a
+    rounding boundary, and those are at least 2^-24 apart: a share of 2 2^-45 / 2^-24 = 2^-20 of the
+    rows, 0.13 here, so more than four of them do not happen. A step of r is 2^-23 at most, of a mean
+    below 2 at most 2^-23 against deviations of at least a quarter: 2^-20 of the scale covers both."""
+    M = 1 << 17
+    g = torch.Generator(device=DEV).manual_seed(K)
+    Y = torch.randn((M, K), device=DEV, generator=g).bfloat16()
+    gamma = torch.rand(K, device=DEV, generator=g) + 0.5
+    h, q, s = B.block_norm_quant(Y, torch.zeros_like(Y), gamma, "int8", kind=kind)
+    q2, s2 = B.norm_quant(Y, gamma, "int8", kind=kind)
+    assert torch.equal(h, Y)
+    off = (s != s2) | (q != q2).any(1)
+    assert int(off.sum()) <= 4
+    assert bool(((s - s2).abs() <= 2.0 ** -20 * s2).all()) and bool(((q.int() - q2.int()).abs() <= 1).all())
+
+
 @pytest.mark.parametrize("K", [352, 3584, 18944])
 def test_block_norm_in_place_and_in_wider_rows(K):
     """Hout as H itself, as Y itself, as the token gate itself, and as columns between H's rows."""

@@ -7,9 +7,12 @@
 //   h' = bf16(fl32(fl32(res h) + t))                          (the new residual stream)
 //   z  = norm of h' with the next block's gain (UAQ's s folded in) -> codes, or bf16
 //
-// The norms' arithmetic is the norm producer's: statistics in float64, r rounded
-// once to fp32, fp32 products in a fixed order (contraction is off in this file), so
-// codes are reproducible bit for bit.
+// The norms' roundings are the norm producer's: statistics in float64, mean and r rounded
+// once to fp32, fp32 products in a fixed order (contraction is off in this file). A call
+// gives the same bits on every run, and the producer's unless a statistic's exact value
+// lies within about 2^-45 of an fp32 rounding boundary: sums are taken in another order
+// here, LayerNorm's variance loses up to 6 bits to cancellation (2^-47), 1 / sqrt is good
+// to 2^-48.
 #include "qr_internal.h"
 #include "qr_mx.h"
 
