@@ -408,8 +408,11 @@ int qr_mxfp4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const 
  *            aligned. scales is not used by QR_ACT_BF16.
  * K a multiple of 16 (32 for the block formats), at most 32768; strides multiples
  * of 8. Per-token formats take finite inputs; the block formats and bf16 follow the
- * formula for others (a NaN in a row makes its z NaN, an infinity makes r zero), and
- * a block whose z is not finite is a NaN block.
+ * formula for others, and a block whose z is not finite is a NaN block. What a norm makes
+ * of its row (Y's for the first, h' for the second): a NaN makes all of it NaN; an infinity
+ * makes RMS's r zero, so the infinite elements become NaN and the others 0 (beta, with
+ * one), and LayerNorm's mean infinite or NaN and so all of its row NaN. An h' past bf16's
+ * range is an infinity.
  */
 int qr_block_norm_quant(const void* Y, int64_t ldy, const void* H, int64_t ldh, int64_t M, int64_t K,
                         int norm, const float* post_gamma, const float* post_beta, const void* gate,

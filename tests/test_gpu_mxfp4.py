@@ -498,6 +498,54 @@ def test_block_norm_of_rows_that_are_zero_or_not_finite():
         assert bool((v[0] == 0).all()) and bool((h[0] == 0).all())
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8", "bf16"])
+@pytest.mark.parametrize("beta", [False, True])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_block_norm_follows_its_formula_for_rows_that_are_not_finite(kind, post, beta, fmt):
+    """A NaN, an infinity of either sign or both in Y or H, finite sums past bf16's range: which
+    elements are NaN and what the others are, for both kinds, with and without the first norm."""
+    K = 256
+    d = _norm_inputs(10, K, 12, post, "none", beta)
+    Y, H = _dev(d["Y"]), _dev(d["H"])
+    inf, big = float("inf"), 3.3e38
+    Y[1, 9], Y[2, 70], Y[3, 70] = float("nan"), inf, -inf
+    H[4, 9], H[5, 200], H[6, 200] = float("nan"), inf, -inf
+    H[7, 3], H[7, 250] = inf, -inf
+    Y[8, 40], H[8, 40] = big, big  # overflows without the first norm
+    h, q, s = B.block_norm_quant(Y, H, _dev(d["gamma"]), fmt, _dev(d["post_gamma"]), None, 1.0, _dev(d["beta"]),
+                                 _dev(d["post_beta"]), kind=kind)
+    v = q if fmt == "bf16" else B.mx_dequantize(q, s)
+    clean = d["beta"] if beta else np.zeros(K, np.float32)
+    if fmt != "bf16":
+        _, _, clean = _quant(clean[None], fmt)
+        clean = clean[0].astype(np.float32)
+    clean = torch.from_numpy(clean).to(DEV).bfloat16()
+    nan = torch.zeros((10, K), dtype=torch.bool, device=DEV)
+    hnan = nan.clone()
+    nan[1], nan[4] = True, True
+    hnan[1] = post
+    hnan[1, 9] = hnan[4, 9] = True
+    if post:  # the first norm's NaN (RMS: at the infinity; LayerNorm: the row) reaches all of h'
+        nan[2], nan[3] = True, True
+        for r in (2, 3):
+            hnan[r] = kind == "layer"
+            hnan[r, 70] = True
+    infs = {5: [200], 6: [200], 7: [3, 250]}
+    if not post:
+        infs.update({2: [70], 3: [70], 8: [40]})
+    step = 1 if fmt == "bf16" else 32
+    for r, at in infs.items():
+        if kind == "layer":
+            nan[r] = True
+        else:
+            for k in at:
+                nan[r, k // step * step:(k // step + 1) * step] = True
+            assert torch.equal(v[r][~nan[r]], clean[~nan[r]]), r
+    assert torch.equal(torch.isnan(v), nan)
+    assert torch.equal(torch.isnan(h), hnan)
+
+
 # ---------------------------------------------------------------------------- SiLU x up
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
