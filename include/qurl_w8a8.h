@@ -575,6 +575,18 @@ size_t qr_workspace_size(const char* fn, int64_t M, int64_t N, int64_t K, int qt
  */
 int qr_gemm_plan(int64_t M, int64_t N, int64_t K, int qt, int* tile, int* splitk, int* rows);
 
+/*
+ * qr_mxfp4_plan -- the same for qr_mxfp4_gemm with tokens of format xfmt:
+ *   *tile_n, *tile_m  weight rows and tokens of a block's tile; *tile_m = 0: the
+ *            kernel for few tokens, which has no token tiles,
+ *   *splits  number of K splits (1 = none),
+ *   *ahead   1 if blocks take several tiles each and copy into the next one ahead.
+ * qr_mxfp4_linear runs this product too, but where it is one launch.
+ * Pure host function; returns QR_OK or the product's error for the shape.
+ */
+int qr_mxfp4_plan(int64_t M, int64_t N, int64_t K, int xfmt, int* tile_n, int* tile_m, int* splits,
+                  int* ahead);
+
 /* Name of tile configuration `tile` (static string) or NULL if out of range. */
 const char* qr_tile_name(int tile);
 

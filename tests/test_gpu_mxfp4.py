@@ -878,6 +878,37 @@ def test_gemm_of_several_rounds_of_tiles(M, N, K, pad, fmt):
     assert bool((wide[:, N:] == 7.0).all())
 
 
+# With SHAPES, CONFIGS and SEVERAL: each tile of the planner's tables as a block a tile, split over K,
+# and with blocks of several tiles (rings of two, three and four slots); last stages half past K
+# (odd multiples of 128) and whole. tests/test_oracle_mxfp4.py holds the lists to that.
+SEVERAL = [(2100, 9000, 512), (2100, 9001, 640), (1030, 37888, 256), (530, 37890, 1280), (2600, 4608, 3584),
+           (8200, 4608, 128), (300, 70000, 384), (4200, 30000, 256)]
+PLANS = [(1, 41192, 896), (27, 41003, 1920), (3, 65588, 896), (38, 41740, 640), (66, 67775, 640), (93, 20712, 6016),
+         (129, 26174, 6400), (132, 21566, 1152), (140, 21714, 4096), (166, 21814, 3328), (173, 5463, 24064),
+         (278, 21280, 896), (395, 2914, 8832), (561, 28162, 1920), (592, 10315, 6400), (1234, 1050, 8320),
+         (1351, 719, 128), (3845, 129, 11776), (4642, 967, 6784), (6609, 647, 4608), (8622, 176, 3584)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K", PLANS)
+def test_gemm_of_every_plan(M, N, K, fmt):
+    """Accumulators against float64; bf16 outputs, in rows whose stride is a multiple of 8, of 2 and odd,
+    are their roundings and leave the padding alone."""
+    xc, xs, x = _random_operand(M, K, fmt, M + N)
+    wc, ws, w = _random_operand(N, K, "mxfp4", K)
+    raw = B.mxfp4_gemm(xc, xs, wc, ws, out="raw")
+    exact, size = x @ w.t(), x.abs() @ w.abs().t()
+    rel = (K / 32 + 64) * 2.0 ** -23 if fmt == "mxfp4" else (K / 8 + 64) * 2.0 ** -23 + E4M3_E2M1_CUT
+    assert bool(((raw.double() - exact).abs() <= rel * size).all())
+    want = raw.bfloat16()
+    up8 = (N + 15) // 8 * 8
+    for ld in (N, up8, up8 + 2, up8 + 1):
+        wide = torch.full((M + 1, ld), 7.0, dtype=torch.bfloat16, device=DEV)
+        B.mxfp4_gemm(xc, xs, wc, ws, Y=wide[:M, :N])
+        assert torch.equal(wide[:M, :N], want), ld
+        assert bool((wide[:, N:] == 7.0).all()) and bool((wide[M] == 7.0).all()), ld
+
+
 @pytest.mark.parametrize("M,N,K", [(16, 300, 512), (40, 200, 384), (901, 1090, 128), (300, 515, 8320), (1200, 900, 256)])
 def test_products_with_e4m3_tokens_are_cut_as_stated(M, N, K):
     """Accumulators are the sums of the cut products but for fp32 roundings: K / 8 group sums and 64

@@ -255,3 +255,39 @@ def test_gate_row_strides():
     for gate in (row, torch.zeros(shape), torch.zeros(128)[::2], torch.zeros(1).expand(64), torch.zeros((64, 4), dtype=torch.bfloat16).t()):
         with pytest.raises(ValueError):
             B._gate_ld(gate, shape)
+
+
+def test_plan_refusals(L):
+    out = [ctypes.byref(ctypes.c_int()) for _ in range(4)]
+    f = L.qr_mxfp4_plan
+    assert f(16, 256, 256, MX4, *out) == 0
+    assert f(16, 256, 256, 1, *out) == -1 and f(-1, 256, 256, MX4, *out) == -1
+    assert f(16, 256, 192, MX4, *out) == -2 and f(1 << 20, 1 << 18, 128, MX8, *out) == -2
+    for i in range(4):
+        assert f(16, 256, 256, MX4, *[None if j == i else o for j, o in enumerate(out)]) == -1
+    assert b"qr_mxfp4_plan" in L.qr_last_error()
+
+
+@pytest.mark.parametrize("x", ["fp4", "fp8"])
+def test_gpu_tests_run_every_plan(x):
+    """(tile, whether K is split, whether blocks take several tiles): each that a sweep of shapes
+    meets is that of a shape of the GPU tests."""
+    import test_gpu_mxfp4 as T
+    from w8a8_gemm_rl_amd import binding as B
+
+    def plan(M, N, K):
+        n, m, splits, ahead = B.mxfp4_plan(M, N, K, x)
+        return n, m, splits > 1, ahead
+
+    run = {plan(*s) for s in T.SHAPES + T.CONFIGS + T.PLANS + [s[:3] for s in T.SEVERAL]}
+    rng = np.random.default_rng(7)
+    met = set()
+    for a, b, c in rng.random((40000, 3)):
+        M, N, K = int(2 ** (13.2 * a)), int(2 ** (3 + 13.2 * b)), 128 * int(2 ** (7.6 * c))
+        if N * K < 1 << 31:
+            met.add(plan(M, N, K))
+    assert len(met) >= 18 and met <= run, sorted(met - run)
+    # one kernel without token tiles, and each tile with and without a split
+    tiles = {p[:2] for p in run if p[1]}
+    assert len(tiles) == (8 if x == "fp4" else 7) and any(p[1] == 0 for p in run)
+    assert all((n, m, s, False) in run for n, m in tiles for s in (False, True))

@@ -36,7 +36,7 @@ EXPORTS = [
     "qr_workspace_size", "qr_gemm_plan", "qr_tile_name", "qr_num_tiles", "qr_set_plan_override",
     "qr_set_small_m_override", "qr_set_fuse_override", "qr_last_error", "qr_version", "qr_probe_read", "qr_probe_mfma",
     "qr_probe_copy_stream", "qr_mxfp4_quantize", "qr_mx_dequantize", "qr_mxfp4_gemm", "qr_mxfp4_linear",
-    "qr_block_norm_quant", "qr_silu_mul_mx",
+    "qr_block_norm_quant", "qr_silu_mul_mx", "qr_mxfp4_plan",
 ]
 
 
@@ -76,6 +76,7 @@ _SIGS = {
     "qr_workspace_size": (_sz, [ctypes.c_char_p, _i64, _i64, _i64, _int]),
     "qr_gemm_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int), ctypes.POINTER(_int),
                             ctypes.POINTER(_int)]),
+    "qr_mxfp4_plan": (_int, [_i64, _i64, _i64, _int] + 4 * [ctypes.POINTER(_int)]),
     "qr_tile_name": (ctypes.c_char_p, [_int]),
     "qr_num_tiles": (_int, []),
     "qr_set_plan_override": (_int, [_int, _int, _int]),
@@ -658,6 +659,23 @@ def _mx4_workspace(fn, M, N, K, xfmt, like, ws):
     return ws.data_ptr(), need, ws
 
 
+def _tokens(x):
+    """QR_ACT_* format of an MXFP4 product's tokens."""
+    if x == "fp4":
+        return 3
+    if x == "fp8":
+        return 2
+    raise ValueError(f"x must be 'fp4' or 'fp8', got {x!r}")
+
+
+def mxfp4_plan(M, N, K, x="fp4"):
+    """(weight rows of a tile, tokens of a tile or 0 for the kernel of few tokens, K splits, whether
+    blocks copy into their next tile ahead): the plan mxfp4_gemm uses for this shape."""
+    n, m, s, a = (ctypes.c_int() for _ in range(4))
+    _check("qr_mxfp4_plan", lib().qr_mxfp4_plan(M, N, K, _tokens(x), *(ctypes.byref(v) for v in (n, m, s, a))))
+    return n.value, m.value, s.value, bool(a.value)
+
+
 def mxfp4_gemm(Xq, sx, Wq, sw, out="bf16", Y=None, ws=None):
     """Product of quantized tokens (uint8 MXFP4 or float8_e4m3fn block-wise codes [M, K] with
     their scale panels) with MXFP4 weights Wq [N, K/2]: bf16 Y [M, N] or the fp32 accumulators."""
@@ -681,12 +699,7 @@ def mxfp4_linear(X, Wq, sw, x="fp4", Y=None, ws=None):
     idx = _one_device(X.device, Wq, sw, Y, ws)
     if X.dtype != torch.bfloat16:
         raise ValueError("X must be bfloat16")
-    if x == "fp4":
-        xfmt = 3
-    elif x == "fp8":
-        xfmt = 2
-    else:
-        raise ValueError(f"x must be 'fp4' or 'fp8', got {x!r}")
+    xfmt = _tokens(x)
     ldx = _ld(X, "X")
     M, K = X.shape
     N, Kw, wfmt = _mx_codes(Wq, sw, "Wq")

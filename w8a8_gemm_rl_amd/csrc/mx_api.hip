@@ -160,6 +160,17 @@ int qr_mxfp4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq, c
               fn);
 }
 
+int qr_mxfp4_plan(int64_t M, int64_t N, int64_t K, int xfmt, int* tile_n, int* tile_m, int* splits,
+                  int* ahead) {
+  const char* fn = "qr_mxfp4_plan";
+  const int st = check_product(fn, M, N, K, xfmt);
+  if (st != QR_OK) return st;
+  if (!tile_n || !tile_m || !splits || !ahead)
+    return qr::set_error(QR_ERR_INVALID_ARG, "%s: null output pointer", fn);
+  qr::mx4_plan(M, N, K, xfmt, tile_n, tile_m, splits, ahead);
+  return done(hipSuccess, fn);
+}
+
 int qr_mxfp4_linear(const void* X, int64_t ldx, int xfmt, const void* Wq, const uint8_t* sw, int64_t M,
                     int64_t N, int64_t K, void* Y, int64_t ldy, void* workspace, size_t ws_bytes,
                     void* stream) {

@@ -786,6 +786,17 @@ __global__ __launch_bounds__(256) void mx4_sum_kernel(const float* __restrict__ 
   mx4_store4(p, m, n, a);
 }
 
+// Whether a product of `tiles` tiles takes one block a CU, each for every so many-th tile of
+// its XCD with copies running ahead, rather than a block a tile: where they fill more than
+// one round (stacked 7B gate and up at 512, 1024 and 2048 tokens 42.4, 80 and 153 us against
+// 44.8, 84.8 and 156; 8192 tokens of 7B QKV 78 against 83). Past five rounds that gains nothing
+// (32B gate at 4096, seven rounds: 309 against 306). `slots`: the ring's, 0 if none can hold a
+// token fragment of each wave's outputs.
+bool mx4_ahead(int64_t tiles, int64_t stages, int splits, int slots, int per_cu) {
+  const int64_t need = (tiles + 7) / 8 * 8, round = (int64_t)kCUs * per_cu;
+  return slots > 0 && splits == 1 && stages >= slots && need > round && need <= 5 * round;
+}
+
 template <bool XFP4, int T, int BN, int BM, int WN, int WM, int S, int KS>
 hipError_t launch_tile(const Mx4Params& g, int splits, int per_cu, float* part, hipStream_t st) {
   Mx4TileParams p;
@@ -799,22 +810,17 @@ hipError_t launch_tile(const Mx4Params& g, int splits, int per_cu, float* part, 
   // 4096 tokens of the stacked 7B gate and up (155 and 310 MB) 140 and 272 us against 152 and
   // 305, the 32B gate at 4096 275 against 299; 1024 tokens (78 MB) 87 against 83.
   p.nt_out = 2 * g.M * g.N > ((int64_t)128 << 20);
-  // A block takes one tile, or, where they fill more than one round and copies can run
-  // ahead, every so many-th of its XCD's (stacked 7B gate and up at 512, 1024 and 2048 tokens
-  // 42.4, 80 and 153 us against 44.8, 84.8 and 156; 8192 tokens of 7B QKV 78 against 83). Past
-  // five rounds that gains nothing (32B gate at 4096, seven rounds: 309 against 306).
-  const int64_t need = ((int64_t)p.tiles_m * p.tiles_n * splits + 7) / 8 * 8;
-  const int64_t round = kCUs * per_cu;
-  bool ahead = false;
-  if constexpr (Mx4Ahead<XFP4, T, BN, BM, WN, WM, KS>::value) {
-    ahead = splits == 1 && p.stages >= S && need > round && need <= 5 * round;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  constexpr bool kAhead = Mx4Ahead<XFP4, T, BN, BM, WN, WM, KS>::value;
+  const bool ahead = mx4_ahead(tiles, p.stages, splits, kAhead ? S : 0, per_cu);
+  if constexpr (kAhead) {
     if (ahead)
-      hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS, true>), dim3((unsigned)round),
+      hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS, true>), dim3((unsigned)(kCUs * per_cu)),
                          dim3(64 * WN * WM), 0, st, p);
   }
   if (!ahead)
-    hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS, false>), dim3((unsigned)need),
-                       dim3(64 * WN * WM), 0, st, p);
+    hipLaunchKernelGGL((mx4_tile_kernel<XFP4, T, BN, BM, WN, WM, S, KS, false>),
+                       dim3((unsigned)((tiles * splits + 7) / 8 * 8)), dim3(64 * WN * WM), 0, st, p);
   if (splits > 1) {
     const int64_t total = g.M * ((g.N + 3) >> 2);
     hipLaunchKernelGGL(mx4_sum_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, part, splits, g);
@@ -838,26 +844,32 @@ hipError_t launch_decode(const Mx4Params& p, const uint16_t* X, int64_t ldx, hip
 struct Mx4Config {
   int BN, BM, KS, per_cu;
   float base, alone, shared;
+  int slots;  // of a ring that can copy into the next tile, else 0
   hipError_t (*run)(const Mx4Params&, int, int, float*, hipStream_t);
 };
+template <bool XFP4, int T, int BN, int BM, int WN, int WM, int S, int KS>
+constexpr Mx4Config config(int per_cu, float base, float alone, float shared = 0.0f) {
+  return {BN, BM, KS, per_cu, base, alone, shared, Mx4Ahead<XFP4, T, BN, BM, WN, WM, KS>::value ? S : 0,
+          launch_tile<XFP4, T, BN, BM, WN, WM, S, KS>};
+}
 constexpr Mx4Config kFp4Configs[] = {
-    {256, 256, 256, 1, 8.0f, 2.00f, 0.0f, launch_tile<true, 32, 256, 256, 2, 4, 2, 256>},
-    {160, 256, 256, 1, 5.5f, 1.50f, 0.0f, launch_tile<true, 16, 160, 256, 2, 4, 2, 256>},
-    {160, 128, 256, 1, 5.0f, 0.87f, 0.0f, launch_tile<true, 16, 160, 128, 2, 4, 3, 256>},
-    {128, 128, 256, 1, 5.0f, 0.65f, 0.0f, launch_tile<true, 32, 128, 128, 2, 4, 4, 256>},
-    {160, 64, 256, 1, 4.5f, 0.65f, 0.0f, launch_tile<true, 16, 160, 64, 2, 4, 4, 256>},
-    {128, 64, 256, 1, 4.0f, 0.45f, 0.0f, launch_tile<true, 16, 128, 64, 4, 2, 4, 256>},
-    {64, 64, 256, 2, 4.4f, 0.31f, 0.44f, launch_tile<true, 16, 64, 64, 2, 2, 4, 256>},
-    {64, 32, 256, 2, 3.5f, 0.30f, 0.35f, launch_tile<true, 16, 64, 32, 4, 1, 4, 256>},
+    config<true, 32, 256, 256, 2, 4, 2, 256>(1, 8.0f, 2.00f),
+    config<true, 16, 160, 256, 2, 4, 2, 256>(1, 5.5f, 1.50f),
+    config<true, 16, 160, 128, 2, 4, 3, 256>(1, 5.0f, 0.87f),
+    config<true, 32, 128, 128, 2, 4, 4, 256>(1, 5.0f, 0.65f),
+    config<true, 16, 160, 64, 2, 4, 4, 256>(1, 4.5f, 0.65f),
+    config<true, 16, 128, 64, 4, 2, 4, 256>(1, 4.0f, 0.45f),
+    config<true, 16, 64, 64, 2, 2, 4, 256>(2, 4.4f, 0.31f, 0.44f),
+    config<true, 16, 64, 32, 4, 1, 4, 256>(2, 3.5f, 0.30f, 0.35f),
 };
 constexpr Mx4Config kFp8Configs[] = {
-    {256, 256, 128, 1, 8.0f, 1.42f, 0.0f, launch_tile<false, 32, 256, 256, 2, 4, 3, 128>},
-    {160, 256, 128, 1, 5.0f, 1.02f, 0.0f, launch_tile<false, 32, 160, 256, 1, 8, 3, 128>},
-    {160, 128, 256, 1, 4.0f, 1.40f, 0.0f, launch_tile<false, 16, 160, 128, 2, 4, 2, 256>},
-    {128, 128, 128, 1, 4.8f, 0.50f, 0.0f, launch_tile<false, 32, 128, 128, 2, 4, 4, 128>},
-    {160, 64, 256, 1, 4.8f, 0.68f, 0.0f, launch_tile<false, 16, 160, 64, 2, 4, 3, 256>},
-    {64, 64, 256, 1, 4.0f, 0.38f, 0.0f, launch_tile<false, 16, 64, 64, 2, 2, 3, 256>},
-    {64, 32, 256, 2, 3.8f, 0.31f, 0.42f, launch_tile<false, 16, 64, 32, 4, 1, 4, 256>},
+    config<false, 32, 256, 256, 2, 4, 3, 128>(1, 8.0f, 1.42f),
+    config<false, 32, 160, 256, 1, 8, 3, 128>(1, 5.0f, 1.02f),
+    config<false, 16, 160, 128, 2, 4, 2, 256>(1, 4.0f, 1.40f),
+    config<false, 32, 128, 128, 2, 4, 4, 128>(1, 4.8f, 0.50f),
+    config<false, 16, 160, 64, 2, 4, 3, 256>(1, 4.8f, 0.68f),
+    config<false, 16, 64, 64, 2, 2, 3, 256>(1, 4.0f, 0.38f),
+    config<false, 16, 64, 32, 4, 1, 4, 256>(2, 3.8f, 0.31f, 0.42f),
 };
 
 struct Mx4Plan {
@@ -939,6 +951,16 @@ hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const vo
   if (plan.c) return plan.c->run(p, plan.splits, plan.c->per_cu, static_cast<float*>(ws), st);
   return fp4 ? launch_decode<true, false, 8, 8, 4>(p, nullptr, 0, st)
              : launch_decode<false, false, 8, 8, 4>(p, nullptr, 0, st);
+}
+
+void mx4_plan(int64_t M, int64_t N, int64_t K, int xfmt, int* tile_n, int* tile_m, int* splits, int* ahead) {
+  const Mx4Plan plan = make_mx4_plan(M, N, K, xfmt == kActMxFp4);
+  const Mx4Config* c = plan.c;
+  *tile_n = c ? c->BN : 16;
+  *tile_m = c ? c->BM : 0;
+  *splits = plan.splits;
+  *ahead = c && mx4_ahead(((M + c->BM - 1) / c->BM) * ((N + c->BN - 1) / c->BN), (K + c->KS - 1) / c->KS,
+                          plan.splits, c->slots, c->per_cu);
 }
 
 size_t mx4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int xfmt) {

@@ -40,6 +40,7 @@ hipError_t launch_mx4_quant(const void* A, int64_t R, int64_t K, int64_t lda, in
                             void* codes, uint8_t* scales, hipStream_t st);
 hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int fmt,
                              void* out, int64_t ldo, int bf16, hipStream_t st);
+void mx4_plan(int64_t M, int64_t N, int64_t K, int xfmt, int* tile_n, int* tile_m, int* splits, int* ahead);
 size_t mx4_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, int xfmt);
 hipError_t launch_mx4_gemm(const void* Xq, const uint8_t* sx, int xfmt, const void* Wq,
                            const uint8_t* sw, int64_t M, int64_t N, int64_t K, int out_raw, void* Y,
