@@ -744,6 +744,25 @@ def test_binding_refusals_on_device_tensors():
         B.block_norm_quant(x, buf[:, :128], torch.ones(128, device=DEV), "mxfp4", Hout=buf[:, 32:])
 
 
+@pytest.mark.parametrize("x", ["fp4", "fp8"])
+@pytest.mark.parametrize("M,N,K", [(33, 512, 18944), (256, 3584, 18944), (300, 640, 256)])
+def test_products_in_a_workspace_of_the_caller(M, N, K, x):
+    """As many bytes as workspace_size says are enough, are left alone past that, and one buffer serves
+    call after call; a byte less is refused."""
+    X = to_dev_bf16(_acts(M, K, 3))
+    _, w, sw = _weights(N, K, 4)
+    xq, sx = B.mxfp4_quantize(X) if x == "fp4" else B.mx_quantize(X)
+    for fn, call in (("qr_mxfp4_gemm", lambda ws: B.mxfp4_gemm(xq, sx, w, sw, ws=ws)),
+                     ("qr_mxfp4_linear", lambda ws: B.mxfp4_linear(X, w, sw, x=x, ws=ws))):
+        need, want = B.workspace_size(fn, M, N, K, x), call(None)
+        buf = torch.full((need + 256,), 7, dtype=torch.uint8, device=DEV)
+        assert all(torch.equal(call(buf[:need]), want) for _ in range(3))
+        assert bool((buf[need:] == 7).all())
+        if need:
+            with pytest.raises(B.QRError, match="workspace"):
+                call(buf[:need - 1])
+
+
 def test_outputs_whose_rows_share_memory_are_refused():
     x = torch.zeros((4, 128), dtype=torch.bfloat16, device=DEV)
     w, sw = B.mxfp4_quantize(torch.zeros((16, 128), device=DEV))

@@ -216,7 +216,10 @@ def gemm_plan(M, N, K, qt):
 
 
 def workspace_size(fn, M, N, K, qt):
-    r = lib().qr_workspace_size(fn.encode(), M, N, K, _qt(qt))
+    """Bytes of workspace `fn` takes for a shape; qt is "int8" or "fp8", for the MXFP4 products the
+    tokens' "fp4" or "fp8"."""
+    qt = _tokens(qt) if fn in ("qr_mxfp4_gemm", "qr_mxfp4_linear") else _qt(qt)
+    r = lib().qr_workspace_size(fn.encode(), M, N, K, qt)
     if r == ctypes.c_size_t(-1).value:
         raise QRError("qr_workspace_size", -1, lib().qr_last_error().decode())
     return r
@@ -678,7 +681,8 @@ def mxfp4_plan(M, N, K, x="fp4"):
 
 def mxfp4_gemm(Xq, sx, Wq, sw, out="bf16", Y=None, ws=None):
     """Product of quantized tokens (uint8 MXFP4 or float8_e4m3fn block-wise codes [M, K] with
-    their scale panels) with MXFP4 weights Wq [N, K/2]: bf16 Y [M, N] or the fp32 accumulators."""
+    their scale panels) with MXFP4 weights Wq [N, K/2]: bf16 Y [M, N] or the fp32 accumulators.
+    `ws`, if given, holds workspace_size("qr_mxfp4_gemm", ...) bytes, 256-byte aligned."""
     idx = _one_device(Xq.device, sx, Wq, sw, Y, ws)
     M, K, xfmt = _mx_codes(Xq, sx, "Xq")
     N, Kw, wfmt = _mx_codes(Wq, sw, "Wq")
@@ -695,7 +699,7 @@ def mxfp4_gemm(Xq, sx, Wq, sw, out="bf16", Y=None, ws=None):
 
 def mxfp4_linear(X, Wq, sw, x="fp4", Y=None, ws=None):
     """One rollout linear with MXFP4 weights: bf16 X [M, K] (any row stride) quantized block-wise
-    to `x` ("fp4" or "fp8"), product, bf16 Y [M, N]."""
+    to `x` ("fp4" or "fp8"), product, bf16 Y [M, N]. `ws` as for mxfp4_gemm ("qr_mxfp4_linear")."""
     idx = _one_device(X.device, Wq, sw, Y, ws)
     if X.dtype != torch.bfloat16:
         raise ValueError("X must be bfloat16")
