@@ -78,9 +78,11 @@ __device__ __forceinline__ void mx_values8(const uint2 q, uint32_t sb, float* v)
 }
 
 // Values of rows [row0, row0 + w.rows), two chunks of eight a thread (18944 x 3584 to bf16:
-// 27.8 us from E2M1, 31.0 from E4M3, 6.2 and 6.6 TB/s; one or four chunks a thread cost 2 us
-// more). NT: values past the L2s' 32 MB leave non-temporally (29.3 and 32.2 us otherwise; 1001
-// x 27648 12.9 against 15.3); fewer stay there for whoever reads them.
+// 28.4 us from E2M1, 31.9 from E4M3, 6.1 and 6.4 TB/s; one or four chunks a thread cost 2 us
+// more). NT: bf16 values past the L2s' 32 MB leave non-temporally (1.2 - 1.5 us more otherwise; 1001
+// x 27648 12.9 against 15.3); fewer stay there for whoever reads them. A chunk of fp32 values is
+// two stores of half a 32-byte piece each, which non-temporally reach memory as such (18944 x 3584
+// 108 us from E2M1 against 79, 4096 x 5120 33 against 23): those leave as ordinary stores.
 template <bool FP4, bool BF16, bool NT>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scales,
@@ -106,18 +108,17 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restri
     if (i0 + u * 256u >= total) break;
     float v[8];
     mx_values8<FP4>(q[u], sb[u], v);
-    auto put = [](auto val, auto* to) {
-      if constexpr (NT) __builtin_nontemporal_store(val, to);
-      else *to = val;
-    };
     if constexpr (BF16) {
       typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-      put(u4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])},
-          reinterpret_cast<u4*>(static_cast<uint16_t*>(out) + row[u] * ldo + 8 * c[u]));
+      const u4 b = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+      u4* o = reinterpret_cast<u4*>(static_cast<uint16_t*>(out) + row[u] * ldo + 8 * c[u]);
+      if constexpr (NT) __builtin_nontemporal_store(b, o);
+      else *o = b;
     } else {
+      static_assert(!NT, "half pieces");
       v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(out) + row[u] * ldo + 8 * c[u]);
-      put(v4f{v[0], v[1], v[2], v[3]}, o);
-      put(v4f{v[4], v[5], v[6], v[7]}, o + 1);
+      o[0] = v4f{v[0], v[1], v[2], v[3]};
+      o[1] = v4f{v[4], v[5], v[6], v[7]};
     }
   }
 }
@@ -926,17 +927,17 @@ hipError_t launch_mx4_quant(const void* A, int64_t R, int64_t K, int64_t lda, in
 hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int fmt,
                              void* out, int64_t ldo, int bf16, hipStream_t st) {
   const uint8_t* q = static_cast<const uint8_t*>(codes);
-  const bool nt = (bf16 ? 2 : 4) * (double)R * (double)K > 32.0 * 1048576.0;
   auto run = [&](auto fp4, auto to_bf16, auto past_l2) {
     return chunk_launches(R, K >> 3, 2, [&](int64_t r, ChunkWalk w, dim3 g) {
       hipLaunchKernelGGL((mx_dequant_kernel<decltype(fp4)::value, decltype(to_bf16)::value, decltype(past_l2)::value>),
                          g, dim3(256), 0, st, q, scales, R, K, out, ldo, r, w);
     });
   };
-  auto by_size = [&](auto fp4, auto to_bf16) {
-    return nt ? run(fp4, to_bf16, std::true_type{}) : run(fp4, to_bf16, std::false_type{});
+  auto by_type = [&](auto fp4) {
+    if (!bf16) return run(fp4, std::false_type{}, std::false_type{});
+    if (2.0 * (double)R * (double)K > 32.0 * 1048576.0) return run(fp4, std::true_type{}, std::true_type{});
+    return run(fp4, std::true_type{}, std::false_type{});
   };
-  auto by_type = [&](auto fp4) { return bf16 ? by_size(fp4, std::true_type{}) : by_size(fp4, std::false_type{}); };
   return fmt == kActMxFp4 ? by_type(std::true_type{}) : by_type(std::false_type{});
 }
 
