@@ -297,15 +297,19 @@ __global__ __launch_bounds__(64 * NW) void mx4_decode_kernel(const Mx4Params p,
 // contiguous part of its tile's stages and writes fp32 partial sums, which
 // mx4_sum_kernel adds in a fixed order.
 //
-// Stacked 7B gate and up, 75 MB of codes and scales in and out at 33 E4M3 tokens: 15.4 us,
-// 4.9 TB/s, what a copy reaches. At 256 E2M1 tokens 93 MB take 26 us: 237 tiles of
-// 160 x 256, one round. The 32B gate at 4096 E2M1 tokens: 275 - 300 us, 3.9 - 4.2 PFLOP/s
-// (cards differ, and their clock under load). There, on 256 x 256 tiles, 20 stages in seven rounds, the products alone take 160 us (the
+// Stacked 7B gate and up, 75 MB of codes and scales in and out at 33 E4M3 tokens: 15.0 us,
+// 5.0 TB/s, what a copy reaches. At 256 E2M1 tokens 93 MB take 26 us: 237 tiles of
+// 160 x 256, one round (E4M3 tokens 35). The 32B gate at 4096 E2M1 tokens: 289 - 298 us, 3.9 -
+// 4.0 PFLOP/s (two cards, call after call; 310 - 316 in the first dozen), with E4M3 tokens 424.
+// There, on 256 x 256 tiles, 20 stages in seven rounds, the products alone take 160 us (the
 // clock falls to 1.93 GHz), a fragment's LDS reads alone 164, the copies alone 193 (20 bytes
-// a clock and CU; 127 from the L2), any two together 205, all three 250; filling the ring
-// and storing the outputs add 25 - 35. Measured slower there: a third operand buffer with
+// a clock and CU; 127 from the L2), any two together 205, all three 250; the rest fills the ring
+// and stores the outputs. Measured slower there: a third operand buffer with
 // refills a step earlier, 64-byte rows with deeper rings, four waves of 128 x 128, wave
 // priorities, non-temporal weight copies, other groupings of tiles.
+//
+// fp32 outputs and partial sums leave straight from the fragments, 16 bytes a lane (gate and
+// up at 256 tokens 34 us with E2M1, 39 with E4M3; the 32B gate at 4096 about 400 and 520).
 // ---------------------------------------------------------------------------
 // One copy of LANES lanes' 16 bytes (a power of two), exec being all ones before and after.
 // The wait state between the write of M0 and the copy (qr_copy.h) is an s_nop, or the write
@@ -789,10 +793,12 @@ __global__ __launch_bounds__(256) void mx4_sum_kernel(const float* __restrict__ 
 
 // Whether a product of `tiles` tiles takes one block a CU, each for every so many-th tile of
 // its XCD with copies running ahead, rather than a block a tile: where they fill more than
-// one round (stacked 7B gate and up at 512, 1024 and 2048 tokens 42.4, 80 and 153 us against
-// 44.8, 84.8 and 156; 8192 tokens of 7B QKV 78 against 83). Past five rounds that gains nothing
-// (32B gate at 4096, seven rounds: 309 against 306). `slots`: the ring's, 0 if none can hold a
-// token fragment of each wave's outputs.
+// one round. On one card, both in turn, three sets of operands: stacked 7B gate and up at 512,
+// 1024 and 2048 E2M1 tokens 51.0, 100 and 144 us against 52.4, 105 and 146; 8192 tokens of 7B QKV
+// 84 against 89; 38 E4M3 tokens of 41740 x 3584 25.7 against 27.2. Past five rounds that gains
+// nothing (32B gate at 4096, seven rounds: 309 against 306). These kernels keep state across tiles
+// that the scalar registers do not hold: 18 to 77 of them (256 x 256) are kept in vector lanes.
+// `slots`: the ring's, 0 if none can hold a token fragment of each wave's outputs.
 bool mx4_ahead(int64_t tiles, int64_t stages, int splits, int slots, int per_cu) {
   const int64_t need = (tiles + 7) / 8 * 8, round = (int64_t)kCUs * per_cu;
   return slots > 0 && splits == 1 && stages >= slots && need > round && need <= 5 * round;
@@ -807,9 +813,10 @@ hipError_t launch_tile(const Mx4Params& g, int splits, int per_cu, float* part, 
   p.tiles_n = (int)((g.N + BN - 1) / BN);
   p.stages = (int)((g.K + KS - 1) / KS);
   p.splits = splits;
-  // Outputs past half the 256 MB of the memory-side cache leave it to the operands: 2048 and
-  // 4096 tokens of the stacked 7B gate and up (155 and 310 MB) 140 and 272 us against 152 and
-  // 305, the 32B gate at 4096 275 against 299; 1024 tokens (78 MB) 87 against 83.
+  // Outputs past half the 256 MB of the memory-side cache leave it to the operands. On one card,
+  // with and without in turn, three sets of operands: 2048 and 4096 E2M1 tokens of the stacked 7B
+  // gate and up (155 and 310 MB) 144 and 291 us against 157 and 327, the 32B gate at 4096 290
+  // against 319 (E4M3 tokens 424 against 439); at 1024 tokens (78 MB) the hint cost 5%.
   p.nt_out = 2 * g.M * g.N > ((int64_t)128 << 20);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   constexpr bool kAhead = Mx4Ahead<XFP4, T, BN, BM, WN, WM, KS>::value;
