@@ -36,6 +36,8 @@
  *            epilogue store four outputs at a time).
  * Ownership  The caller allocates and owns every buffer, including the
  *            workspace. The library never allocates, frees or synchronizes.
+ * Overlap    Arrays that a call writes share no memory with its other arrays,
+ *            unless the call says that they may.
  * Streams    `stream` is a hipStream_t passed as void* (NULL = the null
  *            stream). Every call only enqueues work on it and returns.
  * Errors     Arguments are validated on the host before anything is

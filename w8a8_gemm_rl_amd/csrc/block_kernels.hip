@@ -196,8 +196,8 @@ __device__ __forceinline__ void norm_row(float (&v)[MAXC][8], const Live& live, 
 }
 
 // One row per block of tpr threads, held in registers, so one pass over memory: K <= 8 MAXC
-// tpr. 4096 x 5120 to INT8: 35 us with RMS (147 MB, 4.2 TB/s), 47 with LayerNorm, biases and a
-// gate per token (189 MB, 4.0 TB/s; 5 us of it the four parameter rows, 80 KB that each
+// tpr. 4096 x 5120 to INT8: 35 us with RMS (147 MB, 4.2 TB/s), 47 - 50 with LayerNorm, biases
+// and a gate per token (189 MB, 3.8 - 4.0 TB/s; 5 us of it the four parameter rows, 80 KB that each
 // block reads from the L2). Two or four rows a block, which share those, took 44 (RMS with
 // biases and gate; 48 here) and 54 us (LayerNorm). The residual row
 // is loaded with the block's output, but with four chunks a thread after the post norm. At
