@@ -244,6 +244,68 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
                     void* stream);
 
 /*
+ * Losses over a large vocabulary, beside qr_acr_tis_loss on the trainer's side: from the
+ * last hidden states and the head's weights to per-token losses and back, in pieces of
+ * the vocabulary; the logits are never held whole. qr_vocab_logp gives the
+ * log-probabilities that qr_acr_tis_loss takes, and qr_vocab_logp_grad takes the
+ * gradient that it gives.
+ *
+ *   z[t,v]  = scale * sum_k X[t,k] W[v,k]     (bf16 products, fp32 sums)
+ *   lse[t]  = log sum_v exp(z[t,v])            (fp32 over 256 ids, then float64)
+ *
+ * qr_vocab_logp -- softmax cross entropy (its negative): logp[t] = z[t, target[t]] - lse[t].
+ *   A target outside [0, N) masks its token: logp and lse are 0 there.
+ * qr_vocab_logp_grad -- with g = dlogp:
+ *   G[t,v]  = scale g[t] ([v = target[t]] - exp(z[t,v] - lse[t])), rounded to bf16
+ *   dX[t,:] = bf16_rne(sum_v G[t,v] W[v,:]),  dW[v,:] = bf16_rne(sum_t G[t,v] X[t,:])
+ *   (fp32 sums). Masked tokens: a zero row of dX, no part in dW, whatever X, lse and
+ *   g hold there.
+ *
+ * qr_vocab_distill -- divergence from a teacher whose top logits are known. Entry j of
+ *   token t is the id index[t,j] with the teacher's logit teacher[t,j]; ids outside
+ *   [0, N) are no entries (lists shorter than L), and a token without entries is masked:
+ *   loss and lse are 0 there.
+ *   p[t,j]  = exp(scale teacher[t,j]) / sum over the token's entries, or, with
+ *             teacher_lse, exp(scale teacher[t,j] - teacher_lse[t]) (the teacher's own
+ *             sum at this scale, over its whole vocabulary)
+ *   loss[t] = sum_j p[t,j] (log p[t,j] - (z[t, index[t,j]] - lse[t]));  p = 0 adds 0
+ *   The same id twice counts as two entries. All entries at -inf: every p is 0.
+ * qr_vocab_distill_grad -- with g = dloss and P[t] = sum_j p[t,j]:
+ *   G[t,v]  = scale g[t] (P[t] exp(z[t,v] - lse[t]) - sum_j p[t,j] [v = index[t,j]]),
+ *   rounded to bf16, and dX, dW from it as above.
+ *
+ * All results are the same bits on every run.
+ *
+ *   X        [M, ldx] bf16 hidden states, W [N, ldw] bf16 head (read); rows on 16-byte
+ *            boundaries, strides at most 2^21. M and N at most 2^22, N >= 1, K a multiple
+ *            of 8 in [8, 65536].
+ *   scale    finite, > 0: the logits' scale, 1 / temperature.
+ *   target   [M] int64;  index [M, L] int64, 1 <= L <= 1024;  teacher [M, L] fp32
+ *            (teacher_bf16 = 0) or bf16 (1);  teacher_lse NULL or [M] fp32 (read).
+ *   logp, loss, lse  [M] fp32 (written). The gradients read the lse of their forward call.
+ *   dX       NULL or [M, lddx], dW NULL or [N, lddw] bf16 (written, not accumulated); one
+ *            of them at least.
+ *   workspace  qr_workspace_size(fn, M, N, K, L) bytes (L is ignored for the logp
+ *            functions), 256-byte aligned, contents irrelevant.
+ * Hidden states of tokens that are not masked, weights and teacher logits (but for -inf)
+ * must be finite: else the results of that token, and gradients, are unspecified.
+ */
+int qr_vocab_logp(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                  const int64_t* target, float scale, float* logp, float* lse, void* workspace, size_t ws_bytes,
+                  void* stream);
+int qr_vocab_logp_grad(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                       const int64_t* target, float scale, const float* lse, const float* dlogp, void* dX,
+                       int64_t lddx, void* dW, int64_t lddw, void* workspace, size_t ws_bytes, void* stream);
+int qr_vocab_distill(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                     const int64_t* index, const void* teacher, int teacher_bf16, const float* teacher_lse,
+                     int64_t L, float scale, float* loss, float* lse, void* workspace, size_t ws_bytes,
+                     void* stream);
+int qr_vocab_distill_grad(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                          const int64_t* index, const void* teacher, int teacher_bf16, const float* teacher_lse,
+                          int64_t L, float scale, const float* lse, const float* dloss, void* dX, int64_t lddx,
+                          void* dW, int64_t lddw, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * qr_mx_quantize -- block-wise FP8: every 32 consecutive elements of a row
  * share one power-of-two scale (the block-wise FP8 variant the pages cite,
  * [fugumt] "Related papers"; block of 32 with E8M0 scales as the gfx950
@@ -560,7 +622,8 @@ int qr_linear_fused_noalloc(const void* X, int64_t ldx, float act_mult, const vo
  * qr_workspace_size -- bytes of workspace needed by `fn` ("qr_w8a8_gemm",
  * "qr_w8a8_gemm_quant" or "qr_linear_fused") for this shape; 0 if none. For "qr_acr_tis_loss" M is
  * the token count n (N, K and qt are ignored); for "qr_mxfp4_gemm" and
- * "qr_mxfp4_linear" qt is the tokens' format (QR_ACT_MXFP4 or QR_ACT_MXFP8). Pure
+ * "qr_mxfp4_linear" qt is the tokens' format (QR_ACT_MXFP4 or QR_ACT_MXFP8), for the
+ * "qr_vocab_..." functions the list length L. Pure
  * host function: it
  * depends only on its arguments (and on qr_set_plan_override). Returns
  * (size_t)-1 for an unknown fn or invalid sizes.

@@ -65,6 +65,10 @@ from .qurl import (
     requantize_weights,
     flip_expectation,
     decode_chain,
+    vocab_lists,
+    vocab_logits,
+    vocab_loss,
+    vocab_grad,
 )
 
 __all__ = [
@@ -78,4 +82,5 @@ __all__ = [
     "e2m1_decode", "e2m1_encode", "mxfp4_exponent", "mxfp4_quantize_rows", "mxfp4_pack", "mx_values",
     "block_norm",
     "decode_chain",
+    "vocab_lists", "vocab_logits", "vocab_loss", "vocab_grad",
 ]

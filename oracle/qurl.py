@@ -571,3 +571,66 @@ def block_norm(Y_bits, H_bits, gamma, post_gamma=None, gate=None, res=1.0, beta=
     hb = f32_to_bf16_bits((h + n).astype(np.float32))
     z, _ = norm_folded(hb, gamma, beta, eps, kind)
     return hb, z
+
+
+# ----------------------------------------------------------------------------
+# Losses over a large vocabulary (hidden states X [M, K], head W [N, K]), in float64
+# ----------------------------------------------------------------------------
+
+def vocab_lists(target=None, index=None, teacher=None, teacher_lse=None, scale=1.0, N=0):
+    """(ids [M, L], p [M, L], live [M]): the weighted ids of each token. A log-probability has one
+    id of weight 1; a distillation list the teacher's softmax over its entries, or
+    exp(scale * teacher - teacher_lse). Ids outside [0, N) are no entries (weight 0); tokens without
+    entries are not live. Entries all at -inf have weight 0."""
+    ids = np.asarray(target if index is None else index, np.int64)
+    ids = ids[:, None] if index is None else ids
+    ok = (ids >= 0) & (ids < N)
+    if index is None:
+        return ids, ok.astype(np.float64), ok.any(axis=1)
+    s = np.where(ok, np.asarray(teacher, np.float64) * float(scale), -np.inf)
+    if teacher_lse is not None:
+        shift = np.asarray(teacher_lse, np.float64)[:, None]
+        p = np.where(ok, np.exp(np.where(ok, s, 0.0) - np.where(ok, shift, 0.0)), 0.0)
+        return ids, p, ok.any(axis=1)
+    top = s.max(axis=1, keepdims=True)
+    e = np.where(np.isneginf(s), 0.0, np.exp(s - np.where(np.isneginf(top), 0.0, top)))
+    total = e.sum(axis=1, keepdims=True)
+    return ids, e / np.where(total == 0, 1.0, total), ok.any(axis=1)
+
+
+def vocab_logits(X, W, scale):
+    """(z [M, N], lse [M]) in float64."""
+    z = float(scale) * (np.asarray(X, np.float64) @ np.asarray(W, np.float64).T)
+    top = z.max(axis=1)
+    return z, top + np.log(np.exp(z - top[:, None]).sum(axis=1))
+
+
+def vocab_loss(X, W, scale=1.0, **lists):
+    """(value [M], lse [M]) of tokens: z[target] - lse with `target`, with `index` and `teacher`
+    sum_j p_j (log p_j - (z[index_j] - lse)); zeros for tokens that are not live, whatever their
+    rows of X hold."""
+    N = np.asarray(W).shape[0]
+    ids, p, live = vocab_lists(scale=scale, N=N, **lists)
+    z, lse = vocab_logits(np.where(live[:, None], X, 0.0), W, scale)
+    zi = np.take_along_axis(z, ids.clip(0, N - 1), axis=1) - lse[:, None]
+    if lists.get("index") is None:
+        value = zi[:, 0]
+    else:
+        value = np.where(p > 0, p * (np.log(np.where(p > 0, p, 1.0)) - zi), 0.0).sum(axis=1)
+    return np.where(live, value, 0.0), np.where(live, lse, 0.0)
+
+
+def vocab_grad(X, W, g, scale=1.0, lse=None, **lists):
+    """(dX [M, K], dW [N, K], G [M, N]) for the incoming gradient g [M] of vocab_loss's values:
+    G = d objective / d (X W^T). `lse` as a call is given it (None: computed)."""
+    N = np.asarray(W).shape[0]
+    ids, p, live = vocab_lists(scale=scale, N=N, **lists)
+    Xl = np.where(live[:, None], np.asarray(X, np.float64), 0.0)
+    z, own = vocab_logits(Xl, W, scale)
+    lse = own if lse is None else np.where(live, np.asarray(lse, np.float64), 0.0)
+    sign = 1.0 if lists.get("index") is not None else -1.0
+    G = p.sum(axis=1, keepdims=True) * np.exp(np.where(live[:, None], z - lse[:, None], 0.0))
+    for t in range(G.shape[0]):
+        np.add.at(G[t], ids[t].clip(0, N - 1), -p[t])
+    G *= (sign * float(scale) * np.where(live, np.asarray(g, np.float64), 0.0))[:, None]
+    return G @ np.asarray(W, np.float64), G.T @ Xl, G

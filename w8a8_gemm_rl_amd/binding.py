@@ -36,7 +36,8 @@ EXPORTS = [
     "qr_workspace_size", "qr_gemm_plan", "qr_tile_name", "qr_num_tiles", "qr_set_plan_override",
     "qr_set_small_m_override", "qr_set_fuse_override", "qr_last_error", "qr_version", "qr_probe_read", "qr_probe_mfma",
     "qr_probe_copy_stream", "qr_mxfp4_quantize", "qr_mx_dequantize", "qr_mxfp4_gemm", "qr_mxfp4_linear",
-    "qr_block_norm_quant", "qr_silu_mul_mx", "qr_mxfp4_plan",
+    "qr_block_norm_quant", "qr_silu_mul_mx", "qr_mxfp4_plan", "qr_vocab_logp", "qr_vocab_logp_grad",
+    "qr_vocab_distill", "qr_vocab_distill_grad",
 ]
 
 
@@ -67,6 +68,13 @@ _SIGS = {
     "qr_block_norm_quant": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _i64, _f32, _vp,
                                    _vp, _f32, _int, _vp, _i64, _vp, _vp, _vp]),
     "qr_silu_mul_mx": (_int, [_vp, _vp, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp]),
+    "qr_vocab_logp": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "qr_vocab_logp_grad": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _f32, _vp, _vp, _vp, _i64, _vp,
+                                  _i64, _vp, _sz, _vp]),
+    "qr_vocab_distill": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _int, _vp, _i64, _f32, _vp,
+                                _vp, _vp, _sz, _vp]),
+    "qr_vocab_distill_grad": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _int, _vp, _i64, _f32,
+                                     _vp, _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
     "qr_w8a8_gemm": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _sz, _vp]),
     "qr_w8a8_gemm_quant": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _i64, _i64, _i64,
                                   _f32, _vp, _vp, _vp, _sz, _vp]),
@@ -217,8 +225,11 @@ def gemm_plan(M, N, K, qt):
 
 def workspace_size(fn, M, N, K, qt):
     """Bytes of workspace `fn` takes for a shape; qt is "int8" or "fp8", for the MXFP4 products the
-    tokens' "fp4" or "fp8"."""
-    qt = _tokens(qt) if fn in ("qr_mxfp4_gemm", "qr_mxfp4_linear") else _qt(qt)
+    tokens' "fp4" or "fp8", for the losses over a vocabulary the list length L (1 for the logp calls)."""
+    if fn in ("qr_mxfp4_gemm", "qr_mxfp4_linear"):
+        qt = _tokens(qt)
+    elif not fn.startswith("qr_vocab_"):
+        qt = _qt(qt)
     r = lib().qr_workspace_size(fn.encode(), M, N, K, qt)
     if r == ctypes.c_size_t(-1).value:
         raise QRError("qr_workspace_size", -1, lib().qr_last_error().decode())
@@ -789,6 +800,116 @@ def silu_mul_mx(G, U, fmt, codes=None, scales=None):
     _call("qr_silu_mul_mx", idx, G.data_ptr(), U.data_ptr(), M, N, ldg, ldu, ACT[fmt], codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
+
+
+# ----------------------------------------------------------------------------
+# Losses over a large vocabulary
+# ----------------------------------------------------------------------------
+
+def _head_args(X, W):
+    """(M, N, K, row strides) of bf16 hidden states X [M, K] and head W [N, K]."""
+    if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise ValueError("X and W must be bfloat16")
+    ldx, ldw = _ld(X, "X"), _ld(W, "W")
+    if W.shape[1] != X.shape[1]:
+        raise ValueError("X and W disagree on K")
+    return X.shape[0], W.shape[0], X.shape[1], ldx, ldw
+
+
+def _per_token(t, M, dtype, name):
+    if t.dtype != dtype or t.shape != (M,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {M} entries")
+
+
+def _list_args(index, teacher, teacher_lse, M):
+    """Entries of a token's list."""
+    if index.dtype != torch.int64 or index.dim() != 2 or index.shape[0] != M or not index.is_contiguous():
+        raise ValueError("index must be a contiguous int64 tensor [M, L]")
+    if teacher.dtype not in (torch.float32, torch.bfloat16) or teacher.shape != index.shape \
+            or not teacher.is_contiguous():
+        raise ValueError("teacher must be a contiguous float32 or bfloat16 tensor of index's shape")
+    if teacher_lse is not None:
+        _per_token(teacher_lse, M, torch.float32, "teacher_lse")
+    return index.shape[1]
+
+
+def _grads(X, W, need_dX, need_dW, dX, dW):
+    """Gradient outputs and their row strides."""
+    out = []
+    for t, like, need, name in ((dX, X, need_dX, "dX"), (dW, W, need_dW, "dW")):
+        if t is None and need:
+            t = like.new_empty(like.shape)
+        elif t is not None and (t.shape != like.shape or t.dtype != torch.bfloat16):
+            raise ValueError(f"{name} must be bfloat16 of the shape of its tensor")
+        out += [t, like.shape[1] if t is None else _ld(t, name)]
+    if out[0] is None and out[2] is None:
+        raise ValueError("neither dX nor dW asked for")
+    return out
+
+
+def vocab_logp(X, W, target, scale=1.0, logp=None, lse=None, ws=None):
+    """Log-probabilities of one id per token, without the logits: X [M, K] bf16 hidden states, W [N, K]
+    bf16 head (rows contiguous, any row strides), target int64 [M] -> (logp fp32 [M], lse fp32 [M]);
+    logits are scale * X W^T. Targets outside [0, N) mask their tokens (0). `ws`, if given, holds
+    workspace_size("qr_vocab_logp", M, N, K, 1) bytes, 256-byte aligned."""
+    idx = _one_device(X.device, W, target, logp, lse, ws)
+    M, N, K, ldx, ldw = _head_args(X, W)
+    _per_token(target, M, torch.int64, "target")
+    logp, lse = _out(logp, X, (M,), torch.float32, "logp"), _out(lse, X, (M,), torch.float32, "lse")
+    wsp, wsb, ws = _mx4_workspace("qr_vocab_logp", M, N, K, 1, X, ws)
+    _call("qr_vocab_logp", idx, X.data_ptr(), ldx, W.data_ptr(), ldw, M, N, K, target.data_ptr(), scale,
+          logp.data_ptr(), lse.data_ptr(), wsp, wsb)
+    return logp, lse
+
+
+def vocab_logp_grad(X, W, target, lse, dlogp, scale=1.0, need_dX=True, need_dW=True, dX=None, dW=None, ws=None):
+    """Gradient of vocab_logp: with its lse and dlogp = d loss / d logp (fp32 [M]) -> (dX [M, K],
+    dW [N, K]) in bf16, None where not needed. Given dX and dW are overwritten (any row strides).
+    `ws` as for vocab_logp ("qr_vocab_logp_grad")."""
+    idx = _one_device(X.device, W, target, lse, dlogp, dX, dW, ws)
+    M, N, K, ldx, ldw = _head_args(X, W)
+    _per_token(target, M, torch.int64, "target")
+    _per_token(lse, M, torch.float32, "lse")
+    _per_token(dlogp, M, torch.float32, "dlogp")
+    dX, lddx, dW, lddw = _grads(X, W, need_dX, need_dW, dX, dW)
+    wsp, wsb, ws = _mx4_workspace("qr_vocab_logp_grad", M, N, K, 1, X, ws)
+    _call("qr_vocab_logp_grad", idx, X.data_ptr(), ldx, W.data_ptr(), ldw, M, N, K, target.data_ptr(), scale,
+          lse.data_ptr(), dlogp.data_ptr(), _addr(dX), lddx, _addr(dW), lddw, wsp, wsb)
+    return dX, dW
+
+
+def vocab_distill(X, W, index, teacher, scale=1.0, teacher_lse=None, loss=None, lse=None, ws=None):
+    """Divergence from a teacher's top logits, without the student's logits: token t has the ids
+    index[t] (int64 [M, L], ids outside [0, N) are no entries) with the teacher's logits teacher[t]
+    (fp32 or bf16 [M, L]), weighted by their softmax, or with teacher_lse (fp32 [M]) by
+    exp(scale * teacher - teacher_lse) -> (loss fp32 [M], lse fp32 [M]). X, W, scale and ws as for
+    vocab_logp ("qr_vocab_distill", with L)."""
+    idx = _one_device(X.device, W, index, teacher, teacher_lse, loss, lse, ws)
+    M, N, K, ldx, ldw = _head_args(X, W)
+    L = _list_args(index, teacher, teacher_lse, M)
+    loss, lse = _out(loss, X, (M,), torch.float32, "loss"), _out(lse, X, (M,), torch.float32, "lse")
+    wsp, wsb, ws = _mx4_workspace("qr_vocab_distill", M, N, K, L, X, ws)
+    _call("qr_vocab_distill", idx, X.data_ptr(), ldx, W.data_ptr(), ldw, M, N, K, index.data_ptr(),
+          teacher.data_ptr(), int(teacher.dtype == torch.bfloat16), _addr(teacher_lse), L, scale,
+          loss.data_ptr(), lse.data_ptr(), wsp, wsb)
+    return loss, lse
+
+
+def vocab_distill_grad(X, W, index, teacher, lse, dloss, scale=1.0, teacher_lse=None, need_dX=True, need_dW=True,
+                       dX=None, dW=None, ws=None):
+    """Gradient of vocab_distill: with its lse and dloss = d objective / d loss (fp32 [M]) -> (dX, dW)
+    as vocab_logp_grad."""
+    idx = _one_device(X.device, W, index, teacher, teacher_lse, lse, dloss, dX, dW, ws)
+    M, N, K, ldx, ldw = _head_args(X, W)
+    L = _list_args(index, teacher, teacher_lse, M)
+    _per_token(lse, M, torch.float32, "lse")
+    _per_token(dloss, M, torch.float32, "dloss")
+    dX, lddx, dW, lddw = _grads(X, W, need_dX, need_dW, dX, dW)
+    wsp, wsb, ws = _mx4_workspace("qr_vocab_distill_grad", M, N, K, L, X, ws)
+    _call("qr_vocab_distill_grad", idx, X.data_ptr(), ldx, W.data_ptr(), ldw, M, N, K, index.data_ptr(),
+          teacher.data_ptr(), int(teacher.dtype == torch.bfloat16), _addr(teacher_lse), L, scale,
+          lse.data_ptr(), dloss.data_ptr(), _addr(dX), lddx, _addr(dW), lddw, wsp, wsb)
+    return dX, dW
 
 
 # ----------------------------------------------------------------------------

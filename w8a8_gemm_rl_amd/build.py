@@ -28,7 +28,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqurl_w8a8.so")
 SOURCES = ["quant_kernels.hip", "producer_kernels.hip", "gemm_kernels.hip", "gemm_plan.hip",
            "acr_kernels.hip", "mx_kernels.hip", "probe_kernels.hip", "small_m_kernels.hip", "qr_api.hip",
-           "qr_noalloc.hip", "mxfp4_kernels.hip", "block_kernels.hip", "mx_api.hip"]
+           "qr_noalloc.hip", "mxfp4_kernels.hip", "block_kernels.hip", "mx_api.hip",
+           "vocab_kernels.hip", "vocab_api.hip"]
 # Per-source flags: the fused producers and block norms fix the order of their
 # fp32 roundings, so no multiply-add may be contracted there.
 EXTRA = {"producer_kernels.hip": ["-ffp-contract=off"], "block_kernels.hip": ["-ffp-contract=off"]}

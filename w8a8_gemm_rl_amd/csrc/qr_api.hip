@@ -10,6 +10,7 @@
 #include <string>
 
 #include "qr_internal.h"
+#include "qr_vocab.h"
 #include "qurl_w8a8.h"
 
 namespace {
@@ -154,6 +155,9 @@ size_t qr_workspace_size(const char* fn, int64_t M, int64_t N, int64_t K, int qt
   }
   if (std::strcmp(fn, "qr_mxfp4_gemm") == 0 || std::strcmp(fn, "qr_mxfp4_linear") == 0)
     return qr::mx4_workspace(fn, M, N, K, qt);
+  if (std::strcmp(fn, "qr_vocab_logp") == 0 || std::strcmp(fn, "qr_vocab_logp_grad") == 0 ||
+      std::strcmp(fn, "qr_vocab_distill") == 0 || std::strcmp(fn, "qr_vocab_distill_grad") == 0)
+    return qr::vocab_workspace(fn, M, N, K, qt);
   if (check_shape("qr_workspace_size", M, N, K, qt) != QR_OK) return (size_t)-1;
   const qr::GemmPlan p = qr::make_plan(M, N, K, qt, g_force_tile, g_force_splitk, g_force_rows);
   const size_t gemm = (M == 0 || N == 0) ? 0 : p.ws_bytes();

@@ -1,0 +1,841 @@
+// Losses over a large vocabulary for gfx950: from hidden states X [M, K] and the head
+// W [N, K] (bf16) to per-token losses and back, without the logits.
+//
+//   z[t,v] = c sum_k X[t,k] W[v,k],  lse[t] = log sum_v exp z[t,v]
+//   G[t,v] = a_t exp(z[t,v] - lse[t]) - sum_j b_tj [v = id_tj],  dX = G W,  dW = G^T X
+//
+// A token has a list of ids with weights (one id of weight 1 for a log-probability).
+// Tokens without one are masked: the others are numbered in order ("compact" tokens,
+// their count nv known to the GPU only) and their rows of X copied together, so masked
+// rows cost nothing and what they hold reaches no sum.
+//
+// Four products share one kernel (vocab_tile_kernel): the logits' softmax sums; the same
+// logits again with G as output, a piece of the vocabulary at a time; that piece's part
+// of dX and its rows of dW.
+#include <type_traits>
+
+#include "qr_copy.h"
+#include "qr_internal.h"
+#include "qr_mx.h"
+#include "qr_vocab.h"
+
+namespace qr {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453;
+constexpr int kNone = 0x7fffffff;  // list key of no entry: past every id
+
+// ---------------------------------------------------------------------------
+// Lists and compact tokens
+// ---------------------------------------------------------------------------
+
+// One wave per token: weights p of the list's entries and the entries in the order of
+// their ids (entries of one id in the order of the list, ids outside [0, N) last).
+// p = softmax over the entries, or exp(c s - teacher_lse). L <= kVocabMaxList; ranks by
+// counting in LDS, which is little beside the products.
+template <bool BF16>
+__global__ __launch_bounds__(256) void vocab_list_kernel(const int64_t* __restrict__ index,
+                                                         const void* __restrict__ teacher,
+                                                         const float* __restrict__ teacher_lse, int64_t M,
+                                                         int64_t N, int L, float scale, int* __restrict__ keys,
+                                                         float* __restrict__ wts, float* __restrict__ mass) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t list_smem[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int* key = reinterpret_cast<int*>(list_smem) + wave * L;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t >= M) return;
+  const int64_t* ids = index + t * L;
+  auto logit = [&](int j) {
+    if constexpr (BF16) return scale * bf16_lo(static_cast<const uint16_t*>(teacher)[t * L + j]);
+    else return scale * static_cast<const float*>(teacher)[t * L + j];
+  };
+  float top = -INFINITY;
+  for (int j = lane; j < L; j += 64) {
+    const int64_t id = ids[j];
+    const bool ok = id >= 0 && id < N;
+    key[j] = ok ? (int)id : kNone;
+    if (ok) top = fmaxf(top, logit(j));
+  }
+  top = wave_max(top);
+  float norm, sum = 0.0f;
+  if (teacher_lse) {
+    norm = teacher_lse[t];
+  } else {
+    norm = top == -INFINITY ? 0.0f : top;  // no entry with weight: all weights zero
+  }
+  for (int j = lane; j < L; j += 64)
+    if (key[j] != kNone) sum += expf(logit(j) - norm);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  const float div = teacher_lse ? 1.0f : (sum == 0.0f ? 1.0f : sum);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's own part of LDS
+  for (int j = lane; j < L; j += 64) {
+    const int k = key[j];
+    int rank = 0;
+    for (int i = 0; i < L; ++i) rank += (key[i] < k || (key[i] == k && i < j)) ? 1 : 0;
+    keys[t * L + rank] = k;
+    wts[t * L + rank] = k == kNone ? 0.0f : expf(logit(j) - norm) / div;
+  }
+  if (lane == 0) mass[t] = sum / div;
+}
+
+// One block: numbers the tokens that have a list (key 0 of a list of L; or, with `target`,
+// an id in [0, N), which becomes the key), and writes zeros as the others' results.
+__global__ __launch_bounds__(1024) void vocab_scan_kernel(const int64_t* __restrict__ target, int* keys, int L,
+                                                          int64_t M, int64_t N, int* __restrict__ nv,
+                                                          int* __restrict__ map, int* __restrict__ inv,
+                                                          float* __restrict__ value, float* __restrict__ lse) {
+  __shared__ int wsum[2][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int base = 0, buf = 0;
+  for (int64_t t0 = 0; t0 < M; t0 += 1024, buf ^= 1) {
+    const int64_t t = t0 + threadIdx.x;
+    bool live = false;
+    if (t < M) {
+      if (target) {
+        const int64_t id = target[t];
+        live = id >= 0 && id < N;
+        keys[t] = live ? (int)id : kNone;
+      } else {
+        live = keys[t * L] != kNone;
+      }
+    }
+    const uint64_t b = __ballot(live);
+    if (lane == 0) wsum[buf][wave] = __popcll(b);
+    __syncthreads();
+    int before = base, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) before += wsum[buf][w];
+      all += wsum[buf][w];
+    }
+    const int c = before + __popcll(b & (((uint64_t)1 << lane) - 1));
+    if (t < M) {
+      inv[t] = live ? c : -1;
+      if (live) {
+        map[c] = (int)t;
+      } else if (value) {
+        value[t] = 0.0f;
+        lse[t] = 0.0f;
+      }
+    }
+    base += all;
+  }
+  if (threadIdx.x == 0) *nv = base;
+}
+
+// Rows of the compact tokens, 16 bytes a thread.
+__global__ __launch_bounds__(256) void vocab_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t K,
+                                                           const int* __restrict__ nv, const int* __restrict__ map,
+                                                           uint16_t* __restrict__ Xc) {
+  const int64_t cpr = K >> 3, c = blockIdx.x;
+  if (c >= *nv) return;
+  const uint4* src = reinterpret_cast<const uint4*>(X + (int64_t)map[c] * ldx);
+  uint4* dst = reinterpret_cast<uint4*>(Xc + c * K);
+  for (int64_t i = threadIdx.x; i < cpr; i += 256) dst[i] = src[i];
+}
+
+// ---------------------------------------------------------------------------
+// Products
+// ---------------------------------------------------------------------------
+enum { kSums, kGrad, kDX, kDW };
+
+struct VocabTile {
+  const uint16_t *A, *B;
+  int64_t lda, ldb;
+  const int* nv;
+  int64_t ext_a;   // extent of the A side: ids of the piece (kSums, kGrad), K (kDX, kDW)
+  int64_t ids;     // ids of the piece
+  int64_t id0;     // its first id
+  int64_t K;
+  int tiles_a, splits;
+  const int* map;
+  const int* keys;
+  const float *wts, *mass, *lse, *g;
+  int L;
+  float scale;     // c; negative for the gradient of a log-probability's negative part
+  float sign;
+  float2* part;    // kSums: [tiles_a][ldpart]
+  int64_t ldpart;
+  float* zl;       // kSums: logits of the lists' ids
+  uint16_t* out16; // kGrad: G [nv][ldo]; kDW: dW + id0 ldo
+  int64_t ldo;
+  float* out32;    // kDX: [splits][rows32][K]
+  int64_t rows32;
+  int add;         // kDX: add to what is there
+};
+
+// A block: BN x BM outputs, A side by B side, over K steps of 64 through a ring of S
+// stages in LDS, filled by LDS-DMA copies; 8 waves of 32x32x16 MFMAs. An operand is
+// either K-contiguous ("rows": its rows run along K; LDS rows of 64 elements, 16-byte
+// chunk q of row r at q ^ (r / 2 % 8)) or has its rows along the other axis ("columns": LDS
+// holds 64 rows of K, read with the transposing load, whose 16 lanes take four rows of
+// K by 16 columns; 64-byte pieces of row k at p ^ (k % 4), so that the four rows meet
+// different banks).
+//          A side            B side             K
+//   kSums  ids (W, rows)     tokens (X, rows)   hidden
+//   kGrad  ids (W, rows)     tokens (X, rows)   hidden
+//   kDX    hidden (W, cols)  tokens (G, rows)   ids
+//   kDW    hidden (X, cols)  ids (G, cols)      tokens
+// Register 4 q + r of a fragment: A side 8 q + 4 lg + r, B side lane % 32.
+template <int MODE, int BN, int BM, int WN, int WM, int S>
+__global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const VocabTile p) {
+  constexpr bool TA = MODE == kDX || MODE == kDW, TB = MODE == kDW;
+  constexpr int NW = WN * WM, KS = 64;
+  constexpr int WTN = BN / WN, WTM = BM / WM, FN = WTN / 32, FM = WTM / 32;
+  constexpr int IA = (BN / 8 + NW - 1) / NW * NW, IB = (BM / 8 + NW - 1) / NW * NW;
+  constexpr int NA = IA / NW, NB = IB / NW, GA = (NA + 3) / 4, GB = (NB + 3) / 4, NI = NA + NB;
+  constexpr int STAGE = (IA + IB) * 1024;
+  constexpr int RA = BN * 2, RB = BM * 2;  // bytes of an LDS row of a "columns" operand
+  static_assert(WTN % 32 == 0 && WTM % 32 == 0, "wave tile");
+  static_assert(!TA || BN % 128 == 0, "columns: whole 64-byte pieces of four");
+  static_assert(!TB || BM % 128 == 0, "columns: whole 64-byte pieces of four");
+  static_assert(S >= 2 && (S - 1) * NI <= 63 && S * STAGE <= 160 * 1024, "ring");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+
+  const int nv = *p.nv;
+  const int64_t ext_b = MODE == kDW ? p.ids : nv;
+  const int64_t klen = MODE == kDW ? nv : (MODE == kDX ? p.ids : p.K);
+  const int stages = (int)((klen + KS - 1) / KS);
+
+  // An XCD takes one contiguous part of the tiles; groups of up to 8 B tiles share A tiles.
+  const int tiles_b = (int)((ext_b + BM - 1) / BM);
+  const int tiles = p.tiles_a * tiles_b, total = tiles * p.splits, xcd = blockIdx.x & 7;
+  const int end = (int)((int64_t)total * (xcd + 1) / 8);
+  int cur = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+  if (cur >= end) return;
+  const int split = cur / tiles;
+  cur -= split * tiles;
+  int ta, tb;
+  {
+    const int b0 = cur / (8 * p.tiles_a) * 8, gb = tiles_b - b0 < 8 ? tiles_b - b0 : 8;
+    cur -= b0 * p.tiles_a;
+    tb = __builtin_amdgcn_readfirstlane(b0 + cur % gb);
+    ta = __builtin_amdgcn_readfirstlane(cur / gb);
+  }
+  const int ks0 = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * split / p.splits));
+  const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * (split + 1) / p.splits)) - ks0;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wid % WN, wm = wid / WN;
+  const int lr = lane & 31, lg = lane >> 5;
+  const int64_t a0 = (int64_t)ta * BN, b0 = (int64_t)tb * BM;
+
+  // Copies. Lanes whose 16 bytes lie outside the operand take an offset past the
+  // buffer: zeros.
+  constexpr uint32_t kBig = 0x80000000u;
+  const int ll = lane >> 3, pc = lane & 7;
+  // row of K (columns) or chunk of 8 elements of K (rows) that copy I of an operand takes
+  auto rows_of = [&](int I, int& row, int& chunk) {
+    row = I * 8 + ll;
+    chunk = pc ^ ((row >> 1) & 7);
+  };
+  auto cols_of = [&](int I, int rowbytes, int& k, int& chunk) {
+    const int cpr = rowbytes / 16;  // chunks of a row: 32 or 16
+    k = I * (64 / cpr) + lane / cpr;
+    chunk = (lane % cpr) ^ ((k & 3) << 2);
+  };
+  auto offset = [&](bool cols, int I, int rowbytes, int tile_rows, int64_t ld, int64_t left) {
+    if (cols) {
+      int k, c;
+      cols_of(I, rowbytes, k, c);
+      return c * 8 < left ? (uint32_t)(k * ld * 2 + c * 16) : kBig;
+    }
+    int r, c;
+    rows_of(I, r, c);
+    return r < tile_rows && r < left ? (uint32_t)(r * ld * 2 + c * 16) : kBig;
+  };
+  uint32_t oa[NA], ob[NB];
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+    oa[i] = offset(TA, wid * NA + i, RA, BN, p.lda, p.ext_a - a0) - 1024u * (uint32_t)(i % 4);
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+    ob[i] = offset(TB, wid * NB + i, RB, BM, p.ldb, ext_b - b0) - 1024u * (uint32_t)(i % 4);
+  const uint16_t* const pa = p.A + (TA ? a0 : a0 * p.lda);
+  const uint16_t* const pb = p.B + (TB ? b0 : b0 * p.ldb);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+  constexpr int NG = GA + GB;
+  auto issue_group = [&](int g, int slot, int ks) {
+    const bool isA = g < GA, cols = isA ? TA : TB;
+    const int i0 = (isA ? g : g - GA) * 4, n = isA ? NA : NB, cnt = n - i0 < 4 ? n - i0 : 4;
+    const int I0 = wid * n + i0;
+    const uint32_t lds = lds0 + (uint32_t)(slot * STAGE + ((isA ? 0 : IA) + I0) * 1024);
+    const uint16_t* src = (isA ? pa : pb) + (cols ? (int64_t)ks * KS * (isA ? p.lda : p.ldb) : 0);
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)src, (short)0, 0x7ffffff0, kBufWord3);
+    const int soff = cols ? 0 : ks * (KS * 2);
+    uint32_t vo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e < n ? i0 + e : 0;
+      vo[e] = isA ? oa[i < NA ? i : 0] : ob[i < NB ? i : 0];
+    }
+    const int64_t left = klen - (int64_t)ks * KS;
+    if (left < KS) {  // the last stage: K ends inside it
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        int a, c;
+        if (cols) {
+          cols_of(I0 + e, isA ? RA : RB, a, c);
+        } else {
+          rows_of(I0 + e, a, c);
+          a = c * 8;
+        }
+        if (a >= left) vo[e] = kBig - 1024u * (uint32_t)e;
+      }
+    }
+    if (cnt == 4) dma_group<4, false>(lds, vo, r, soff);
+    else if (cnt == 3) dma_group<3, false>(lds, vo, r, soff);
+    else if (cnt == 2) dma_group<2, false>(lds, vo, r, soff);
+    else dma_group<1, false>(lds, vo, r, soff);
+  };
+
+  // Operand reads of K step h (16 elements): lane (lr, lg) takes row or column lr of a
+  // fragment and elements 8 lg .. 8 lg + 7.
+  const int jl = lane & 15, tk = 8 * lg + (jl >> 2);  // columns: K row of the lane's address
+  const int tc = 32 * ((lane >> 4) & 1) + 8 * (jl & 3);
+  auto read = [&](bool cols, const uint8_t* base, int w0, int i, int h, int rowbytes) {
+    if (cols) {
+      const int c = ((w0 + 32 * i) * 2 + tc) ^ ((jl >> 2) << 6);
+      const uint8_t* s = base + (16 * h + tk) * rowbytes + c;
+      typedef __attribute__((address_space(3))) v4s* lds_v4s;
+      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s));
+      const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s + 4 * rowbytes));
+      const v8s v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(v8b, v);
+    }
+    const int r = w0 + 32 * i + lr;
+    return *reinterpret_cast<const v8b*>(base + r * 128 + (((2 * h + lg) ^ ((lr >> 1) & 7)) << 4));
+  };
+  v16f acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = v16f{};
+  v8b fa[2][FN], fb[2][FM];
+  auto load_ops = [&](const uint8_t* st, int h, int buf) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i) fa[buf][i] = read(TA, st, wn * WTN, i, h, RA);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) fb[buf][j] = read(TB, st + IA * 1024, wm * WTM, j, h, RB);
+  };
+  auto multiply_row = [&](int buf, int i) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[buf][i], fb[buf][j], acc[i][j], 0, 0, 0);
+  };
+  auto interleave = [&]() {
+    constexpr int NR = FN * (TA ? 2 : 1) + FM * (TB ? 2 : 1), NM = FN * FM;
+#pragma unroll
+    for (int q = 0; q < NM; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, (NR + NM - 1) / NM, 0);
+    }
+  };
+
+  // Compact tokens of the lane, and where their lists enter the wave's ids.
+  const int64_t id_lo = p.id0 + a0 + wn * WTN;
+  const int own = (int)(p.ids - a0 - wn * WTN < WTN ? p.ids - a0 - wn * WTN : WTN);  // ids of the wave
+  int tok[FM], ent[FM];
+  if constexpr (MODE == kSums || MODE == kGrad) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int64_t c = b0 + wm * WTM + 32 * j + lr;
+      tok[j] = c < nv ? p.map[c] : -1;
+    }
+  }
+
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < nk) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) issue_group(g, s, ks0 + s);
+    }
+
+  if constexpr (MODE == kSums || MODE == kGrad) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      int lo = 0;
+      if (p.L > 1 && tok[j] >= 0) {  // first entry whose id is not below id_lo
+        const int* key = p.keys + (int64_t)tok[j] * p.L;
+        int hi = p.L;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (key[mid] < id_lo) lo = mid + 1;
+          else hi = mid;
+        }
+      }
+      ent[j] = lo;
+    }
+  }
+
+  if (nk > 0) {
+    wait_stages<NI, S - 1>(nk - 1);
+    __syncthreads();
+    load_ops(smem, 0, 0);
+    int cs = 0;
+    for (int it = 0; it < nk; ++it) {
+      const int ns = cs + 1 == S ? 0 : cs + 1;
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        load_ops(smem + cs * STAGE, h + 1, (h + 1) & 1);
+#pragma unroll
+        for (int i = 0; i < FN; ++i) multiply_row(h & 1, i);
+        interleave();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // Stage it + 1 opens when its copies have landed and no wave reads stage it any
+      // more (the last step's operands are in registers); its slot is refilled at once.
+      if (it + 1 < nk) {
+        wait_stages<NI, S - 2>(nk - 2 - it);
+        __syncthreads();
+        load_ops(smem + ns * STAGE, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const bool refill = it + S < nk;
+#pragma unroll
+      for (int i = 0; i < (FN > NG ? FN : NG); ++i) {
+        if (i < FN) multiply_row(1, i);
+        if (refill && i < NG) issue_group(i, cs, ks0 + it + S);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      cs = ns;
+    }
+  }
+
+  // Entries of the lists among the wave's ids: f(fragment j, entry, offset from id_lo).
+  auto hits = [&](int j, auto f) {
+    if (tok[j] < 0) return;
+    const int64_t base = (int64_t)tok[j] * p.L;
+    for (int e = ent[j]; e < p.L; ++e) {
+      const int key = p.keys[base + e];
+      if (key == kNone || key >= id_lo + own) break;
+      const int d = (int)(key - id_lo);
+      if (d < 0) continue;  // a list of one entry is not searched
+      if (((d >> 2) & 1) == lg) f(base + e, (d >> 5) * 16 + ((d >> 3) & 3) * 4 + (d & 3));
+    }
+  };
+  const float c2 = p.scale * kLog2e;
+
+  if constexpr (MODE == kSums) {
+    // base-2 maximum and sum of each token over the tile's ids
+    __syncthreads();
+    float2* red = reinterpret_cast<float2*>(smem);  // [WN][BM]
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      hits(j, [&](int64_t e, int reg) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v = reg == i * 16 + r ? acc[i][j][r] : v;
+        p.zl[e] = v * p.scale;
+      });
+      float m = -INFINITY, s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if (32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= own) acc[i][j][r] = -INFINITY;
+          m = fmaxf(m, acc[i][j][r]);
+        }
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      m = m == -INFINITY ? m : m * c2;
+      const float sub = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -sub));
+      s += __shfl_xor(s, 32, 64);
+      if (lg == 0) red[wn * BM + wm * WTM + 32 * j + lr] = make_float2(m, s);
+    }
+    __syncthreads();
+    for (int c = tid; c < BM; c += 64 * NW) {
+      if (b0 + c >= nv) continue;
+      float m = -INFINITY, s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) m = fmaxf(m, red[w * BM + c].x);
+      const float sub = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) s += red[w * BM + c].y * __builtin_amdgcn_exp2f(red[w * BM + c].x - sub);
+      p.part[(int64_t)ta * p.ldpart + b0 + c] = make_float2(m, s);
+    }
+    return;
+  }
+
+  if constexpr (MODE == kGrad) {
+    // G in fp32, rounded once to bf16 (half a step, 2^-8 of each element: a product of two
+    // bf16 operands is what the matrix cores take)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      float a = 0.0f, l2 = 0.0f, gt = 0.0f;
+      if (tok[j] >= 0) {
+        gt = p.g[tok[j]] * p.scale * p.sign;
+        a = p.mass ? gt * p.mass[tok[j]] : gt;
+        l2 = p.lse[tok[j]] * kLog2e;
+      }
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float v = a * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -l2));
+          acc[i][j][r] = 32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) < own ? v : 0.0f;
+        }
+      hits(j, [&](int64_t e, int reg) {
+        const float b = p.wts ? gt * p.wts[e] : gt;
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] -= reg == i * 16 + r ? b : 0.0f;
+      });
+    }
+  }
+
+  if constexpr (MODE == kDX) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int64_t c = b0 + wm * WTM + 32 * j + lr;
+      if (c >= nv) continue;
+      float* row = p.out32 + ((int64_t)split * p.rows32 + c) * p.K;
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t h = a0 + wn * WTN + 32 * i + 8 * q + 4 * lg;
+          if (h >= p.K) continue;
+          const v16f& v = acc[i][j];
+          float4 o = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          float4* d = reinterpret_cast<float4*>(row + h);
+          if (p.add) {
+            const float4 w = *d;
+            o.x += w.x; o.y += w.y; o.z += w.z; o.w += w.w;
+          }
+          *d = o;
+        }
+    }
+    return;
+  }
+
+  // bf16 outputs leave through the ring, each wave its own part, so that stores run along
+  // the B side's rows, 16 bytes a lane.
+  if constexpr (MODE == kGrad || MODE == kDW) {
+    __syncthreads();
+    constexpr int LD = WTN * 2 + 16;
+    static_assert(NW * 32 * LD <= S * STAGE, "a fragment per wave fits");
+    uint8_t* so = smem + wid * (32 * LD);
+    const int64_t row0 = b0 + wm * WTM, lim = MODE == kGrad ? nv : p.ids;
+    const int64_t col0 = a0 + wn * WTN, left = MODE == kGrad ? WTN : p.K - col0;
+    constexpr int CPR = WTN / 8;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v16f& v = acc[i][j];
+          *reinterpret_cast<uint2*>(so + lr * LD + (32 * i + 8 * q + 4 * lg) * 2) =
+              make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int k = 0; k < 32 * CPR / 64; ++k) {
+        const int c = lane + 64 * k, ml = c / CPR, nl = 8 * (c % CPR);
+        const int64_t m = row0 + 32 * j + ml;
+        if (m < lim && nl < left)
+          *reinterpret_cast<uint4*>(p.out16 + m * p.ldo + col0 + nl) =
+              *reinterpret_cast<const uint4*>(so + ml * LD + nl * 2);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+}
+
+// Sums of the tiles' parts, 16 compact tokens a block, 64 threads each: lse, and
+// sum_j p (log p - (z_j - lse)) (with wts) or z - lse. Float64, fixed order.
+__global__ __launch_bounds__(1024) void vocab_finish_kernel(const float2* __restrict__ part, int64_t ldpart,
+                                                            int tiles, const int* __restrict__ nv,
+                                                            const int* __restrict__ map,
+                                                            const int* __restrict__ keys,
+                                                            const float* __restrict__ wts,
+                                                            const float* __restrict__ zl, int L,
+                                                            float* __restrict__ value, float* __restrict__ lse) {
+  __shared__ float red_m[64][17];
+  __shared__ double red_s[64][17];
+  const int tl = threadIdx.x & 15, gr = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + tl;
+  const int n = *nv;
+  if ((int64_t)blockIdx.x * 16 >= n) return;
+  float m = -INFINITY;
+  double s = 0.0;
+  if (c < n)
+    for (int i = gr; i < tiles; i += 64) {
+      const float2 v = part[(int64_t)i * ldpart + c];
+      if (v.x == -INFINITY && v.y == 0.0f) continue;
+      const float top = fmaxf(m, v.x);
+      s = s * (double)exp2f(m - top) + (double)v.y * (double)exp2f(v.x - top);
+      m = top;
+    }
+  red_m[gr][tl] = m;
+  red_s[gr][tl] = s;
+  __syncthreads();
+  for (int h = 32; h > 0; h >>= 1) {
+    if (gr < h) {
+      const float a = red_m[gr][tl], b = red_m[gr + h][tl], top = fmaxf(a, b);
+      if (top != -INFINITY)
+        red_s[gr][tl] = red_s[gr][tl] * (double)exp2f(a - top) + red_s[gr + h][tl] * (double)exp2f(b - top);
+      red_m[gr][tl] = top;
+    }
+    __syncthreads();
+  }
+  const double total = ((double)red_m[0][tl] + log2(red_s[0][tl])) * kLn2;
+  __syncthreads();
+  const int64_t t = c < n ? map[c] : 0;
+  double v = 0.0;
+  if (c < n) {
+    if (wts) {
+      for (int j = gr; j < L; j += 64) {
+        const double w = (double)wts[t * L + j];
+        if (keys[t * L + j] != kNone && w != 0.0) v += w * (log(w) - ((double)zl[t * L + j] - total));
+      }
+    } else if (gr == 0) {
+      v = (double)zl[t] - total;
+    }
+  }
+  red_s[gr][tl] = v;
+  __syncthreads();
+  for (int h = 32; h > 0; h >>= 1) {
+    if (gr < h) red_s[gr][tl] += red_s[gr + h][tl];
+    __syncthreads();
+  }
+  if (gr == 0 && c < n) {
+    value[t] = (float)red_s[0][tl];
+    lse[t] = (float)total;
+  }
+}
+
+// dX of all tokens: the splits' sums in order, rounded once; zeros for masked tokens.
+__global__ __launch_bounds__(256) void vocab_dx_kernel(const float* __restrict__ part, int splits, int64_t rows,
+                                                       int64_t K, const int* __restrict__ inv,
+                                                       uint16_t* __restrict__ dX, int64_t lddx) {
+  const int64_t t = blockIdx.x, c = inv[t];
+  for (int64_t i = threadIdx.x; i < K >> 3; i += 256) {
+    float v[8] = {};
+    if (c >= 0)
+      for (int s = 0; s < splits; ++s) {
+        const float4* q = reinterpret_cast<const float4*>(part + (s * rows + c) * K) + 2 * i;
+        const float4 a = q[0], b = q[1];
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      }
+    *reinterpret_cast<uint4*>(dX + t * lddx + 8 * i) = make_uint4(
+        bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+  }
+}
+
+// dW where there are no tokens at all.
+__global__ __launch_bounds__(256) void vocab_zero_kernel(uint16_t* __restrict__ dW, int64_t ld, int64_t K) {
+  for (int64_t i = threadIdx.x; i < K >> 3; i += 256)
+    *reinterpret_cast<uint4*>(dW + blockIdx.x * ld + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---------------------------------------------------------------------------
+// Plans and launches
+// ---------------------------------------------------------------------------
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int MODE, int BN, int BM, int WN, int WM, int S>
+hipError_t launch_one(VocabTile p, int64_t max_b, hipStream_t st) {
+  p.tiles_a = (int)ceil_div(p.ext_a, BN);
+  const int64_t blocks = p.tiles_a * ceil_div(max_b, BM) * p.splits;
+  const dim3 grid((unsigned)ceil_div(blocks, 8) * 8);
+  hipLaunchKernelGGL((vocab_tile_kernel<MODE, BN, BM, WN, WM, S>), grid, dim3(64 * WN * WM), 0, st, p);
+  return hipGetLastError();
+}
+
+// Tokens of a tile by their number.
+int tile_tokens(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+template <int MODE>
+hipError_t launch_tokens(const VocabTile& p, int64_t M, hipStream_t st) {
+  switch (tile_tokens(M)) {
+    case 32: return launch_one<MODE, 256, 32, 8, 1, 4>(p, M, st);
+    case 64: return launch_one<MODE, 256, 64, 4, 2, 3>(p, M, st);
+    case 128: return launch_one<MODE, 256, 128, 4, 2, 3>(p, M, st);
+    default: return launch_one<MODE, 256, 256, 2, 4, 2>(p, M, st);
+  }
+}
+
+struct Layout {
+  size_t nv, map, inv, keys, wts, mass, zl, xc, part, g, dx, bytes;
+  int64_t piece;  // ids of a piece of the gradient
+  int splits;     // parts of a piece's ids whose sums of dX are kept apart
+};
+
+Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad) {
+  Layout w = {};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += align256(n);
+    return o;
+  };
+  w.nv = take(4);
+  w.map = take((size_t)M * 4);
+  w.inv = take((size_t)M * 4);
+  w.keys = take((size_t)(M * L) * 4);
+  if (lists) {
+    w.wts = take((size_t)(M * L) * 4);
+    w.mass = take((size_t)M * 4);
+  }
+  w.xc = take((size_t)(M * K) * 2);
+  if (!grad) {
+    w.zl = take((size_t)(M * L) * 4);
+    w.part = take((size_t)(ceil_div(N, 256) * M) * 8);
+  } else {
+    // G of a piece: 256 MiB, between 4096 ids and all of them
+    const int64_t want = ((int64_t)128 << 20) / M / 256 * 256;
+    w.piece = want < 4096 ? 4096 : want;
+    if (w.piece > N) w.piece = ceil_div(N, 256) * 256;
+    const int64_t tiles = ceil_div(K, 256) * ceil_div(M, tile_tokens(M));
+    int64_t s = 256 / tiles;
+    if (s > w.piece / 256) s = w.piece / 256;
+    w.splits = (int)(s < 1 ? 1 : s);
+    w.g = take((size_t)(M * w.piece) * 2);
+    w.dx = take((size_t)(w.splits * M * K) * 4);
+  }
+  w.bytes = at;
+  return w;
+}
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
+}
+
+// Lists, compact tokens and their rows.
+hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, hipStream_t st) {
+  if (p.index) {
+    const dim3 grid((unsigned)ceil_div(p.M, 4));
+    const size_t lds = (size_t)p.L * 4 * sizeof(int);
+    if (p.teacher_bf16)
+      hipLaunchKernelGGL((vocab_list_kernel<true>), grid, dim3(256), lds, st, p.index, p.teacher, p.teacher_lse,
+                         p.M, p.N, (int)p.L, p.scale, at<int>(ws, w.keys), at<float>(ws, w.wts),
+                         at<float>(ws, w.mass));
+    else
+      hipLaunchKernelGGL((vocab_list_kernel<false>), grid, dim3(256), lds, st, p.index, p.teacher, p.teacher_lse,
+                         p.M, p.N, (int)p.L, p.scale, at<int>(ws, w.keys), at<float>(ws, w.wts),
+                         at<float>(ws, w.mass));
+  }
+  hipLaunchKernelGGL(vocab_scan_kernel, dim3(1), dim3(1024), 0, st, p.index ? nullptr : p.target,
+                     at<int>(ws, w.keys), (int)p.L, p.M, p.N, at<int>(ws, w.nv), at<int>(ws, w.map),
+                     at<int>(ws, w.inv), p.value, p.lse_out);
+  hipLaunchKernelGGL(vocab_gather_kernel, dim3((unsigned)p.M), dim3(256), 0, st, p.X, p.ldx, p.K,
+                     at<int>(ws, w.nv), at<int>(ws, w.map), at<uint16_t>(ws, w.xc));
+  return hipGetLastError();
+}
+
+VocabTile common(const VocabArgs& p, const Layout& w, void* ws) {
+  VocabTile t = {};
+  t.nv = at<int>(ws, w.nv);
+  t.K = p.K;
+  t.map = at<int>(ws, w.map);
+  t.keys = at<int>(ws, w.keys);
+  if (p.index) {
+    t.wts = at<float>(ws, w.wts);
+    t.mass = at<float>(ws, w.mass);
+  }
+  t.L = (int)p.L;
+  t.scale = p.scale;
+  t.splits = 1;
+  return t;
+}
+
+}  // namespace
+
+size_t vocab_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad) {
+  return M == 0 ? 0 : layout(M, N, K, L, lists, grad).bytes;
+}
+
+hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
+  const Layout w = layout(p.M, p.N, p.K, p.L, p.index != nullptr, false);
+  hipError_t e = prepare(p, w, ws, st);
+  if (e != hipSuccess) return e;
+  VocabTile t = common(p, w, ws);
+  t.A = p.W;
+  t.lda = p.ldw;
+  t.B = at<uint16_t>(ws, w.xc);
+  t.ldb = p.K;
+  t.ext_a = t.ids = p.N;
+  t.part = at<float2>(ws, w.part);
+  t.ldpart = p.M;
+  t.zl = at<float>(ws, w.zl);
+  e = launch_tokens<kSums>(t, p.M, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(vocab_finish_kernel, dim3((unsigned)ceil_div(p.M, 16)), dim3(1024), 0, st, t.part, t.ldpart,
+                     (int)ceil_div(p.N, 256), t.nv, t.map, t.keys, t.wts, t.zl, t.L, p.value, p.lse_out);
+  return hipGetLastError();
+}
+
+hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
+  if (p.M == 0) {
+    if (p.dW) hipLaunchKernelGGL(vocab_zero_kernel, dim3((unsigned)p.N), dim3(256), 0, st, p.dW, p.lddw, p.K);
+    return hipGetLastError();
+  }
+  const Layout w = layout(p.M, p.N, p.K, p.L, p.index != nullptr, true);
+  hipError_t e = prepare(p, w, ws, st);
+  if (e != hipSuccess) return e;
+  uint16_t* G = at<uint16_t>(ws, w.g);
+  for (int64_t id0 = 0; id0 < p.N; id0 += w.piece) {
+    const int64_t ids = p.N - id0 < w.piece ? p.N - id0 : w.piece;
+    VocabTile t = common(p, w, ws);
+    t.A = p.W + id0 * p.ldw;
+    t.lda = p.ldw;
+    t.B = at<uint16_t>(ws, w.xc);
+    t.ldb = p.K;
+    t.ext_a = t.ids = ids;
+    t.id0 = id0;
+    t.lse = p.lse;
+    t.g = p.g;
+    t.sign = p.index ? 1.0f : -1.0f;
+    t.out16 = G;
+    t.ldo = w.piece;
+    if ((e = launch_tokens<kGrad>(t, p.M, st)) != hipSuccess) return e;
+    if (p.dX) {
+      VocabTile x = t;
+      x.B = G;
+      x.ldb = w.piece;
+      x.ext_a = p.K;
+      x.splits = w.splits;
+      x.out32 = at<float>(ws, w.dx);
+      x.rows32 = p.M;
+      x.add = id0 > 0;
+      if ((e = launch_tokens<kDX>(x, p.M, st)) != hipSuccess) return e;
+    }
+    if (p.dW) {
+      VocabTile x = t;
+      x.A = at<uint16_t>(ws, w.xc);
+      x.lda = p.K;
+      x.B = G;
+      x.ldb = w.piece;
+      x.ext_a = p.K;
+      x.out16 = p.dW + id0 * p.lddw;
+      x.ldo = p.lddw;
+      if ((e = launch_one<kDW, 256, 256, 2, 4, 2>(x, ids, st)) != hipSuccess) return e;
+    }
+  }
+  if (p.dX)
+    hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M), dim3(256), 0, st, at<float>(ws, w.dx), w.splits, p.M,
+                       p.K, at<int>(ws, w.inv), p.dX, p.lddx);
+  return hipGetLastError();
+}
+
+}  // namespace qr
