@@ -184,8 +184,15 @@ struct VocabTile {
 //   kDX    hidden (W, cols)  tokens (G, rows)   ids
 //   kDW    hidden (X, cols)  ids (G, cols)      tokens
 // Register 4 q + r of a fragment: A side 8 q + 4 lg + r, B side lane % 32.
+//
+// `block` and the grid it belongs to may be a part of the launch's.
+template <int BN, int BM, int S>
+constexpr int ring_bytes() {
+  return S * (BN + (BM < 64 ? 64 : BM)) * 128;  // copies of 8 rows, one a wave at least
+}
+
 template <int MODE, int BN, int BM, int WN, int WM, int S>
-__global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const VocabTile p) {
+__device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_t* smem) {
   constexpr bool TA = MODE == kDX || MODE == kDW, TB = MODE == kDW;
   constexpr int NW = WN * WM, KS = 64;
   constexpr int WTN = BN / WN, WTM = BM / WM, FN = WTN / 32, FM = WTM / 32;
@@ -197,7 +204,7 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const Vocab
   static_assert(!TA || BN % 128 == 0, "columns: whole 64-byte pieces of four");
   static_assert(!TB || BM % 128 == 0, "columns: whole 64-byte pieces of four");
   static_assert(S >= 2 && (S - 1) * NI <= 63 && S * STAGE <= 160 * 1024, "ring");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+  static_assert(S * STAGE == ring_bytes<BN, BM, S>(), "the kernels' array");
 
   const int nv = *p.nv;
   const int64_t ext_b = MODE == kDW ? p.ids : nv;
@@ -206,9 +213,9 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const Vocab
 
   // An XCD takes one contiguous part of the tiles; groups of up to 8 B tiles share A tiles.
   const int tiles_b = (int)((ext_b + BM - 1) / BM);
-  const int tiles = p.tiles_a * tiles_b, total = tiles * p.splits, xcd = blockIdx.x & 7;
+  const int tiles = p.tiles_a * tiles_b, total = tiles * p.splits, xcd = block & 7;
   const int end = (int)((int64_t)total * (xcd + 1) / 8);
-  int cur = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+  int cur = (int)((int64_t)total * xcd / 8) + (block >> 3);
   if (cur >= end) return;
   const int split = cur / tiles;
   cur -= split * tiles;
@@ -377,38 +384,47 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const Vocab
     }
   }
 
+  // One stage. The next one opens when its copies have landed and no wave reads this one
+  // any more (the last step's operands are in registers); its slot is refilled at once. The
+  // three kinds of stage are bodies of their own: waits merged over a branch would be
+  // those of the worst path.
+  int cs = 0, it = 0;
+  auto stage = [&](auto refill, auto last) {
+    const int ns = cs + 1 == S ? 0 : cs + 1;
+#pragma unroll
+    for (int h = 0; h < 3; ++h) {
+      load_ops(smem + cs * STAGE, h + 1, (h + 1) & 1);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) multiply_row(h & 1, i);
+      interleave();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (!decltype(last)::value) {
+      if constexpr (decltype(refill)::value) wait_vm<(S - 2) * NI>();
+      else wait_stages<NI, S - 2>(nk - 2 - it);
+      __syncthreads();
+      load_ops(smem + ns * STAGE, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < (FN > NG ? FN : NG); ++i) {
+      if (i < FN) multiply_row(1, i);
+      if constexpr (decltype(refill)::value) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (i < NG) issue_group(i, cs, ks0 + it + S);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    cs = ns;
+  };
   if (nk > 0) {
     wait_stages<NI, S - 1>(nk - 1);
     __syncthreads();
     load_ops(smem, 0, 0);
-    int cs = 0;
-    for (int it = 0; it < nk; ++it) {
-      const int ns = cs + 1 == S ? 0 : cs + 1;
-#pragma unroll
-      for (int h = 0; h < 3; ++h) {
-        load_ops(smem + cs * STAGE, h + 1, (h + 1) & 1);
-#pragma unroll
-        for (int i = 0; i < FN; ++i) multiply_row(h & 1, i);
-        interleave();
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // Stage it + 1 opens when its copies have landed and no wave reads stage it any
-      // more (the last step's operands are in registers); its slot is refilled at once.
-      if (it + 1 < nk) {
-        wait_stages<NI, S - 2>(nk - 2 - it);
-        __syncthreads();
-        load_ops(smem + ns * STAGE, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      const bool refill = it + S < nk;
-#pragma unroll
-      for (int i = 0; i < (FN > NG ? FN : NG); ++i) {
-        if (i < FN) multiply_row(1, i);
-        if (refill && i < NG) issue_group(i, cs, ks0 + it + S);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      cs = ns;
-    }
+    for (; it < nk - S; ++it) stage(std::true_type{}, std::false_type{});
+    for (; it < nk - 1; ++it) stage(std::false_type{}, std::false_type{});
+    stage(std::false_type{}, std::true_type{});
   }
 
   // Entries of the lists among the wave's ids: f(fragment j, entry, offset from id_lo).
@@ -558,6 +574,23 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const Vocab
   }
 }
 
+template <int MODE, int BN, int BM, int WN, int WM, int S>
+__global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const VocabTile p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[ring_bytes<BN, BM, S>()];
+  vocab_tile<MODE, BN, BM, WN, WM, S>(p, blockIdx.x, smem);
+}
+
+// A piece's part of dX (the first `dx_blocks` blocks) and rows of dW in one launch: dX has
+// few tiles of many stages, which seldom fill the CUs, dW many of few.
+template <int BM, int WN, int WM, int S>
+__global__ __launch_bounds__(512, 1) void vocab_grads_kernel(const VocabTile x, const VocabTile w, int dx_blocks) {
+  static_assert(WN * WM == 8, "one block size");
+  constexpr int A = ring_bytes<256, BM, S>(), C = ring_bytes<256, 256, 2>();
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[A > C ? A : C];
+  if ((int)blockIdx.x < dx_blocks) vocab_tile<kDX, 256, BM, WN, WM, S>(x, blockIdx.x, smem);
+  else vocab_tile<kDW, 256, 256, 2, 4, 2>(w, blockIdx.x - dx_blocks, smem);
+}
+
 // Sums of the tiles' parts, 16 compact tokens a block, 64 threads each: lse, and
 // sum_j p (log p - (z_j - lse)) (with wts) or z - lse. Float64, fixed order.
 __global__ __launch_bounds__(1024) void vocab_finish_kernel(const float2* __restrict__ part, int64_t ldpart,
@@ -652,12 +685,23 @@ __global__ __launch_bounds__(256) void vocab_zero_kernel(uint16_t* __restrict__ 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int MODE, int BN, int BM, int WN, int WM, int S>
+// Blocks of a product, a multiple of 8 (an XCD's share each).
+int64_t product_blocks(VocabTile& p, int64_t max_b, int BM) {
+  p.tiles_a = (int)ceil_div(p.ext_a, 256);
+  return ceil_div(p.tiles_a * ceil_div(max_b, BM) * p.splits, 8) * 8;
+}
+
+template <int MODE, int BM, int WN, int WM, int S>
 hipError_t launch_one(VocabTile p, int64_t max_b, hipStream_t st) {
-  p.tiles_a = (int)ceil_div(p.ext_a, BN);
-  const int64_t blocks = p.tiles_a * ceil_div(max_b, BM) * p.splits;
-  const dim3 grid((unsigned)ceil_div(blocks, 8) * 8);
-  hipLaunchKernelGGL((vocab_tile_kernel<MODE, BN, BM, WN, WM, S>), grid, dim3(64 * WN * WM), 0, st, p);
+  const dim3 grid((unsigned)product_blocks(p, max_b, BM));
+  hipLaunchKernelGGL((vocab_tile_kernel<MODE, 256, BM, WN, WM, S>), grid, dim3(512), 0, st, p);
+  return hipGetLastError();
+}
+
+template <int BM, int WN, int WM, int S>
+hipError_t launch_grads(VocabTile x, VocabTile w, int64_t M, hipStream_t st) {
+  const int64_t nx = product_blocks(x, M, BM), nw = product_blocks(w, w.ids, 256);
+  hipLaunchKernelGGL((vocab_grads_kernel<BM, WN, WM, S>), dim3((unsigned)(nx + nw)), dim3(512), 0, st, x, w, (int)nx);
   return hipGetLastError();
 }
 
@@ -667,10 +711,19 @@ int tile_tokens(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128
 template <int MODE>
 hipError_t launch_tokens(const VocabTile& p, int64_t M, hipStream_t st) {
   switch (tile_tokens(M)) {
-    case 32: return launch_one<MODE, 256, 32, 8, 1, 4>(p, M, st);
-    case 64: return launch_one<MODE, 256, 64, 4, 2, 3>(p, M, st);
-    case 128: return launch_one<MODE, 256, 128, 4, 2, 3>(p, M, st);
-    default: return launch_one<MODE, 256, 256, 2, 4, 2>(p, M, st);
+    case 32: return launch_one<MODE, 32, 8, 1, 4>(p, M, st);
+    case 64: return launch_one<MODE, 64, 4, 2, 3>(p, M, st);
+    case 128: return launch_one<MODE, 128, 4, 2, 3>(p, M, st);
+    default: return launch_one<MODE, 256, 2, 4, 2>(p, M, st);
+  }
+}
+
+hipError_t launch_both(const VocabTile& x, const VocabTile& w, int64_t M, hipStream_t st) {
+  switch (tile_tokens(M)) {
+    case 32: return launch_grads<32, 8, 1, 4>(x, w, M, st);
+    case 64: return launch_grads<64, 4, 2, 3>(x, w, M, st);
+    case 128: return launch_grads<128, 4, 2, 3>(x, w, M, st);
+    default: return launch_grads<256, 2, 4, 2>(x, w, M, st);
   }
 }
 
@@ -809,28 +862,22 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     t.out16 = G;
     t.ldo = w.piece;
     if ((e = launch_tokens<kGrad>(t, p.M, st)) != hipSuccess) return e;
-    if (p.dX) {
-      VocabTile x = t;
-      x.B = G;
-      x.ldb = w.piece;
-      x.ext_a = p.K;
-      x.splits = w.splits;
-      x.out32 = at<float>(ws, w.dx);
-      x.rows32 = p.M;
-      x.add = id0 > 0;
-      if ((e = launch_tokens<kDX>(x, p.M, st)) != hipSuccess) return e;
-    }
-    if (p.dW) {
-      VocabTile x = t;
-      x.A = at<uint16_t>(ws, w.xc);
-      x.lda = p.K;
-      x.B = G;
-      x.ldb = w.piece;
-      x.ext_a = p.K;
-      x.out16 = p.dW + id0 * p.lddw;
-      x.ldo = p.lddw;
-      if ((e = launch_one<kDW, 256, 256, 2, 4, 2>(x, ids, st)) != hipSuccess) return e;
-    }
+    VocabTile x = t, y = t;  // dX, dW
+    x.B = y.B = G;
+    x.ldb = y.ldb = w.piece;
+    x.ext_a = y.ext_a = p.K;
+    x.splits = w.splits;
+    x.out32 = at<float>(ws, w.dx);
+    x.rows32 = p.M;
+    x.add = id0 > 0;
+    y.A = at<uint16_t>(ws, w.xc);
+    y.lda = p.K;
+    y.out16 = p.dW + (p.dW ? id0 * p.lddw : 0);
+    y.ldo = p.lddw;
+    if (p.dX && p.dW) e = launch_both(x, y, p.M, st);
+    else if (p.dX) e = launch_tokens<kDX>(x, p.M, st);
+    else e = launch_one<kDW, 256, 2, 4, 2>(y, ids, st);
+    if (e != hipSuccess) return e;
   }
   if (p.dX)
     hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M), dim3(256), 0, st, at<float>(ws, w.dx), w.splits, p.M,
