@@ -85,27 +85,84 @@ __global__ __launch_bounds__(256) void vocab_list_kernel(const int64_t* __restri
   if (lane == 0) mass[t] = sum / div;
 }
 
-// One block: numbers the tokens that have a list (key 0 of a list of L; or, with `target`,
-// an id in [0, N), which becomes the key), and writes zeros as the others' results.
-__global__ __launch_bounds__(1024) void vocab_scan_kernel(const int64_t* __restrict__ target, int* keys, int L,
-                                                          int64_t M, int64_t N, int* __restrict__ nv,
-                                                          int* __restrict__ map, int* __restrict__ inv,
-                                                          float* __restrict__ value, float* __restrict__ lse) {
+// Whether token t has a list (key 0 of its L), or, with `target`, an id in [0, N).
+__device__ __forceinline__ bool vocab_live(const int64_t* target, const int* keys, int L, int64_t N, int64_t t) {
+  if (!target) return keys[t * L] != kNone;
+  const int64_t id = target[t];
+  return id >= 0 && id < N;
+}
+
+struct VocabCompact {
+  const int64_t* target;  // NULL: lists
+  int* keys;              // [M][L]; written (L = 1) with `target`
+  int L;
+  int64_t M, N, K, ldx;
+  const uint16_t* X;
+  uint16_t* Xc;  // rows of the compact tokens; twice over where nv <= twice
+  int twice;
+  int *nv, *map, *inv;
+  float *value, *lse;  // losses: masked tokens' results
+};
+
+// Token t (live, compact number c of n): its entries of the tables, its rows of Xc. One block.
+__device__ __forceinline__ void vocab_take_row(const VocabCompact& p, int64_t t, int c, int n) {
+  const uint4* src = reinterpret_cast<const uint4*>(p.X + t * p.ldx);
+  uint4* dst = reinterpret_cast<uint4*>(p.Xc + c * p.K);
+  const int64_t again = n <= p.twice ? n * p.K / 8 : 0;
+  for (int64_t i = threadIdx.x; i < p.K >> 3; i += 256) {
+    const uint4 v = src[i];
+    dst[i] = v;
+    if (again) dst[again + i] = v;
+  }
+}
+
+// Compact numbers and rows in one launch, a block a token that counts the live ones itself
+// (M reads a block: up to kVocabCount tokens less than another launch).
+constexpr int64_t kVocabCount = 2048;
+__global__ __launch_bounds__(256) void vocab_compact_kernel(const VocabCompact p) {
+  __shared__ int below[4], all[4];
+  const int64_t t = blockIdx.x;
+  int nb = 0, na = 0;
+  bool mine = false;
+  for (int64_t i = threadIdx.x; i < p.M; i += 256) {
+    const bool live = vocab_live(p.target, p.keys, p.L, p.N, i);
+    nb += live && i < t;
+    na += live;
+    mine |= live && i == t;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    nb += __shfl_xor(nb, o, 64);
+    na += __shfl_xor(na, o, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    below[threadIdx.x >> 6] = nb;
+    all[threadIdx.x >> 6] = na;
+  }
+  const bool live = __syncthreads_or(mine);
+  const int c = below[0] + below[1] + below[2] + below[3], n = all[0] + all[1] + all[2] + all[3];
+  if (threadIdx.x == 0) {
+    if (t == 0) *p.nv = n;
+    if (p.target) p.keys[t] = live ? (int)p.target[t] : kNone;
+    p.inv[t] = live ? c : -1;
+    if (live) {
+      p.map[c] = (int)t;
+    } else if (p.value) {
+      p.value[t] = 0.0f;
+      p.lse[t] = 0.0f;
+    }
+  }
+  if (live) vocab_take_row(p, t, c, n);
+}
+
+// The same for more tokens: one block numbers them, then a block a compact token copies.
+__global__ __launch_bounds__(1024) void vocab_scan_kernel(const VocabCompact p) {
   __shared__ int wsum[2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int base = 0, buf = 0;
-  for (int64_t t0 = 0; t0 < M; t0 += 1024, buf ^= 1) {
+  for (int64_t t0 = 0; t0 < p.M; t0 += 1024, buf ^= 1) {
     const int64_t t = t0 + threadIdx.x;
-    bool live = false;
-    if (t < M) {
-      if (target) {
-        const int64_t id = target[t];
-        live = id >= 0 && id < N;
-        keys[t] = live ? (int)id : kNone;
-      } else {
-        live = keys[t * L] != kNone;
-      }
-    }
+    const bool live = t < p.M && vocab_live(p.target, p.keys, p.L, p.N, t);
     const uint64_t b = __ballot(live);
     if (lane == 0) wsum[buf][wave] = __popcll(b);
     __syncthreads();
@@ -116,29 +173,24 @@ __global__ __launch_bounds__(1024) void vocab_scan_kernel(const int64_t* __restr
       all += wsum[buf][w];
     }
     const int c = before + __popcll(b & (((uint64_t)1 << lane) - 1));
-    if (t < M) {
-      inv[t] = live ? c : -1;
+    if (t < p.M) {
+      if (p.target) p.keys[t] = live ? (int)p.target[t] : kNone;
+      p.inv[t] = live ? c : -1;
       if (live) {
-        map[c] = (int)t;
-      } else if (value) {
-        value[t] = 0.0f;
-        lse[t] = 0.0f;
+        p.map[c] = (int)t;
+      } else if (p.value) {
+        p.value[t] = 0.0f;
+        p.lse[t] = 0.0f;
       }
     }
     base += all;
   }
-  if (threadIdx.x == 0) *nv = base;
+  if (threadIdx.x == 0) *p.nv = base;
 }
 
-// Rows of the compact tokens, 16 bytes a thread.
-__global__ __launch_bounds__(256) void vocab_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t K,
-                                                           const int* __restrict__ nv, const int* __restrict__ map,
-                                                           uint16_t* __restrict__ Xc) {
-  const int64_t cpr = K >> 3, c = blockIdx.x;
-  if (c >= *nv) return;
-  const uint4* src = reinterpret_cast<const uint4*>(X + (int64_t)map[c] * ldx);
-  uint4* dst = reinterpret_cast<uint4*>(Xc + c * K);
-  for (int64_t i = threadIdx.x; i < cpr; i += 256) dst[i] = src[i];
+__global__ __launch_bounds__(256) void vocab_gather_kernel(const VocabCompact p) {
+  const int c = blockIdx.x, n = *p.nv;
+  if (c < n) vocab_take_row(p, p.map[c], c, n);
 }
 
 // ---------------------------------------------------------------------------
@@ -169,6 +221,7 @@ struct VocabTile {
   float* out32;    // kDX: [splits][rows32][K]
   int64_t rows32;
   int add;         // kDX: add to what is there
+  int twice;       // up to so many compact tokens G is held in two parts
 };
 
 // A block: BN x BM outputs, A side by B side, over K steps of 64 through a ring of S
@@ -186,9 +239,9 @@ struct VocabTile {
 // Register 4 q + r of a fragment: A side 8 q + 4 lg + r, B side lane % 32.
 //
 // `block` and the grid it belongs to may be a part of the launch's.
-template <int BN, int BM, int S>
-constexpr int ring_bytes() {
-  return S * (BN + (BM < 64 ? 64 : BM)) * 128;  // copies of 8 rows, one a wave at least
+template <int BN, int BM, int NW, int S>
+constexpr int ring_bytes() {  // copies of 8 rows (1 KB), as many by each wave
+  return S * ((BN / 8 + NW - 1) / NW + (BM / 8 + NW - 1) / NW) * NW * 1024;
 }
 
 template <int MODE, int BN, int BM, int WN, int WM, int S>
@@ -204,11 +257,13 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   static_assert(!TA || BN % 128 == 0, "columns: whole 64-byte pieces of four");
   static_assert(!TB || BM % 128 == 0, "columns: whole 64-byte pieces of four");
   static_assert(S >= 2 && (S - 1) * NI <= 63 && S * STAGE <= 160 * 1024, "ring");
-  static_assert(S * STAGE == ring_bytes<BN, BM, S>(), "the kernels' array");
+  static_assert(S * STAGE == ring_bytes<BN, BM, NW, S>(), "the kernels' array");
 
   const int nv = *p.nv;
-  const int64_t ext_b = MODE == kDW ? p.ids : nv;
-  const int64_t klen = MODE == kDW ? nv : (MODE == kDX ? p.ids : p.K);
+  const bool twice = nv <= p.twice;       // G in two parts of bf16
+  const int rows = twice ? 2 * nv : nv;   // of G, and of X beside it
+  const int64_t ext_b = MODE == kDW ? p.ids : (MODE == kDX ? rows : nv);
+  const int64_t klen = MODE == kDW ? rows : (MODE == kDX ? p.ids : p.K);
   const int stages = (int)((klen + KS - 1) / KS);
 
   // An XCD takes one contiguous part of the tiles; groups of up to 8 B tiles share A tiles.
@@ -488,8 +543,9 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   }
 
   if constexpr (MODE == kGrad) {
-    // G in fp32, rounded once to bf16 (half a step, 2^-8 of each element: a product of two
-    // bf16 operands is what the matrix cores take)
+    // G in fp32. The matrix cores take bf16: up to `twice` tokens, where the products are
+    // bound by memory, G is held in two parts (its rounding to bf16 and what that left: 2^-16 of
+    // each element); beyond, rounded once (2^-8, as much as the results' own rounding).
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       float a = 0.0f, l2 = 0.0f, gt = 0.0f;
@@ -519,7 +575,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       const int64_t c = b0 + wm * WTM + 32 * j + lr;
-      if (c >= nv) continue;
+      if (c >= ext_b) continue;
       float* row = p.out32 + ((int64_t)split * p.rows32 + c) * p.K;
 #pragma unroll
       for (int i = 0; i < FN; ++i)
@@ -550,8 +606,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     const int64_t row0 = b0 + wm * WTM, lim = MODE == kGrad ? nv : p.ids;
     const int64_t col0 = a0 + wn * WTN, left = MODE == kGrad ? WTN : p.K - col0;
     constexpr int CPR = WTN / 8;
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    auto rows_out = [&](int j, uint16_t* out) {
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -566,17 +621,31 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
         const int c = lane + 64 * k, ml = c / CPR, nl = 8 * (c % CPR);
         const int64_t m = row0 + 32 * j + ml;
         if (m < lim && nl < left)
-          *reinterpret_cast<uint4*>(p.out16 + m * p.ldo + col0 + nl) =
+          *reinterpret_cast<uint4*>(out + m * p.ldo + col0 + nl) =
               *reinterpret_cast<const uint4*>(so + ml * LD + nl * 2);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+#pragma unroll
+    for (int j = 0; j < FM; ++j) rows_out(j, p.out16);
+    if constexpr (MODE == kGrad) {
+      if (!twice) return;
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            acc[i][j][r] -= __uint_as_float(bf16_pair(0.0f, acc[i][j][r]) & 0xffff0000u);
+        rows_out(j, p.out16 + nv * p.ldo);
+      }
     }
   }
 }
 
 template <int MODE, int BN, int BM, int WN, int WM, int S>
 __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const VocabTile p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[ring_bytes<BN, BM, S>()];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[ring_bytes<BN, BM, WN * WM, S>()];
   vocab_tile<MODE, BN, BM, WN, WM, S>(p, blockIdx.x, smem);
 }
 
@@ -585,71 +654,60 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const Vocab
 template <int BM, int WN, int WM, int S>
 __global__ __launch_bounds__(512, 1) void vocab_grads_kernel(const VocabTile x, const VocabTile w, int dx_blocks) {
   static_assert(WN * WM == 8, "one block size");
-  constexpr int A = ring_bytes<256, BM, S>(), C = ring_bytes<256, 256, 2>();
+  constexpr int A = ring_bytes<256, BM, 8, S>(), C = ring_bytes<256, 256, 8, 2>();
   __shared__ __attribute__((aligned(1024))) uint8_t smem[A > C ? A : C];
   if ((int)blockIdx.x < dx_blocks) vocab_tile<kDX, 256, BM, WN, WM, S>(x, blockIdx.x, smem);
   else vocab_tile<kDW, 256, 256, 2, 4, 2>(w, blockIdx.x - dx_blocks, smem);
 }
 
-// Sums of the tiles' parts, 16 compact tokens a block, 64 threads each: lse, and
-// sum_j p (log p - (z_j - lse)) (with wts) or z - lse. Float64, fixed order.
-__global__ __launch_bounds__(1024) void vocab_finish_kernel(const float2* __restrict__ part, int64_t ldpart,
-                                                            int tiles, const int* __restrict__ nv,
-                                                            const int* __restrict__ map,
-                                                            const int* __restrict__ keys,
-                                                            const float* __restrict__ wts,
-                                                            const float* __restrict__ zl, int L,
-                                                            float* __restrict__ value, float* __restrict__ lse) {
-  __shared__ float red_m[64][17];
-  __shared__ double red_s[64][17];
-  const int tl = threadIdx.x & 15, gr = threadIdx.x >> 4;
-  const int64_t c = (int64_t)blockIdx.x * 16 + tl;
-  const int n = *nv;
-  if ((int64_t)blockIdx.x * 16 >= n) return;
+// Sums of the tiles' parts, a wave a compact token: lse, and sum_j p (log p - (z_j - lse))
+// (with wts) or z - lse. Float64, fixed order.
+__global__ __launch_bounds__(256) void vocab_finish_kernel(const float2* __restrict__ part, int64_t ldpart,
+                                                           int tiles, const int* __restrict__ nv,
+                                                           const int* __restrict__ map,
+                                                           const int* __restrict__ keys,
+                                                           const float* __restrict__ wts,
+                                                           const float* __restrict__ zl, int L,
+                                                           float* __restrict__ value, float* __restrict__ lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (c >= *nv) return;
+  const int64_t t = map[c];
   float m = -INFINITY;
   double s = 0.0;
-  if (c < n)
-    for (int i = gr; i < tiles; i += 64) {
-      const float2 v = part[(int64_t)i * ldpart + c];
-      if (v.x == -INFINITY && v.y == 0.0f) continue;
-      const float top = fmaxf(m, v.x);
-      s = s * (double)exp2f(m - top) + (double)v.y * (double)exp2f(v.x - top);
-      m = top;
-    }
-  red_m[gr][tl] = m;
-  red_s[gr][tl] = s;
-  __syncthreads();
-  for (int h = 32; h > 0; h >>= 1) {
-    if (gr < h) {
-      const float a = red_m[gr][tl], b = red_m[gr + h][tl], top = fmaxf(a, b);
-      if (top != -INFINITY)
-        red_s[gr][tl] = red_s[gr][tl] * (double)exp2f(a - top) + red_s[gr + h][tl] * (double)exp2f(b - top);
-      red_m[gr][tl] = top;
-    }
-    __syncthreads();
+  constexpr int U = 8;
+  for (int i0 = lane; i0 < tiles; i0 += 64 * U) {
+    float2 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = i0 + 64 * u < tiles ? part[(int64_t)(i0 + 64 * u) * ldpart + c] : make_float2(-INFINITY, 0.0f);
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, v[u].x);
+    const float sub = top == -INFINITY ? 0.0f : top;
+    s *= (double)exp2f(m - sub);
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += (double)(v[u].y * exp2f(v[u].x - sub));
+    m = top;
   }
-  const double total = ((double)red_m[0][tl] + log2(red_s[0][tl])) * kLn2;
-  __syncthreads();
-  const int64_t t = c < n ? map[c] : 0;
+  const float top = wave_max(m);
+  s *= (double)exp2f(m - (top == -INFINITY ? 0.0f : top));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  const double total = ((double)top + log2(s)) * kLn2;
   double v = 0.0;
-  if (c < n) {
-    if (wts) {
-      for (int j = gr; j < L; j += 64) {
-        const double w = (double)wts[t * L + j];
-        if (keys[t * L + j] != kNone && w != 0.0) v += w * (log(w) - ((double)zl[t * L + j] - total));
-      }
-    } else if (gr == 0) {
-      v = (double)zl[t] - total;
+  if (wts) {
+    for (int j = lane; j < L; j += 64) {
+      const double w = (double)wts[t * L + j];
+      if (keys[t * L + j] != kNone && w != 0.0) v += w * (log(w) - ((double)zl[t * L + j] - total));
     }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  } else {
+    v = (double)zl[t] - total;
   }
-  red_s[gr][tl] = v;
-  __syncthreads();
-  for (int h = 32; h > 0; h >>= 1) {
-    if (gr < h) red_s[gr][tl] += red_s[gr + h][tl];
-    __syncthreads();
-  }
-  if (gr == 0 && c < n) {
-    value[t] = (float)red_s[0][tl];
+  if (lane == 0) {
+    value[t] = (float)v;
     lse[t] = (float)total;
   }
 }
@@ -657,13 +715,16 @@ __global__ __launch_bounds__(1024) void vocab_finish_kernel(const float2* __rest
 // dX of all tokens: the splits' sums in order, rounded once; zeros for masked tokens.
 __global__ __launch_bounds__(256) void vocab_dx_kernel(const float* __restrict__ part, int splits, int64_t rows,
                                                        int64_t K, const int* __restrict__ inv,
+                                                       const int* __restrict__ nv, int twice,
                                                        uint16_t* __restrict__ dX, int64_t lddx) {
   const int64_t t = blockIdx.x, c = inv[t];
+  const int n = *nv, parts = n <= twice ? 2 : 1;
   for (int64_t i = threadIdx.x; i < K >> 3; i += 256) {
     float v[8] = {};
     if (c >= 0)
-      for (int s = 0; s < splits; ++s) {
-        const float4* q = reinterpret_cast<const float4*>(part + (s * rows + c) * K) + 2 * i;
+      for (int s = 0; s < splits * parts; ++s) {  // parts of G innermost
+        const int64_t row = (s / parts) * rows + c + (s % parts) * n;
+        const float4* q = reinterpret_cast<const float4*>(part + row * K) + 2 * i;
         const float4 a = q[0], b = q[1];
         v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
         v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
@@ -685,45 +746,99 @@ __global__ __launch_bounds__(256) void vocab_zero_kernel(uint16_t* __restrict__ 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Up to so many tokens that count G is held in two parts of bf16.
+constexpr int kTwice = 128;
+int64_t grad_rows(int64_t M) { return M <= kTwice ? 2 * M : (M < 2 * kTwice ? 2 * kTwice : M); }
+
 // Blocks of a product, a multiple of 8 (an XCD's share each).
-int64_t product_blocks(VocabTile& p, int64_t max_b, int BM) {
-  p.tiles_a = (int)ceil_div(p.ext_a, 256);
+int64_t product_blocks(VocabTile& p, int64_t max_b, int BN, int BM) {
+  p.tiles_a = (int)ceil_div(p.ext_a, BN);
   return ceil_div(p.tiles_a * ceil_div(max_b, BM) * p.splits, 8) * 8;
 }
 
-template <int MODE, int BM, int WN, int WM, int S>
+template <int MODE, int BN, int BM, int WN, int WM, int S>
 hipError_t launch_one(VocabTile p, int64_t max_b, hipStream_t st) {
-  const dim3 grid((unsigned)product_blocks(p, max_b, BM));
-  hipLaunchKernelGGL((vocab_tile_kernel<MODE, 256, BM, WN, WM, S>), grid, dim3(512), 0, st, p);
+  const dim3 grid((unsigned)product_blocks(p, max_b, BN, BM));
+  hipLaunchKernelGGL((vocab_tile_kernel<MODE, BN, BM, WN, WM, S>), grid, dim3(64 * WN * WM), 0, st, p);
   return hipGetLastError();
 }
 
 template <int BM, int WN, int WM, int S>
-hipError_t launch_grads(VocabTile x, VocabTile w, int64_t M, hipStream_t st) {
-  const int64_t nx = product_blocks(x, M, BM), nw = product_blocks(w, w.ids, 256);
+hipError_t launch_grads(VocabTile x, VocabTile w, int64_t rows, hipStream_t st) {
+  const int64_t nx = product_blocks(x, rows, 256, BM), nw = product_blocks(w, w.ids, 256, 256);
   hipLaunchKernelGGL((vocab_grads_kernel<BM, WN, WM, S>), dim3((unsigned)(nx + nw)), dim3(512), 0, st, x, w, (int)nx);
   return hipGetLastError();
 }
 
-// Tokens of a tile by their number.
-int tile_tokens(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+// Tiles of the logits' products, and what a round of them takes: us a stage and beside
+// the stages, measured where the matrix cores and copies bind (one card; 257 tokens of 100003
+// ids, 3584 wide: 64 x 32 tiles 641 us, 64 x 64 427, 64 x 128 385, 256 x 32 604, 256 x 64 352, 256 x 128 307,
+// 256 x 256 381; 64 tokens of 5000 ids: 26, 26, 29, 35, 38, 48, 76; 64 of 131072: 249, 193, 211, 207, 171, 177, 229).
+// What memory bounds takes the same on every tile.
+struct LogitTile {
+  int bn, bm;     // ids, tokens
+  int per_round;  // tiles that the CUs hold at once
+  float stage, base;
+};
+const LogitTile kLogitTiles[] = {
+    {64, 32, 512, 0.375f, 2.0f}, {64, 64, 512, 0.44f, 3.0f},  {64, 128, 512, 0.66f, 4.0f}, {256, 32, 256, 0.66f, 3.0f},
+    {256, 64, 256, 0.73f, 4.0f}, {256, 128, 256, 0.98f, 7.0f}, {256, 256, 256, 1.5f, 11.0f},
+};
+
+const LogitTile& logit_tile(int64_t M, int64_t N, int64_t K) {
+#ifdef FORCE_TILE
+  return kLogitTiles[FORCE_TILE];
+#endif
+  const LogitTile* best = nullptr;
+  float least = 0.0f;
+  for (const LogitTile& t : kLogitTiles) {
+    const int64_t tiles = ceil_div(N, t.bn) * ceil_div(M, t.bm);
+    const float cost = (float)ceil_div(tiles, t.per_round) * (t.stage * (float)ceil_div(K, 64) + t.base);
+    if (!best || cost < least) {
+      best = &t;
+      least = cost;
+    }
+  }
+  return *best;
+}
 
 template <int MODE>
-hipError_t launch_tokens(const VocabTile& p, int64_t M, hipStream_t st) {
-  switch (tile_tokens(M)) {
-    case 32: return launch_one<MODE, 32, 8, 1, 4>(p, M, st);
-    case 64: return launch_one<MODE, 64, 4, 2, 3>(p, M, st);
-    case 128: return launch_one<MODE, 128, 4, 2, 3>(p, M, st);
-    default: return launch_one<MODE, 256, 2, 4, 2>(p, M, st);
+hipError_t launch_logits(const VocabTile& p, const LogitTile& t, int64_t M, hipStream_t st) {
+  if (t.bn == 64) {
+    if (t.bm == 32) return launch_one<MODE, 64, 32, 2, 1, 6>(p, M, st);
+    if (t.bm == 64) return launch_one<MODE, 64, 64, 2, 2, 5>(p, M, st);
+    return launch_one<MODE, 64, 128, 2, 2, 3>(p, M, st);
+  }
+  switch (t.bm) {
+    case 32: return launch_one<MODE, 256, 32, 8, 1, 4>(p, M, st);
+    case 64: return launch_one<MODE, 256, 64, 4, 2, 3>(p, M, st);
+    case 128: return launch_one<MODE, 256, 128, 4, 2, 3>(p, M, st);
+    default: return launch_one<MODE, 256, 256, 2, 4, 2>(p, M, st);
   }
 }
 
-hipError_t launch_both(const VocabTile& x, const VocabTile& w, int64_t M, hipStream_t st) {
-  switch (tile_tokens(M)) {
-    case 32: return launch_grads<32, 8, 1, 4>(x, w, M, st);
-    case 64: return launch_grads<64, 4, 2, 3>(x, w, M, st);
-    case 128: return launch_grads<128, 4, 2, 3>(x, w, M, st);
-    default: return launch_grads<256, 2, 4, 2>(x, w, M, st);
+// Rows of G in a tile of dX
+int dx_tile(int64_t rows) {
+  if (rows <= 32) return 32;
+  if (rows <= 64) return 64;
+  return ceil_div(rows, 128) * 55 < ceil_div(rows, 256) * 92 ? 128 : 256;
+}
+
+hipError_t launch_dx(const VocabTile& x, int64_t rows, hipStream_t st) {
+  switch (dx_tile(rows)) {
+    case 32: return launch_one<kDX, 256, 32, 8, 1, 4>(x, rows, st);
+    case 64: return launch_one<kDX, 256, 64, 4, 2, 3>(x, rows, st);
+    case 128: return launch_one<kDX, 256, 128, 4, 2, 3>(x, rows, st);
+    default: return launch_one<kDX, 256, 256, 2, 4, 2>(x, rows, st);
+  }
+}
+
+hipError_t launch_both(const VocabTile& x, const VocabTile& w, int64_t rows, hipStream_t st) {
+  switch (dx_tile(rows)) {
+    case 32: return launch_grads<32, 8, 1, 4>(x, w, rows, st);
+    case 64: return launch_grads<64, 4, 2, 3>(x, w, rows, st);
+    case 128: return launch_grads<128, 4, 2, 3>(x, w, rows, st);
+    default: return launch_grads<256, 2, 4, 2>(x, w, rows, st);
   }
 }
 
@@ -749,21 +864,22 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad)
     w.wts = take((size_t)(M * L) * 4);
     w.mass = take((size_t)M * 4);
   }
-  w.xc = take((size_t)(M * K) * 2);
+  const int64_t rows = grad ? grad_rows(M) : M;
+  w.xc = take((size_t)(rows * K) * 2);
   if (!grad) {
     w.zl = take((size_t)(M * L) * 4);
-    w.part = take((size_t)(ceil_div(N, 256) * M) * 8);
+    w.part = take((size_t)(ceil_div(N, logit_tile(M, N, K).bn) * M) * 8);
   } else {
     // G of a piece: 256 MiB, between 4096 ids and all of them
-    const int64_t want = ((int64_t)128 << 20) / M / 256 * 256;
+    const int64_t want = ((int64_t)128 << 20) / rows / 256 * 256;
     w.piece = want < 4096 ? 4096 : want;
     if (w.piece > N) w.piece = ceil_div(N, 256) * 256;
-    const int64_t tiles = ceil_div(K, 256) * ceil_div(M, tile_tokens(M));
+    const int64_t tiles = ceil_div(K, 256) * ceil_div(rows, dx_tile(rows));
     int64_t s = 256 / tiles;
     if (s > w.piece / 256) s = w.piece / 256;
     w.splits = (int)(s < 1 ? 1 : s);
-    w.g = take((size_t)(M * w.piece) * 2);
-    w.dx = take((size_t)(w.splits * M * K) * 4);
+    w.g = take((size_t)(rows * w.piece) * 2);
+    w.dx = take((size_t)(w.splits * rows * K) * 4);
   }
   w.bytes = at;
   return w;
@@ -788,11 +904,26 @@ hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, hipStream_t st
                          p.M, p.N, (int)p.L, p.scale, at<int>(ws, w.keys), at<float>(ws, w.wts),
                          at<float>(ws, w.mass));
   }
-  hipLaunchKernelGGL(vocab_scan_kernel, dim3(1), dim3(1024), 0, st, p.index ? nullptr : p.target,
-                     at<int>(ws, w.keys), (int)p.L, p.M, p.N, at<int>(ws, w.nv), at<int>(ws, w.map),
-                     at<int>(ws, w.inv), p.value, p.lse_out);
-  hipLaunchKernelGGL(vocab_gather_kernel, dim3((unsigned)p.M), dim3(256), 0, st, p.X, p.ldx, p.K,
-                     at<int>(ws, w.nv), at<int>(ws, w.map), at<uint16_t>(ws, w.xc));
+  VocabCompact c = {};
+  c.target = p.index ? nullptr : p.target;
+  c.keys = at<int>(ws, w.keys);
+  c.L = (int)p.L;
+  c.M = p.M; c.N = p.N; c.K = p.K; c.ldx = p.ldx;
+  c.X = p.X;
+  c.Xc = at<uint16_t>(ws, w.xc);
+  c.twice = p.lse_out ? -1 : kTwice;
+  c.nv = at<int>(ws, w.nv);
+  c.map = at<int>(ws, w.map);
+  c.inv = at<int>(ws, w.inv);
+  c.value = p.value;
+  c.lse = p.lse_out;
+  const dim3 grid((unsigned)p.M);
+  if (p.M <= kVocabCount) {
+    hipLaunchKernelGGL(vocab_compact_kernel, grid, dim3(256), 0, st, c);
+  } else {
+    hipLaunchKernelGGL(vocab_scan_kernel, dim3(1), dim3(1024), 0, st, c);
+    hipLaunchKernelGGL(vocab_gather_kernel, grid, dim3(256), 0, st, c);
+  }
   return hipGetLastError();
 }
 
@@ -809,6 +940,7 @@ VocabTile common(const VocabArgs& p, const Layout& w, void* ws) {
   t.L = (int)p.L;
   t.scale = p.scale;
   t.splits = 1;
+  t.twice = p.lse_out ? -1 : kTwice;
   return t;
 }
 
@@ -831,10 +963,11 @@ hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
   t.part = at<float2>(ws, w.part);
   t.ldpart = p.M;
   t.zl = at<float>(ws, w.zl);
-  e = launch_tokens<kSums>(t, p.M, st);
+  const LogitTile& tile = logit_tile(p.M, p.N, p.K);
+  e = launch_logits<kSums>(t, tile, p.M, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(vocab_finish_kernel, dim3((unsigned)ceil_div(p.M, 16)), dim3(1024), 0, st, t.part, t.ldpart,
-                     (int)ceil_div(p.N, 256), t.nv, t.map, t.keys, t.wts, t.zl, t.L, p.value, p.lse_out);
+  hipLaunchKernelGGL(vocab_finish_kernel, dim3((unsigned)ceil_div(p.M, 4)), dim3(256), 0, st, t.part, t.ldpart,
+                     (int)ceil_div(p.N, tile.bn), t.nv, t.map, t.keys, t.wts, t.zl, t.L, p.value, p.lse_out);
   return hipGetLastError();
 }
 
@@ -847,6 +980,7 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
   hipError_t e = prepare(p, w, ws, st);
   if (e != hipSuccess) return e;
   uint16_t* G = at<uint16_t>(ws, w.g);
+  const int64_t rows = grad_rows(p.M);
   for (int64_t id0 = 0; id0 < p.N; id0 += w.piece) {
     const int64_t ids = p.N - id0 < w.piece ? p.N - id0 : w.piece;
     VocabTile t = common(p, w, ws);
@@ -861,27 +995,27 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     t.sign = p.index ? 1.0f : -1.0f;
     t.out16 = G;
     t.ldo = w.piece;
-    if ((e = launch_tokens<kGrad>(t, p.M, st)) != hipSuccess) return e;
+    if ((e = launch_logits<kGrad>(t, logit_tile(p.M, ids, p.K), p.M, st)) != hipSuccess) return e;
     VocabTile x = t, y = t;  // dX, dW
     x.B = y.B = G;
     x.ldb = y.ldb = w.piece;
     x.ext_a = y.ext_a = p.K;
     x.splits = w.splits;
     x.out32 = at<float>(ws, w.dx);
-    x.rows32 = p.M;
+    x.rows32 = rows;
     x.add = id0 > 0;
     y.A = at<uint16_t>(ws, w.xc);
     y.lda = p.K;
     y.out16 = p.dW + (p.dW ? id0 * p.lddw : 0);
     y.ldo = p.lddw;
-    if (p.dX && p.dW) e = launch_both(x, y, p.M, st);
-    else if (p.dX) e = launch_tokens<kDX>(x, p.M, st);
-    else e = launch_one<kDW, 256, 2, 4, 2>(y, ids, st);
+    if (p.dX && p.dW) e = launch_both(x, y, rows, st);
+    else if (p.dX) e = launch_dx(x, rows, st);
+    else e = launch_one<kDW, 256, 256, 2, 4, 2>(y, ids, st);
     if (e != hipSuccess) return e;
   }
   if (p.dX)
-    hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M), dim3(256), 0, st, at<float>(ws, w.dx), w.splits, p.M,
-                       p.K, at<int>(ws, w.inv), p.dX, p.lddx);
+    hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M), dim3(256), 0, st, at<float>(ws, w.dx), w.splits, rows,
+                       p.K, at<int>(ws, w.inv), at<int>(ws, w.nv), kTwice, p.dX, p.lddx);
   return hipGetLastError();
 }
 
