@@ -221,6 +221,12 @@ struct VocabTile {
   float* out32;    // kDX: [splits][rows32][K]
   int64_t rows32;
   int add;         // kDX: add to what is there
+  // kSums, kGrad, kDX: W's copies carry the non-temporal hint; kDW: stores do. Where a
+  // tile holds all tokens nothing of W is read again, and dW is written to be read later (us
+  // with / without, 3584 wide, W past the MALL or not there yet): logp 1 x 131072 145 / 164, 128 x
+  // 131072 166 / 181, 1 x 32768 45 / 50; gradient 1 x 131072 466 / 575, 33 x 32768 148 / 183. kGrad reads
+  // without it where kDX will find W in the MALL (33 x 32768: 3 us).
+  bool stream;
   int twice;       // up to so many compact tokens G is held in two parts
 };
 
@@ -352,6 +358,15 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
           a = c * 8;
         }
         if (a >= left) vo[e] = kBig - 1024u * (uint32_t)e;
+      }
+    }
+    if constexpr (MODE != kDW && BM <= 128) {
+      if (isA && p.stream) {
+        if (cnt == 4) dma_group<4, true>(lds, vo, r, soff);
+        else if (cnt == 3) dma_group<3, true>(lds, vo, r, soff);
+        else if (cnt == 2) dma_group<2, true>(lds, vo, r, soff);
+        else dma_group<1, true>(lds, vo, r, soff);
+        return;
       }
     }
     if (cnt == 4) dma_group<4, false>(lds, vo, r, soff);
@@ -606,7 +621,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     const int64_t row0 = b0 + wm * WTM, lim = MODE == kGrad ? nv : p.ids;
     const int64_t col0 = a0 + wn * WTN, left = MODE == kGrad ? WTN : p.K - col0;
     constexpr int CPR = WTN / 8;
-    auto rows_out = [&](int j, uint16_t* out) {
+    auto rows_out = [&](int j, uint16_t* out, auto nt) {
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -620,14 +635,23 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       for (int k = 0; k < 32 * CPR / 64; ++k) {
         const int c = lane + 64 * k, ml = c / CPR, nl = 8 * (c % CPR);
         const int64_t m = row0 + 32 * j + ml;
-        if (m < lim && nl < left)
-          *reinterpret_cast<uint4*>(out + m * p.ldo + col0 + nl) =
-              *reinterpret_cast<const uint4*>(so + ml * LD + nl * 2);
+        if (m >= lim || nl >= left) continue;
+        typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+        const u4 v = *reinterpret_cast<const u4*>(so + ml * LD + nl * 2);
+        u4* dst = reinterpret_cast<u4*>(out + m * p.ldo + col0 + nl);
+        if constexpr (decltype(nt)::value) __builtin_nontemporal_store(v, dst);
+        else *dst = v;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
+    // (the branch around the loop: around the store the two are merged, without nt)
+    if (MODE == kDW && p.stream) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) rows_out(j, p.out16);
+      for (int j = 0; j < FM; ++j) rows_out(j, p.out16, std::true_type{});
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) rows_out(j, p.out16, std::false_type{});
     if constexpr (MODE == kGrad) {
       if (!twice) return;
 #pragma unroll
@@ -637,7 +661,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             acc[i][j][r] -= __uint_as_float(bf16_pair(0.0f, acc[i][j][r]) & 0xffff0000u);
-        rows_out(j, p.out16 + nv * p.ldo);
+        rows_out(j, p.out16 + nv * p.ldo, std::false_type{});
       }
     }
   }
@@ -712,26 +736,36 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const float2* __restr
   }
 }
 
-// dX of all tokens: the splits' sums in order, rounded once; zeros for masked tokens.
-__global__ __launch_bounds__(256) void vocab_dx_kernel(const float* __restrict__ part, int splits, int64_t rows,
-                                                       int64_t K, const int* __restrict__ inv,
-                                                       const int* __restrict__ nv, int twice,
-                                                       uint16_t* __restrict__ dX, int64_t lddx) {
-  const int64_t t = blockIdx.x, c = inv[t];
-  const int n = *nv, parts = n <= twice ? 2 : 1;
-  for (int64_t i = threadIdx.x; i < K >> 3; i += 256) {
-    float v[8] = {};
-    if (c >= 0)
-      for (int s = 0; s < splits * parts; ++s) {  // parts of G innermost
-        const int64_t row = (s / parts) * rows + c + (s % parts) * n;
-        const float4* q = reinterpret_cast<const float4*>(part + row * K) + 2 * i;
-        const float4 a = q[0], b = q[1];
-        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+// dX of all tokens: the splits' sums in order (a split's parts of G one after the other),
+// rounded once; zeros for masked tokens. A wave takes 256 values of a token, eight sums at
+// once, so that a few tokens still fill the chip.
+__global__ __launch_bounds__(64) void vocab_dx_kernel(const float* __restrict__ part, int splits, int64_t rows,
+                                                      int64_t K, const int* __restrict__ inv,
+                                                      const int* __restrict__ nv, int twice,
+                                                      uint16_t* __restrict__ dX, int64_t lddx) {
+  const int64_t t = blockIdx.x, c = inv[t], h = 256 * (int64_t)blockIdx.y + 4 * threadIdx.x;
+  if (h >= K) return;
+  const int n = *nv, parts = n <= twice ? 2 : 1, sums = splits * parts;
+  float v[4] = {};
+  if (c >= 0) {
+    constexpr int U = 8;
+    for (int s0 = 0; s0 < sums; s0 += U) {
+      float4 a[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int s = s0 + u < sums ? s0 + u : sums - 1;
+        const int64_t row = (parts == 2 ? s >> 1 : s) * rows + c + (parts == 2 ? (s & 1) * n : 0);
+        a[u] = *reinterpret_cast<const float4*>(part + row * K + h);
       }
-    *reinterpret_cast<uint4*>(dX + t * lddx + 8 * i) = make_uint4(
-        bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = s0 + u < sums;
+        v[0] += in ? a[u].x : 0.0f; v[1] += in ? a[u].y : 0.0f;
+        v[2] += in ? a[u].z : 0.0f; v[3] += in ? a[u].w : 0.0f;
+      }
+    }
   }
+  *reinterpret_cast<uint2*>(dX + t * lddx + h) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
 }
 
 // dW where there are no tokens at all.
@@ -745,6 +779,8 @@ __global__ __launch_bounds__(256) void vocab_zero_kernel(uint16_t* __restrict__ 
 // ---------------------------------------------------------------------------
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+constexpr int64_t kMall = (int64_t)256 << 20;
 
 // Up to so many tokens that count G is held in two parts of bf16.
 constexpr int kTwice = 128;
@@ -786,9 +822,6 @@ const LogitTile kLogitTiles[] = {
 };
 
 const LogitTile& logit_tile(int64_t M, int64_t N, int64_t K) {
-#ifdef FORCE_TILE
-  return kLogitTiles[FORCE_TILE];
-#endif
   const LogitTile* best = nullptr;
   float least = 0.0f;
   for (const LogitTile& t : kLogitTiles) {
@@ -875,7 +908,9 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad)
     w.piece = want < 4096 ? 4096 : want;
     if (w.piece > N) w.piece = ceil_div(N, 256) * 256;
     const int64_t tiles = ceil_div(K, 256) * ceil_div(rows, dx_tile(rows));
+    // as fill the CUs, while their sums (written and read once) stay a quarter of W's bytes
     int64_t s = 256 / tiles;
+    if (s > w.piece / (16 * rows)) s = w.piece / (16 * rows);
     if (s > w.piece / 256) s = w.piece / 256;
     w.splits = (int)(s < 1 ? 1 : s);
     w.g = take((size_t)(rows * w.piece) * 2);
@@ -964,6 +999,7 @@ hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
   t.ldpart = p.M;
   t.zl = at<float>(ws, w.zl);
   const LogitTile& tile = logit_tile(p.M, p.N, p.K);
+  t.stream = p.M <= tile.bm;
   e = launch_logits<kSums>(t, tile, p.M, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(vocab_finish_kernel, dim3((unsigned)ceil_div(p.M, 4)), dim3(256), 0, st, t.part, t.ldpart,
@@ -995,7 +1031,9 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     t.sign = p.index ? 1.0f : -1.0f;
     t.out16 = G;
     t.ldo = w.piece;
-    if ((e = launch_logits<kGrad>(t, logit_tile(p.M, ids, p.K), p.M, st)) != hipSuccess) return e;
+    const LogitTile& tile = logit_tile(p.M, ids, p.K);
+    t.stream = p.M <= tile.bm && (!p.dX || ids * p.K * 2 > kMall);
+    if ((e = launch_logits<kGrad>(t, tile, p.M, st)) != hipSuccess) return e;
     VocabTile x = t, y = t;  // dX, dW
     x.B = y.B = G;
     x.ldb = y.ldb = w.piece;
@@ -1004,6 +1042,8 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     x.out32 = at<float>(ws, w.dx);
     x.rows32 = rows;
     x.add = id0 > 0;
+    x.stream = rows <= dx_tile(rows);
+    y.stream = rows <= 2 * kTwice;
     y.A = at<uint16_t>(ws, w.xc);
     y.lda = p.K;
     y.out16 = p.dW + (p.dW ? id0 * p.lddw : 0);
@@ -1014,7 +1054,7 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (p.dX)
-    hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M), dim3(256), 0, st, at<float>(ws, w.dx), w.splits, rows,
+    hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M, (unsigned)ceil_div(p.K, 256)), dim3(64), 0, st, at<float>(ws, w.dx), w.splits, rows,
                        p.K, at<int>(ws, w.inv), at<int>(ws, w.nv), kTwice, p.dX, p.lddx);
   return hipGetLastError();
 }
