@@ -202,6 +202,9 @@ struct VocabTile {
   const uint16_t *A, *B;
   int64_t lda, ldb;
   const int* nv;
+  int direct;      // kSums, M of them: tokens are numbered by each block, B is X itself
+  const int64_t* target;
+  int64_t N;       // ids in all
   int64_t ext_a;   // extent of the A side: ids of the piece (kSums, kGrad), K (kDX, kDW)
   int64_t ids;     // ids of the piece
   int64_t id0;     // its first id
@@ -229,6 +232,31 @@ struct VocabTile {
   bool stream;
   int twice;       // up to so many compact tokens G is held in two parts
 };
+
+// Tokens that a launch's blocks number themselves (vocab_number).
+constexpr int kVocabDirect = 256;
+
+// The compact tokens of p.direct tokens into LDS (int [nv] from the start); their count. All
+// waves of the block; the caller synchronizes before it writes there again.
+__device__ __forceinline__ int vocab_number(const VocabTile& p, int wid, int lane, int waves, uint8_t* smem) {
+  int* const map = reinterpret_cast<int*>(smem);
+  uint64_t* const mask = reinterpret_cast<uint64_t*>(smem + kVocabDirect * 4);
+  for (int g = wid; g < kVocabDirect / 64; g += waves) {
+    const int t = 64 * g + lane;
+    const uint64_t b = __ballot(t < p.direct && vocab_live(p.target, p.keys, p.L, p.N, t));
+    if (lane == 0) mask[g] = b;
+  }
+  __syncthreads();
+  int n = 0;
+#pragma unroll
+  for (int g = 0; g < kVocabDirect / 64; ++g) {
+    const uint64_t b = mask[g];
+    if (g % waves == wid && ((b >> lane) & 1)) map[n + __popcll(b & (((uint64_t)1 << lane) - 1))] = 64 * g + lane;
+    n += __popcll(b);
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(n);
+}
 
 // A block: BN x BM outputs, A side by B side, over K steps of 64 through a ring of S
 // stages in LDS, filled by LDS-DMA copies; 8 waves of 32x32x16 MFMAs. An operand is
@@ -265,7 +293,12 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   static_assert(S >= 2 && (S - 1) * NI <= 63 && S * STAGE <= 160 * 1024, "ring");
   static_assert(S * STAGE == ring_bytes<BN, BM, NW, S>(), "the kernels' array");
 
-  const int nv = *p.nv;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // A few tokens need no launch to number them: each block does, and copies from X itself.
+  const bool direct = MODE == kSums && p.direct != 0;
+  const int nv = direct ? vocab_number(p, wid, lane, NW, smem) : *p.nv;
+  const int* const rowmap = reinterpret_cast<const int*>(smem);  // direct: token of a compact one
   const bool twice = nv <= p.twice;       // G in two parts of bf16
   const int rows = twice ? 2 * nv : nv;   // of G, and of X beside it
   const int64_t ext_b = MODE == kDW ? p.ids : (MODE == kDX ? rows : nv);
@@ -290,8 +323,6 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   const int ks0 = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * split / p.splits));
   const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * (split + 1) / p.splits)) - ks0;
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wid % WN, wm = wid / WN;
   const int lr = lane & 31, lg = lane >> 5;
   const int64_t a0 = (int64_t)ta * BN, b0 = (int64_t)tb * BM;
@@ -327,8 +358,19 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
 #pragma unroll
   for (int i = 0; i < NB; ++i)
     ob[i] = offset(TB, wid * NB + i, RB, BM, p.ldb, ext_b - b0) - 1024u * (uint32_t)(i % 4);
+  if constexpr (MODE == kSums) {
+    if (direct) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        int r, c;
+        rows_of(wid * NB + i, r, c);
+        const uint32_t o = r < BM && r < nv - b0 ? (uint32_t)(rowmap[b0 + r] * p.ldb * 2 + c * 16) : kBig;
+        ob[i] = o - 1024u * (uint32_t)(i % 4);
+      }
+    }
+  }
   const uint16_t* const pa = p.A + (TA ? a0 : a0 * p.lda);
-  const uint16_t* const pb = p.B + (TB ? b0 : b0 * p.ldb);
+  const uint16_t* const pb = p.B + (TB ? b0 : direct ? 0 : b0 * p.ldb);
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
   constexpr int NG = GA + GB;
   auto issue_group = [&](int g, int slot, int ks) {
@@ -426,8 +468,9 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       const int64_t c = b0 + wm * WTM + 32 * j + lr;
-      tok[j] = c < nv ? p.map[c] : -1;
+      tok[j] = c < nv ? (direct ? rowmap[c] : p.map[c]) : -1;
     }
+    if (direct) __syncthreads();  // the map's place is the ring's
   }
 
 #pragma unroll
@@ -502,7 +545,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     if (tok[j] < 0) return;
     const int64_t base = (int64_t)tok[j] * p.L;
     for (int e = ent[j]; e < p.L; ++e) {
-      const int key = p.keys[base + e];
+      const int key = direct && p.target ? (int)p.target[base] : p.keys[base + e];
       if (key == kNone || key >= id_lo + own) break;
       const int d = (int)(key - id_lo);
       if (d < 0) continue;  // a list of one entry is not searched
@@ -686,17 +729,34 @@ __global__ __launch_bounds__(512, 1) void vocab_grads_kernel(const VocabTile x, 
 
 // Sums of the tiles' parts, a wave a compact token: lse, and sum_j p (log p - (z_j - lse))
 // (with wts) or z - lse. Float64, fixed order.
-__global__ __launch_bounds__(256) void vocab_finish_kernel(const float2* __restrict__ part, int64_t ldpart,
-                                                           int tiles, const int* __restrict__ nv,
-                                                           const int* __restrict__ map,
-                                                           const int* __restrict__ keys,
-                                                           const float* __restrict__ wts,
-                                                           const float* __restrict__ zl, int L,
-                                                           float* __restrict__ value, float* __restrict__ lse) {
-  const int lane = threadIdx.x & 63;
-  const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (c >= *nv) return;
-  const int64_t t = map[c];
+__global__ __launch_bounds__(256) void vocab_finish_kernel(const VocabTile p, float* __restrict__ value,
+                                                           float* __restrict__ lse) {
+  const float2* __restrict__ const part = p.part;
+  const float* __restrict__ const wts = p.wts;
+  const float* __restrict__ const zl = p.zl;
+  const int* __restrict__ const keys = p.keys;
+  const int tiles = p.tiles_a, L = p.L, lane = threadIdx.x & 63;
+  const int64_t ldpart = p.ldpart;
+  int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), t = c;
+  if (p.direct) {  // a wave a token, which counts those before its own
+    if (t >= p.direct) return;
+    c = 0;
+    bool mine = false;
+    for (int i = lane; i <= t; i += 64) {
+      const bool live = vocab_live(p.target, p.keys, L, p.N, i);
+      c += live && i < t;
+      mine |= live && i == t;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) c += __shfl_xor((int)c, o, 64);
+    if (!__any(mine)) {
+      if (lane == 0) value[t] = lse[t] = 0.0f;
+      return;
+    }
+  } else {
+    if (c >= *p.nv) return;
+    t = p.map[c];
+  }
   float m = -INFINITY;
   double s = 0.0;
   constexpr int U = 8;
@@ -926,7 +986,7 @@ T* at(void* ws, size_t off) {
 }
 
 // Lists, compact tokens and their rows.
-hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, hipStream_t st) {
+hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, bool direct, hipStream_t st) {
   if (p.index) {
     const dim3 grid((unsigned)ceil_div(p.M, 4));
     const size_t lds = (size_t)p.L * 4 * sizeof(int);
@@ -939,6 +999,7 @@ hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, hipStream_t st
                          p.M, p.N, (int)p.L, p.scale, at<int>(ws, w.keys), at<float>(ws, w.wts),
                          at<float>(ws, w.mass));
   }
+  if (direct) return hipGetLastError();
   VocabCompact c = {};
   c.target = p.index ? nullptr : p.target;
   c.keys = at<int>(ws, w.keys);
@@ -987,23 +1048,27 @@ size_t vocab_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bo
 
 hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
   const Layout w = layout(p.M, p.N, p.K, p.L, p.index != nullptr, false);
-  hipError_t e = prepare(p, w, ws, st);
+  const bool direct = p.M <= kVocabDirect;
+  hipError_t e = prepare(p, w, ws, direct, st);
   if (e != hipSuccess) return e;
+  const LogitTile& tile = logit_tile(p.M, p.N, p.K);
   VocabTile t = common(p, w, ws);
   t.A = p.W;
   t.lda = p.ldw;
-  t.B = at<uint16_t>(ws, w.xc);
-  t.ldb = p.K;
+  t.direct = direct ? (int)p.M : 0;
+  t.target = p.index ? nullptr : p.target;
+  t.N = p.N;
+  t.B = direct ? p.X : at<uint16_t>(ws, w.xc);
+  t.ldb = direct ? p.ldx : p.K;
   t.ext_a = t.ids = p.N;
   t.part = at<float2>(ws, w.part);
   t.ldpart = p.M;
   t.zl = at<float>(ws, w.zl);
-  const LogitTile& tile = logit_tile(p.M, p.N, p.K);
   t.stream = p.M <= tile.bm;
   e = launch_logits<kSums>(t, tile, p.M, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(vocab_finish_kernel, dim3((unsigned)ceil_div(p.M, 4)), dim3(256), 0, st, t.part, t.ldpart,
-                     (int)ceil_div(p.N, tile.bn), t.nv, t.map, t.keys, t.wts, t.zl, t.L, p.value, p.lse_out);
+  t.tiles_a = (int)ceil_div(p.N, tile.bn);
+  hipLaunchKernelGGL(vocab_finish_kernel, dim3((unsigned)ceil_div(p.M, 4)), dim3(256), 0, st, t, p.value, p.lse_out);
   return hipGetLastError();
 }
 
@@ -1013,7 +1078,7 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     return hipGetLastError();
   }
   const Layout w = layout(p.M, p.N, p.K, p.L, p.index != nullptr, true);
-  hipError_t e = prepare(p, w, ws, st);
+  hipError_t e = prepare(p, w, ws, false, st);
   if (e != hipSuccess) return e;
   uint16_t* G = at<uint16_t>(ws, w.g);
   const int64_t rows = grad_rows(p.M);
