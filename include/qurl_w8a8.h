@@ -256,7 +256,8 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  * qr_vocab_logp -- softmax cross entropy (its negative): logp[t] = z[t, target[t]] - lse[t].
  *   A target outside [0, N) masks its token: logp and lse are 0 there.
  * qr_vocab_logp_grad -- with g = dlogp:
- *   G[t,v]  = scale g[t] ([v = target[t]] - exp(z[t,v] - lse[t])), rounded to bf16
+ *   G[t,v]  = scale g[t] ([v = target[t]] - exp(z[t,v] - lse[t])), in two parts of bf16 (to
+ *             2^-16) where at most 128 tokens are not masked, else rounded to bf16
  *   dX[t,:] = bf16_rne(sum_v G[t,v] W[v,:]),  dW[v,:] = bf16_rne(sum_t G[t,v] X[t,:])
  *   (fp32 sums). Masked tokens: a zero row of dX, no part in dW, whatever X, lse and
  *   g hold there.
@@ -272,14 +273,15 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  *   The same id twice counts as two entries. All entries at -inf: every p is 0.
  * qr_vocab_distill_grad -- with g = dloss and P[t] = sum_j p[t,j]:
  *   G[t,v]  = scale g[t] (P[t] exp(z[t,v] - lse[t]) - sum_j p[t,j] [v = index[t,j]]),
- *   rounded to bf16, and dX, dW from it as above.
+ *   and dX, dW from it as above.
  *
  * All results are the same bits on every run.
  *
  *   X        [M, ldx] bf16 hidden states, W [N, ldw] bf16 head (read); rows on 16-byte
  *            boundaries, strides at most 2^21. M and N at most 2^22, N >= 1, K a multiple
  *            of 8 in [8, 65536].
- *   scale    finite, > 0: the logits' scale, 1 / temperature.
+ *   scale    finite, > 0: the logits' scale, 1 / temperature (scaled logits stay in fp32's
+ *            range; scaled teacher logits below it count as -inf).
  *   target   [M] int64;  index [M, L] int64, 1 <= L <= 1024;  teacher [M, L] fp32
  *            (teacher_bf16 = 0) or bf16 (1);  teacher_lse NULL or [M] fp32 (read).
  *   logp, loss, lse  [M] fp32 (written). The gradients read the lse of their forward call.
@@ -651,6 +653,15 @@ int qr_gemm_plan(int64_t M, int64_t N, int64_t K, int qt, int* tile, int* splitk
  */
 int qr_mxfp4_plan(int64_t M, int64_t N, int64_t K, int xfmt, int* tile_n, int* tile_m, int* splits,
                   int* ahead);
+
+/*
+ * qr_vocab_plan -- the same for the losses over a vocabulary, M >= 1 tokens:
+ *   *tile_ids, *tile_tokens  ids and tokens of a tile of the logits,
+ *   *dx_rows  rows of a tile of dX (tokens, or up to 128 of them in two parts),
+ *   *piece    ids that a gradient's workspace holds at once.
+ * Pure host function; returns QR_OK or the calls' error for the shape.
+ */
+int qr_vocab_plan(int64_t M, int64_t N, int64_t K, int* tile_ids, int* tile_tokens, int* dx_rows, int64_t* piece);
 
 /* Name of tile configuration `tile` (static string) or NULL if out of range. */
 const char* qr_tile_name(int tile);

@@ -29,6 +29,7 @@ from w8a8_gemm_rl_amd import binding as B
 from w8a8_gemm_rl_amd import inputs as I
 
 from gpu_helpers import DEV
+from vocab_shapes import LARGE, SMALL
 
 pytestmark = pytest.mark.gpu
 
@@ -174,22 +175,70 @@ def _both(d, need_dX=True, need_dW=True, seed=5):
     return value, lse, g, dX, dW
 
 
-# tokens around the tiles' 32, 64, 128 and 256, ids around 256 (and below a wave's 32), K around the
-# copies' 64 and with ends inside them
-SIZES = [(1, 1, 8), (1, 256, 64), (2, 7, 16), (31, 255, 56), (32, 257, 72), (33, 300, 128), (64, 1000, 136),
-         (65, 511, 64), (100, 700, 200), (128, 256, 264), (129, 513, 72), (200, 33, 8), (256, 512, 128),
-         (257, 769, 136), (300, 1031, 520), (513, 300, 64)]
-
-
-@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("M,N,K", SMALL)
 def test_logp_sizes(M, N, K):
     _both(_inputs(M, N, K, seed=M + N + K, pad=8 * (M % 3)))
 
 
-@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("M,N,K", SMALL)
 @pytest.mark.parametrize("L,dtype,own_sum", [(1, "fp32", False), (5, "bf16", True), (70, "fp32", False)])
 def test_distill_sizes(M, N, K, L, dtype, own_sum):
     _both(_inputs(M, N, K, L=L, seed=M + N + K + L, dtype=dtype, own_sum=own_sum, scale=0.7, pad=8 * (N % 2)))
+
+
+def _check_large(X, W, got, lse, grads, g, ids, p, live, sign, e_p):
+    """The bounds of the module's head, in float64 on the device. ids [M, L], p [M, L], `got` the
+    losses' values; zeros where not live."""
+    M, K = X.shape
+    N = W.shape[0]
+    x, w = X.double() * live[:, None], W.double()
+    z = x @ w.T
+    l64 = torch.logsumexp(z, 1)
+    e = (x.abs() @ w.abs().T).amax(1) * (2 * K + 2) * U + (4 * z.abs().amax(1) + 5 * l64.abs() + 616) * U
+    assert torch.all(((lse.double() - l64).abs() <= e)[live]) and not bool(lse[~live].any())
+    zi = torch.gather(z, 1, ids.clamp(0, N - 1)) - l64[:, None]
+    lp = torch.where(p > 0, p, 1.0).log()
+    want = (p * (lp - zi)).sum(1) if sign > 0 else zi[:, 0]
+    lim = (p * (2 * e[:, None] + (lp.abs() + zi.abs() + 1) * (e_p + 8 * U))).sum(1) + want.abs() * U
+    assert torch.all(((got.double() - want).abs() <= lim)[live]) and not bool(got[~live].any())
+    a = (g.double() * live * sign)[:, None]
+    q = p.sum(1, keepdim=True) * torch.exp(z - lse.double()[:, None])
+    t = torch.zeros_like(q).scatter_add_(1, ids.clamp(0, N - 1), p)
+    G, mag = (q - t) * a, (q + t) * a.abs()
+    eG = HALF * G.abs() + mag * (e[:, None] + e_p + 24 * U) * (1 + HALF) + (a.abs() + 1) * 2.0 ** -126
+    for out, want, bound, big, n in ((grads[0], G @ w, eG @ w.abs(), G.abs() @ w.abs(), N),
+                                     (grads[1], G.T @ x, eG.T @ x.abs(), G.abs().T @ x.abs(), M)):
+        lim = bound + (big + bound) * (2 * n + 2) * U
+        assert torch.all((out.double() - want).abs() <= lim + HALF * (want.abs() + lim) + TINY)
+    assert not bool(grads[0][~live].any())
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_sizes(M, N, K):
+    r = torch.Generator().manual_seed(M + N + K)
+    X = torch.randn((M, K), generator=r).to(torch.bfloat16).to(DEV)
+    W = (torch.randn((N, K), generator=r) * (1.5 / K ** 0.5)).to(torch.bfloat16).to(DEV)
+    live = (torch.rand(M, generator=r) < 0.9).to(DEV)
+    live[M // 2] = True
+    g = torch.randn(M, generator=r).to(DEV)
+    target = torch.randint(0, N, (M,), generator=r).to(DEV)
+    target[~live] = -1
+    logp, lse = B.vocab_logp(X, W, target)
+    grads = B.vocab_logp_grad(X, W, target, lse, g)
+    _check_large(X, W, logp, lse, grads, g, target[:, None], live[:, None].double(), live, -1.0, 0.0)
+    L = 12
+    index = torch.randint(0, N, (M, L), generator=r).to(DEV)
+    index[:, 3] = N - 1 - torch.arange(M, device=DEV) % 3
+    index[torch.rand((M, L), generator=r).to(DEV) < 0.2] = N
+    index[:, 0] = 0
+    index[~live] = -1
+    teacher = (torch.randn((M, L), generator=r) * 2).to(DEV)
+    loss, lse = B.vocab_distill(X, W, index, teacher)
+    grads = B.vocab_distill_grad(X, W, index, teacher, lse, g)
+    ok = (index >= 0) & (index < N)
+    p = torch.softmax(teacher.double().masked_fill(~ok, -1e9), 1) * ok
+    e_p = 2 * (6 * float(teacher.abs().max()) + L + 10) * U
+    _check_large(X, W, loss, lse, grads, g, index, p, live, 1.0, e_p)
 
 
 @pytest.mark.parametrize("L", [0, 6])
@@ -388,6 +437,64 @@ def test_offsets_past_32_bits():
     want = -(g.double() * torch.exp(-lse.double())) @ X.double()
     mag = (g.double().abs() * torch.exp(-lse.double())) @ X.double().abs()
     assert torch.all((rest.double() - want).abs() <= mag * (HALF + 2 * float(e.max()) + 20 * U) + HALF * want.abs())
+
+
+def test_more_tiles_than_one_launch_takes():
+    """2^20 tokens of 2^18 + 77 ids: 2^22 tiles and more, several launches of the logits, lists at their
+    borders. X and W repeat a few rows, so float64 needs each pair once."""
+    M, N, K, nx, nw = 1 << 20, (1 << 18) + 77, 8, 16, 61
+    r = torch.Generator().manual_seed(9)
+    xs = torch.randn((nx, K), generator=r).to(torch.bfloat16).to(DEV)
+    wr = torch.randn((nw, K), generator=r).to(torch.bfloat16).to(DEV)
+    X, W = xs[torch.arange(M, device=DEV) % nx], wr[torch.arange(N, device=DEV) % nw]
+    per = (1 << 21) // (M // 256) * 256  # ids of a launch
+    edges = torch.tensor([0, per - 1, per, 2 * per - 1, 2 * per, N - 1, N, -1], device=DEV)
+    target = edges[(torch.arange(M, device=DEV) // nx) % len(edges)]
+    logp, lse = B.vocab_logp(X, W, target)
+    z = xs.double() @ wr.double().T
+    count = torch.bincount(torch.arange(N, device=DEV) % nw, minlength=nw).double()
+    l64 = torch.log((torch.exp(z) * count).sum(1))
+    live = (target >= 0) & (target < N)
+    zmax = z.abs().amax(1)
+    e = (xs.double().abs() @ wr.double().abs().T).amax(1) * (2 * K + 2) * U + (4 * zmax + 616 + l64.abs()) * U
+    which = torch.arange(M, device=DEV) % nx
+    assert torch.all(((lse.double() - l64[which]).abs() <= e[which])[live]) and not bool(lse[~live].any())
+    want = z[which, target.clamp(0, N - 1) % nw] - l64[which]
+    assert torch.all(((logp.double() - want).abs() <= 2 * e[which] + want.abs() * U)[live])
+    assert not bool(logp[~live].any())
+
+
+def test_gradient_past_32_bits_of_tokens():
+    """700000 tokens: a piece's G (4096 ids each) is 5.7 GB, its last rows lie past 2^31 elements; some
+    live tokens at the end, the others masked or of no gradient."""
+    M, N, K = 700_000, 5000, 16
+    r = torch.Generator().manual_seed(2)
+    X = torch.randn((M, K), generator=r).to(torch.bfloat16).to(DEV)
+    W = (torch.randn((N, K), generator=r) * 0.5).to(torch.bfloat16).to(DEV)
+    target = torch.randint(0, N, (M,), generator=r).to(DEV)
+    g = torch.zeros(M, device=DEV)
+    rows = torch.tensor([0, 5, 349_999, 524_288, M - 3, M - 2, M - 1], device=DEV)
+    g[rows] = torch.randn(len(rows), generator=r).to(DEV)
+    logp, lse = B.vocab_logp(X, W, target)
+    dX, dW = B.vocab_logp_grad(X, W, target, lse, g)
+    x, w = X[rows].double(), W.double()
+    z = x @ w.T
+    G = -torch.exp(z - lse[rows].double()[:, None])
+    G[torch.arange(len(rows), device=DEV), target[rows]] += 1.0
+    G *= g[rows].double()[:, None]
+    e = (x.abs() @ w.abs().T).amax(1) * (2 * K + 2) * U + (8 * z.abs().amax(1) + 616) * U
+    eG = HALF * G.abs() + (G.abs() + g[rows].double().abs()[:, None] * torch.exp(z - lse[rows].double()[:, None])) \
+        * (e[:, None] + 16 * U) * 2
+    lim = eG @ w.abs() + (G.abs() @ w.abs()) * (2 * N + 2) * U
+    want = G @ w
+    assert torch.all((dX[rows].double() - want).abs() <= lim + HALF * (want.abs() + lim) + TINY)
+    keep = torch.ones(M, dtype=torch.bool, device=DEV)
+    keep[rows] = False
+    assert not bool(dX[keep].any())
+    # dW: M terms of which all but seven are zero (no rounding)
+    lim = eG.T @ x.abs() + (G.abs().T @ x.abs()) * 20 * U
+    want = G.T @ x
+    assert torch.all((dW.double() - want).abs() <= lim + HALF * (want.abs() + lim) + TINY)
 
 
 def test_given_outputs_and_strides():

@@ -167,3 +167,24 @@ def test_workspace_sizes(B):
     for fn in FN[2:]:
         with pytest.raises(B.QRError):
             B.workspace_size(fn, 4, 100, 64, 0)
+
+
+def test_plans(B):
+    """Every plan that a sweep of shapes meets is one that the GPU tests run."""
+    from vocab_shapes import LARGE, SMALL
+
+    run = {B.vocab_plan(*s)[:3] for s in SMALL + LARGE}
+    # the gradient's pieces have plans of their own, of fewer ids
+    r = RNG(7)
+    met = set()
+    for _ in range(20000):
+        M, N, K = (int(round(2 ** r.uniform(0, hi))) for hi in (14, 18, 13))
+        K = max(8, K // 8 * 8)
+        ids, tokens, rows, piece = B.vocab_plan(M, N, K)
+        assert piece <= N and (piece == N or piece % 256 == 0)
+        met.add((ids, tokens, rows))
+    assert {p[:2] for p in met} <= {p[:2] for p in run}
+    assert {p[2] for p in met} <= {p[2] for p in run}
+    for bad in ((0, 10, 64), (4, 0, 64), (4, 10, 12)):
+        with pytest.raises(B.QRError):
+            B.vocab_plan(*bad)

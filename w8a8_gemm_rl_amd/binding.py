@@ -37,7 +37,7 @@ EXPORTS = [
     "qr_set_small_m_override", "qr_set_fuse_override", "qr_last_error", "qr_version", "qr_probe_read", "qr_probe_mfma",
     "qr_probe_copy_stream", "qr_mxfp4_quantize", "qr_mx_dequantize", "qr_mxfp4_gemm", "qr_mxfp4_linear",
     "qr_block_norm_quant", "qr_silu_mul_mx", "qr_mxfp4_plan", "qr_vocab_logp", "qr_vocab_logp_grad",
-    "qr_vocab_distill", "qr_vocab_distill_grad",
+    "qr_vocab_distill", "qr_vocab_distill_grad", "qr_vocab_plan",
 ]
 
 
@@ -85,6 +85,7 @@ _SIGS = {
     "qr_gemm_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int), ctypes.POINTER(_int),
                             ctypes.POINTER(_int)]),
     "qr_mxfp4_plan": (_int, [_i64, _i64, _i64, _int] + 4 * [ctypes.POINTER(_int)]),
+    "qr_vocab_plan": (_int, [_i64, _i64, _i64] + 3 * [ctypes.POINTER(_int)] + [ctypes.POINTER(_i64)]),
     "qr_tile_name": (ctypes.c_char_p, [_int]),
     "qr_num_tiles": (_int, []),
     "qr_set_plan_override": (_int, [_int, _int, _int]),
@@ -845,6 +846,14 @@ def _grads(X, W, need_dX, need_dW, dX, dW):
     if out[0] is None and out[2] is None:
         raise ValueError("neither dX nor dW asked for")
     return out
+
+
+def vocab_plan(M, N, K):
+    """(ids and tokens of a tile of the logits, rows of a tile of dX, ids of a gradient's piece) of the
+    plan that the calls use for M >= 1 tokens, N ids and K hidden values."""
+    a, b, c, d = ctypes.c_int(), ctypes.c_int(), ctypes.c_int(), ctypes.c_int64()
+    _check("qr_vocab_plan", lib().qr_vocab_plan(M, N, K, *(ctypes.byref(v) for v in (a, b, c, d))))
+    return a.value, b.value, c.value, d.value
 
 
 def vocab_logp(X, W, target, scale=1.0, logp=None, lse=None, ws=None):

@@ -29,6 +29,7 @@ struct VocabArgs {
 size_t vocab_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad);
 // Workspace of an entry point by its name; (size_t)-1 for invalid sizes.
 size_t vocab_workspace(const char* fn, int64_t M, int64_t N, int64_t K, int64_t L);
+void vocab_plan(int64_t M, int64_t N, int64_t K, int* ids, int* tokens, int* rows, int64_t* piece);
 hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st);
 hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st);
 

@@ -187,4 +187,15 @@ int qr_vocab_distill_grad(const void* X, int64_t ldx, const void* W, int64_t ldw
   return st != QR_OK ? st : run_grad(fn, a, lse, dloss, dX, lddx, dW, lddw, workspace, ws_bytes, stream);
 }
 
+int qr_vocab_plan(int64_t M, int64_t N, int64_t K, int* tile_ids, int* tile_tokens, int* dx_rows, int64_t* piece) {
+  const char* fn = "qr_vocab_plan";
+  const int st = check_shape(fn, M, N, K);
+  if (st != QR_OK) return st;
+  if (M == 0) return qr::set_error(QR_ERR_INVALID_ARG, "%s: no tokens", fn);
+  if (!tile_ids || !tile_tokens || !dx_rows || !piece)
+    return qr::set_error(QR_ERR_INVALID_ARG, "%s: null output pointer", fn);
+  qr::vocab_plan(M, N, K, tile_ids, tile_tokens, dx_rows, piece);
+  return qr::hip_error(hipSuccess, fn);
+}
+
 }  // extern "C"

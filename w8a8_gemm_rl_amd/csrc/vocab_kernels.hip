@@ -373,7 +373,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   const uint16_t* const pb = p.B + (TB ? b0 : direct ? 0 : b0 * p.ldb);
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
   constexpr int NG = GA + GB;
-  auto issue_group = [&](int g, int slot, int ks) {
+  auto issue_group = [&](int g, int slot, int ks, bool inside) {
     const bool isA = g < GA, cols = isA ? TA : TB;
     const int i0 = (isA ? g : g - GA) * 4, n = isA ? NA : NB, cnt = n - i0 < 4 ? n - i0 : 4;
     const int I0 = wid * n + i0;
@@ -389,7 +389,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       vo[e] = isA ? oa[i < NA ? i : 0] : ob[i < NB ? i : 0];
     }
     const int64_t left = klen - (int64_t)ks * KS;
-    if (left < KS) {  // the last stage: K ends inside it
+    if (!inside && left < KS) {  // the last stage: K ends inside it
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         int a, c;
@@ -463,28 +463,39 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   // Compact tokens of the lane, and where their lists enter the wave's ids.
   const int64_t id_lo = p.id0 + a0 + wn * WTN;
   const int own = (int)(p.ids - a0 - wn * WTN < WTN ? p.ids - a0 - wn * WTN : WTN);  // ids of the wave
-  int tok[FM], ent[FM];
+  int tok[FM], ent[FM];  // ent: the one entry's id, or of a longer list the first that may be here
+  float gt[FM], l2[FM], ga[FM];
   if constexpr (MODE == kSums || MODE == kGrad) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       const int64_t c = b0 + wm * WTM + 32 * j + lr;
       tok[j] = c < nv ? (direct ? rowmap[c] : p.map[c]) : -1;
+      ent[j] = kNone;
+      gt[j] = l2[j] = ga[j] = 0.0f;
+      if (tok[j] >= 0) {
+        if (p.L == 1) ent[j] = direct && p.target ? (int)p.target[tok[j]] : p.keys[tok[j]];
+        if constexpr (MODE == kGrad) {
+          gt[j] = p.g[tok[j]] * p.scale * p.sign;
+          ga[j] = p.mass ? gt[j] * p.mass[tok[j]] : gt[j];
+          l2[j] = p.lse[tok[j]] * kLog2e;
+        }
+      }
     }
     if (direct) __syncthreads();  // the map's place is the ring's
   }
-
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (s < nk) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) issue_group(g, s, ks0 + s);
+      for (int g = 0; g < NG; ++g) issue_group(g, s, ks0 + s, false);
     }
 
   if constexpr (MODE == kSums || MODE == kGrad) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
+      if (p.L == 1) continue;
       int lo = 0;
-      if (p.L > 1 && tok[j] >= 0) {  // first entry whose id is not below id_lo
+      if (tok[j] >= 0) {  // first entry whose id is not below id_lo
         const int* key = p.keys + (int64_t)tok[j] * p.L;
         int hi = p.L;
         while (lo < hi) {
@@ -513,7 +524,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!decltype(last)::value) {
-      if constexpr (decltype(refill)::value) wait_vm<(S - 2) * NI>();
+      if constexpr (decltype(refill)::value != 0) wait_vm<(S - 2) * NI>();
       else wait_stages<NI, S - 2>(nk - 2 - it);
       __syncthreads();
       load_ops(smem + ns * STAGE, 0, 0);
@@ -522,9 +533,9 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
 #pragma unroll
     for (int i = 0; i < (FN > NG ? FN : NG); ++i) {
       if (i < FN) multiply_row(1, i);
-      if constexpr (decltype(refill)::value) {
+      if constexpr (decltype(refill)::value != 0) {
         __builtin_amdgcn_sched_barrier(0);
-        if (i < NG) issue_group(i, cs, ks0 + it + S);
+        if (i < NG) issue_group(i, cs, ks0 + it + S, decltype(refill)::value == 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -535,21 +546,29 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     wait_stages<NI, S - 1>(nk - 1);
     __syncthreads();
     load_ops(smem, 0, 0);
-    for (; it < nk - S; ++it) stage(std::true_type{}, std::false_type{});
-    for (; it < nk - 1; ++it) stage(std::false_type{}, std::false_type{});
-    stage(std::false_type{}, std::true_type{});
+    // refills: 1 of a whole stage, 2 of one that K may end in, 0 none
+    for (; it < nk - S - 1; ++it) stage(std::integral_constant<int, 1>{}, std::false_type{});
+    for (; it < nk - S; ++it) stage(std::integral_constant<int, 2>{}, std::false_type{});
+    for (; it < nk - 1; ++it) stage(std::integral_constant<int, 0>{}, std::false_type{});
+    stage(std::integral_constant<int, 0>{}, std::true_type{});
   }
 
   // Entries of the lists among the wave's ids: f(fragment j, entry, offset from id_lo).
+  auto hit = [&](int64_t e, int key, auto f) {
+    const int d = (int)(key - id_lo);
+    if (((d >> 2) & 1) == lg) f(e, (d >> 5) * 16 + ((d >> 3) & 3) * 4 + (d & 3));
+  };
   auto hits = [&](int j, auto f) {
+    if (p.L == 1) {
+      if (ent[j] >= id_lo && ent[j] < id_lo + own) hit(tok[j], ent[j], f);
+      return;
+    }
     if (tok[j] < 0) return;
     const int64_t base = (int64_t)tok[j] * p.L;
     for (int e = ent[j]; e < p.L; ++e) {
-      const int key = direct && p.target ? (int)p.target[base] : p.keys[base + e];
+      const int key = p.keys[base + e];
       if (key == kNone || key >= id_lo + own) break;
-      const int d = (int)(key - id_lo);
-      if (d < 0) continue;  // a list of one entry is not searched
-      if (((d >> 2) & 1) == lg) f(base + e, (d >> 5) * 16 + ((d >> 3) & 3) * 4 + (d & 3));
+      hit(base + e, key, f);
     }
   };
   const float c2 = p.scale * kLog2e;
@@ -569,13 +588,17 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
         p.zl[e] = v * p.scale;
       });
       float m = -INFINITY, s = 0.0f;
+      if (own < WTN) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= own) acc[i][j][r] = -INFINITY;
+      }
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if (32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= own) acc[i][j][r] = -INFINITY;
-          m = fmaxf(m, acc[i][j][r]);
-        }
+        for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
       m = fmaxf(m, __shfl_xor(m, 32, 64));
       m = m == -INFINITY ? m : m * c2;
       const float sub = m == -INFINITY ? 0.0f : m;
@@ -606,21 +629,20 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     // each element); beyond, rounded once (2^-8, as much as the results' own rounding).
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      float a = 0.0f, l2 = 0.0f, gt = 0.0f;
-      if (tok[j] >= 0) {
-        gt = p.g[tok[j]] * p.scale * p.sign;
-        a = p.mass ? gt * p.mass[tok[j]] : gt;
-        l2 = p.lse[tok[j]] * kLog2e;
-      }
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float v = a * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -l2));
-          acc[i][j][r] = 32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) < own ? v : 0.0f;
-        }
+        for (int r = 0; r < 16; ++r)
+          acc[i][j][r] = ga[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -l2[j]));
+      if (own < WTN) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= own) acc[i][j][r] = 0.0f;
+      }
       hits(j, [&](int64_t e, int reg) {
-        const float b = p.wts ? gt * p.wts[e] : gt;
+        const float b = p.wts ? gt[j] * p.wts[e] : gt[j];
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -840,6 +862,7 @@ __global__ __launch_bounds__(256) void vocab_zero_kernel(uint16_t* __restrict__ 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+constexpr int64_t kMaxBlocks = (int64_t)1 << 21;
 constexpr int64_t kMall = (int64_t)256 << 20;
 
 // Up to so many tokens that count G is held in two parts of bf16.
@@ -1046,6 +1069,15 @@ size_t vocab_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bo
   return M == 0 ? 0 : layout(M, N, K, L, lists, grad).bytes;
 }
 
+void vocab_plan(int64_t M, int64_t N, int64_t K, int* ids, int* tokens, int* rows, int64_t* piece) {
+  const Layout w = layout(M, N, K, 1, false, true);
+  const LogitTile& t = logit_tile(M, N, K);
+  *ids = t.bn;
+  *tokens = t.bm;
+  *rows = dx_tile(grad_rows(M));
+  *piece = w.piece < N ? w.piece : N;
+}
+
 hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
   const Layout w = layout(p.M, p.N, p.K, p.L, p.index != nullptr, false);
   const bool direct = p.M <= kVocabDirect;
@@ -1053,20 +1085,26 @@ hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
   if (e != hipSuccess) return e;
   const LogitTile& tile = logit_tile(p.M, p.N, p.K);
   VocabTile t = common(p, w, ws);
-  t.A = p.W;
   t.lda = p.ldw;
   t.direct = direct ? (int)p.M : 0;
   t.target = p.index ? nullptr : p.target;
   t.N = p.N;
   t.B = direct ? p.X : at<uint16_t>(ws, w.xc);
   t.ldb = direct ? p.ldx : p.K;
-  t.ext_a = t.ids = p.N;
-  t.part = at<float2>(ws, w.part);
   t.ldpart = p.M;
   t.zl = at<float>(ws, w.zl);
   t.stream = p.M <= tile.bm;
-  e = launch_logits<kSums>(t, tile, p.M, st);
-  if (e != hipSuccess) return e;
+  float2* const part = at<float2>(ws, w.part);
+  // a launch's blocks times their threads stay in 32 bits
+  const int64_t ids = kMaxBlocks / ceil_div(p.M, tile.bm) * tile.bn;
+  for (int64_t id0 = 0; id0 < p.N; id0 += ids) {
+    t.id0 = id0;
+    t.A = p.W + id0 * p.ldw;
+    t.ext_a = t.ids = p.N - id0 < ids ? p.N - id0 : ids;
+    t.part = part + id0 / tile.bn * t.ldpart;
+    if ((e = launch_logits<kSums>(t, tile, p.M, st)) != hipSuccess) return e;
+  }
+  t.part = part;
   t.tiles_a = (int)ceil_div(p.N, tile.bn);
   hipLaunchKernelGGL(vocab_finish_kernel, dim3((unsigned)ceil_div(p.M, 4)), dim3(256), 0, st, t, p.value, p.lse_out);
   return hipGetLastError();
