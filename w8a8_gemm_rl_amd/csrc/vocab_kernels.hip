@@ -12,6 +12,7 @@
 // Four products share one kernel (vocab_tile_kernel): the logits' softmax sums; the same
 // logits again with G as output, a piece of the vocabulary at a time; that piece's part
 // of dX and its rows of dW.
+#include <cmath>
 #include <type_traits>
 
 #include "qr_copy.h"
@@ -38,16 +39,19 @@ constexpr int kNone = 0x7fffffff;  // list key of no entry: past every id
 // One wave per token: weights p of the list's entries and the entries in the order of
 // their ids (entries of one id in the order of the list, ids outside [0, N) last).
 // p = softmax over the entries, or exp(c s - teacher_lse). L <= kVocabMaxList; ranks by
-// counting in LDS, which is little beside the products.
+// counting in LDS, which is little beside the products. first[b] is the first entry whose id is
+// not below b << shift, where a tile's waves begin to look for their entries.
 template <bool BF16>
 __global__ __launch_bounds__(256) void vocab_list_kernel(const int64_t* __restrict__ index,
                                                          const void* __restrict__ teacher,
                                                          const float* __restrict__ teacher_lse, int64_t M,
                                                          int64_t N, int L, float scale, int* __restrict__ keys,
-                                                         float* __restrict__ wts, float* __restrict__ mass) {
+                                                         float* __restrict__ wts, float* __restrict__ mass,
+                                                         uint16_t* __restrict__ first, int buckets, int shift) {
   extern __shared__ __attribute__((aligned(16))) uint8_t list_smem[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int* key = reinterpret_cast<int*>(list_smem) + wave * L;
+  int* key = reinterpret_cast<int*>(list_smem) + wave * 2 * L;
+  int* sorted = key + L;
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   if (t >= M) return;
   const int64_t* ids = index + t * L;
@@ -79,10 +83,18 @@ __global__ __launch_bounds__(256) void vocab_list_kernel(const int64_t* __restri
     const int k = key[j];
     int rank = 0;
     for (int i = 0; i < L; ++i) rank += (key[i] < k || (key[i] == k && i < j)) ? 1 : 0;
+    sorted[rank] = k;
     keys[t * L + rank] = k;
     wts[t * L + rank] = k == kNone ? 0.0f : expf(logit(j) - norm) / div;
   }
   if (lane == 0) mass[t] = sum / div;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int r = lane; r <= L; r += 64) {  // buckets behind entry r - 1's, up to entry r's
+    int b = 0, end = buckets;
+    if (r > 0) b = sorted[r - 1] == kNone ? buckets : (sorted[r - 1] >> shift) + 1;
+    if (r < L && sorted[r] != kNone) end = (sorted[r] >> shift) + 1;
+    for (; b < end; ++b) first[t * buckets + b] = (uint16_t)r;
+  }
 }
 
 // Whether token t has a list (key 0 of its L), or, with `target`, an id in [0, N).
@@ -214,8 +226,9 @@ struct VocabTile {
   const int* keys;
   const float *wts, *mass, *lse, *g;
   int L;
-  float scale;     // c; negative for the gradient of a log-probability's negative part
-  float sign;
+  const uint16_t* first;  // [M][buckets], L > 1
+  int buckets, shift;
+  float scale, sign;  // G = sign * ...: -1 for a log-probability
   float2* part;    // kSums: [tiles_a][ldpart]
   int64_t ldpart;
   float* zl;       // kSums: logits of the lists' ids
@@ -463,7 +476,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   // Compact tokens of the lane, and where their lists enter the wave's ids.
   const int64_t id_lo = p.id0 + a0 + wn * WTN;
   const int own = (int)(p.ids - a0 - wn * WTN < WTN ? p.ids - a0 - wn * WTN : WTN);  // ids of the wave
-  int tok[FM], ent[FM];  // ent: the one entry's id, or of a longer list the first that may be here
+  int tok[FM], ent[FM];  // ent: a list's one id, or its first entry that may be the wave's
   float gt[FM], l2[FM], ga[FM];
   if constexpr (MODE == kSums || MODE == kGrad) {
 #pragma unroll
@@ -491,20 +504,11 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     }
 
   if constexpr (MODE == kSums || MODE == kGrad) {
+    if (p.L > 1) {
+      const int64_t bucket = id_lo >> p.shift;
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      if (p.L == 1) continue;
-      int lo = 0;
-      if (tok[j] >= 0) {  // first entry whose id is not below id_lo
-        const int* key = p.keys + (int64_t)tok[j] * p.L;
-        int hi = p.L;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (key[mid] < id_lo) lo = mid + 1;
-          else hi = mid;
-        }
-      }
-      ent[j] = lo;
+      for (int j = 0; j < FM; ++j)
+        if (tok[j] >= 0 && own > 0) ent[j] = p.first[(int64_t)tok[j] * p.buckets + bucket];
     }
   }
 
@@ -553,22 +557,33 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     stage(std::integral_constant<int, 0>{}, std::true_type{});
   }
 
-  // Entries of the lists among the wave's ids: f(fragment j, entry, offset from id_lo).
-  auto hit = [&](int64_t e, int key, auto f) {
+  // Entries of the lists among the wave's ids: f(entry, its weight, register of its id).
+  auto hit = [&](int64_t e, int key, float w, auto f) {
     const int d = (int)(key - id_lo);
-    if (((d >> 2) & 1) == lg) f(e, (d >> 5) * 16 + ((d >> 3) & 3) * 4 + (d & 3));
+    if (((d >> 2) & 1) == lg) f(e, w, (d >> 5) * 16 + ((d >> 3) & 3) * 4 + (d & 3));
   };
   auto hits = [&](int j, auto f) {
+    if (tok[j] < 0 || own <= 0) return;
     if (p.L == 1) {
-      if (ent[j] >= id_lo && ent[j] < id_lo + own) hit(tok[j], ent[j], f);
+      const float w = MODE == kGrad && p.wts ? p.wts[tok[j]] : 1.0f;
+      if (ent[j] >= id_lo && ent[j] < id_lo + own) hit(tok[j], ent[j], w, f);
       return;
     }
-    if (tok[j] < 0) return;
     const int64_t base = (int64_t)tok[j] * p.L;
-    for (int e = ent[j]; e < p.L; ++e) {
-      const int key = p.keys[base + e];
-      if (key == kNone || key >= id_lo + own) break;
-      hit(base + e, key, f);
+    constexpr int U = 4;  // entries read at once: lists are dense where ids are frequent ones
+    for (int e = ent[j]; e < p.L; e += U) {
+      int key[U];
+      float w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = e + u < p.L ? e + u : p.L - 1;
+        key[u] = e + u < p.L ? p.keys[base + i] : kNone;
+        w[u] = MODE == kGrad ? p.wts[base + i] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (key[u] >= id_lo && key[u] < id_lo + own) hit(base + e + u, key[u], w[u], f);
+      if (key[U - 1] >= id_lo + own) break;
     }
   };
   const float c2 = p.scale * kLog2e;
@@ -579,7 +594,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     float2* red = reinterpret_cast<float2*>(smem);  // [WN][BM]
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      hits(j, [&](int64_t e, int reg) {
+      hits(j, [&](int64_t e, float, int reg) {
         float v = 0.0f;
 #pragma unroll
         for (int i = 0; i < FN; ++i)
@@ -641,8 +656,8 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
           for (int r = 0; r < 16; ++r)
             if (32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= own) acc[i][j][r] = 0.0f;
       }
-      hits(j, [&](int64_t e, int reg) {
-        const float b = p.wts ? gt[j] * p.wts[e] : gt[j];
+      hits(j, [&](int64_t, float w, int reg) {
+        const float b = gt[j] * w;
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -959,7 +974,8 @@ hipError_t launch_both(const VocabTile& x, const VocabTile& w, int64_t rows, hip
 }
 
 struct Layout {
-  size_t nv, map, inv, keys, wts, mass, zl, xc, part, g, dx, bytes;
+  size_t nv, map, inv, keys, wts, mass, first, zl, xc, part, g, dx, bytes;
+  int buckets, shift;  // of ids, for lists
   int64_t piece;  // ids of a piece of the gradient
   int splits;     // parts of a piece's ids whose sums of dX are kept apart
 };
@@ -979,6 +995,11 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad)
   if (lists) {
     w.wts = take((size_t)(M * L) * 4);
     w.mass = take((size_t)M * 4);
+    // buckets of 64 ids or more, four for an entry
+    w.shift = 6;
+    while (ceil_div(N, (int64_t)1 << w.shift) > 4 * L) ++w.shift;
+    w.buckets = (int)ceil_div(N, (int64_t)1 << w.shift);
+    w.first = take((size_t)(M * w.buckets) * 2);
   }
   const int64_t rows = grad ? grad_rows(M) : M;
   w.xc = take((size_t)(rows * K) * 2);
@@ -991,10 +1012,14 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad)
     w.piece = want < 4096 ? 4096 : want;
     if (w.piece > N) w.piece = ceil_div(N, 256) * 256;
     const int64_t tiles = ceil_div(K, 256) * ceil_div(rows, dx_tile(rows));
-    // as fill the CUs, while their sums (written and read once) stay a quarter of W's bytes
+    // as fill the CUs, unless their sums (4 bytes each, written and read at about 4 TB/s) take
+    // longer than the stages that another split saves: the least of stages * us / s + s * sums
     int64_t s = 256 / tiles;
-    if (s > w.piece / (16 * rows)) s = w.piece / (16 * rows);
-    if (s > w.piece / 256) s = w.piece / 256;
+    const int64_t stages = w.piece / 64;
+    const double us = dx_tile(rows) <= 64 ? 0.4 : dx_tile(rows) <= 128 ? 0.6 : 1.0;
+    const double best = std::sqrt((double)stages * us / ((double)rows * (double)K * 8.0 / 4.0e6));
+    if ((double)s > best) s = (int64_t)best;
+    if (s > stages / 2) s = stages / 2;
     w.splits = (int)(s < 1 ? 1 : s);
     w.g = take((size_t)(rows * w.piece) * 2);
     w.dx = take((size_t)(w.splits * rows * K) * 4);
@@ -1012,15 +1037,15 @@ T* at(void* ws, size_t off) {
 hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, bool direct, hipStream_t st) {
   if (p.index) {
     const dim3 grid((unsigned)ceil_div(p.M, 4));
-    const size_t lds = (size_t)p.L * 4 * sizeof(int);
+    const size_t lds = (size_t)p.L * 8 * sizeof(int);
     if (p.teacher_bf16)
       hipLaunchKernelGGL((vocab_list_kernel<true>), grid, dim3(256), lds, st, p.index, p.teacher, p.teacher_lse,
                          p.M, p.N, (int)p.L, p.scale, at<int>(ws, w.keys), at<float>(ws, w.wts),
-                         at<float>(ws, w.mass));
+                         at<float>(ws, w.mass), at<uint16_t>(ws, w.first), w.buckets, w.shift);
     else
       hipLaunchKernelGGL((vocab_list_kernel<false>), grid, dim3(256), lds, st, p.index, p.teacher, p.teacher_lse,
                          p.M, p.N, (int)p.L, p.scale, at<int>(ws, w.keys), at<float>(ws, w.wts),
-                         at<float>(ws, w.mass));
+                         at<float>(ws, w.mass), at<uint16_t>(ws, w.first), w.buckets, w.shift);
   }
   if (direct) return hipGetLastError();
   VocabCompact c = {};
@@ -1055,6 +1080,9 @@ VocabTile common(const VocabArgs& p, const Layout& w, void* ws) {
   if (p.index) {
     t.wts = at<float>(ws, w.wts);
     t.mass = at<float>(ws, w.mass);
+    t.first = at<uint16_t>(ws, w.first);
+    t.buckets = w.buckets;
+    t.shift = w.shift;
   }
   t.L = (int)p.L;
   t.scale = p.scale;
