@@ -278,8 +278,8 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  * All results are the same bits on every run.
  *
  *   X        [M, ldx] bf16 hidden states, W [N, ldw] bf16 head (read); rows on 16-byte
- *            boundaries, strides at most 2^21. M and N at most 2^22, N >= 1, K a multiple
- *            of 8 in [8, 65536].
+ *            boundaries, strides at most 2^21. M at most 2^22, N in [1, 2^22 - 1], K a
+ *            multiple of 8 in [8, 65536].
  *   scale    finite, > 0: the logits' scale, 1 / temperature (scaled logits stay in fp32's
  *            range; scaled teacher logits below it count as -inf).
  *   target   [M] int64;  index [M, L] int64, 1 <= L <= 1024;  teacher [M, L] fp32

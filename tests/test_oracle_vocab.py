@@ -136,7 +136,7 @@ def test_refusals(B, fn):
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert c(scale=s) == -1
     for bad in (dict(K=60), dict(ldx=68), dict(ldw=65), dict(X=P(4104)), dict(W=P(8200)), dict(K=65544, ldx=65544, ldw=65544, lddx=65544, lddw=65544),
-                dict(M=(1 << 22) + 1), dict(N=(1 << 22) + 1), dict(ldw=(1 << 21) + 8), dict(ldx=(1 << 21) + 8),
+                dict(M=(1 << 22) + 1), dict(N=1 << 22), dict(ldw=(1 << 21) + 8), dict(ldx=(1 << 21) + 8),
                 dict(lse=P(258))):
         assert c(**bad) == -2, bad
     if "grad" in fn:

@@ -10,9 +10,10 @@
 
 namespace {
 
-// Tokens and ids: what keeps the products' tile counts in 31 bits. Rows: offsets inside a
-// tile of 256 rows in 30 bits.
-constexpr int64_t kMaxRows = (int64_t)1 << 22, kMaxK = (int64_t)1 << 16, kMaxLd = (int64_t)1 << 21;
+// Tokens and ids: what keeps the products' tile counts in 31 bits, and an id with a place in a
+// list in 32. Rows: offsets inside a tile of 256 rows in 30 bits.
+constexpr int64_t kMaxTokens = (int64_t)1 << 22, kMaxIds = kMaxTokens - 1;
+constexpr int64_t kMaxK = (int64_t)1 << 16, kMaxLd = (int64_t)1 << 21;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -22,8 +23,8 @@ int check_shape(const char* fn, int64_t M, int64_t N, int64_t K) {
                          (long long)N, (long long)K);
   if (K % 8 != 0)
     return qr::set_error(QR_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 8", fn, (long long)K);
-  if (M > kMaxRows || N > kMaxRows || K > kMaxK)
-    return qr::set_error(QR_ERR_UNSUPPORTED, "%s: M and N are at most 2^22, K 2^16", fn);
+  if (M > kMaxTokens || N > kMaxIds || K > kMaxK)
+    return qr::set_error(QR_ERR_UNSUPPORTED, "%s: M is at most 2^22, N 2^22 - 1, K 2^16", fn);
   return QR_OK;
 }
 

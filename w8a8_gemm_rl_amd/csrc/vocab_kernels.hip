@@ -39,8 +39,8 @@ constexpr int kNone = 0x7fffffff;  // list key of no entry: past every id
 // One wave per token: weights p of the list's entries and the entries in the order of
 // their ids (entries of one id in the order of the list, ids outside [0, N) last).
 // p = softmax over the entries, or exp(c s - teacher_lse). L <= kVocabMaxList; ranks by
-// counting in LDS, which is little beside the products. first[b] is the first entry whose id is
-// not below b << shift, where a tile's waves begin to look for their entries.
+// counting in LDS. first[b] is the first entry whose id is not below b << shift, where a tile's
+// waves begin to look for theirs. 4096 tokens of 64 entries take 8.5 us, a launch 2 of them.
 template <bool BF16>
 __global__ __launch_bounds__(256) void vocab_list_kernel(const int64_t* __restrict__ index,
                                                          const void* __restrict__ teacher,
@@ -49,51 +49,76 @@ __global__ __launch_bounds__(256) void vocab_list_kernel(const int64_t* __restri
                                                          float* __restrict__ wts, float* __restrict__ mass,
                                                          uint16_t* __restrict__ first, int buckets, int shift) {
   extern __shared__ __attribute__((aligned(16))) uint8_t list_smem[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int* key = reinterpret_cast<int*>(list_smem) + wave * 2 * L;
-  int* sorted = key + L;
+  // An entry's id and place in the list, in that order of weight: no two alike. N < 2^22, so
+  // that ~0 is no entry's.
+  static_assert(kVocabMaxList <= 1024, "places of 10 bits");
+  constexpr uint32_t kNoCode = ~0u;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, L4 = (L + 3) & ~3;
+  uint32_t* code = reinterpret_cast<uint32_t*>(list_smem) + wave * 3 * L4;
+  int* sorted = reinterpret_cast<int*>(code + L4);
+  float* y = reinterpret_cast<float*>(sorted + L4);  // c s, then the weight
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   if (t >= M) return;
-  const int64_t* ids = index + t * L;
-  auto logit = [&](int j) {
-    if constexpr (BF16) return scale * bf16_lo(static_cast<const uint16_t*>(teacher)[t * L + j]);
-    else return scale * static_cast<const float*>(teacher)[t * L + j];
-  };
-  float top = -INFINITY;
-  for (int j = lane; j < L; j += 64) {
-    const int64_t id = ids[j];
-    const bool ok = id >= 0 && id < N;
-    key[j] = ok ? (int)id : kNone;
-    if (ok) top = fmaxf(top, logit(j));
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+  float top = -INFINITY, sum = 0.0f;
+  int none = 0;  // entries that are none
+  for (int j0 = 0; j0 < L4; j0 += 64) {
+    const int j = j0 + lane;
+    bool ok = false;
+    if (j < L) {
+      const int64_t id = index[t * L + j];
+      float s;
+      if constexpr (BF16) s = bf16_lo(static_cast<const uint16_t*>(teacher)[t * L + j]);
+      else s = static_cast<const float*>(teacher)[t * L + j];
+      ok = id >= 0 && id < N;
+      code[j] = ok ? (uint32_t)id << 10 | (uint32_t)j : kNoCode;
+      y[j] = scale * s;
+      if (ok) top = fmaxf(top, y[j]);
+    } else if (j < L4) {
+      code[j] = kNoCode;
+    }
+    none += __popcll(__ballot(j < L && !ok));
   }
   top = wave_max(top);
-  float norm, sum = 0.0f;
-  if (teacher_lse) {
-    norm = teacher_lse[t];
-  } else {
-    norm = top == -INFINITY ? 0.0f : top;  // no entry with weight: all weights zero
+  // without an entry of weight all weights are zero
+  const float norm = teacher_lse ? teacher_lse[t] : top == -INFINITY ? 0.0f : top;
+  for (int j = lane; j < L; j += 64) {
+    y[j] = code[j] == kNoCode ? 0.0f : expf(y[j] - norm);
+    sum += y[j];
   }
-  for (int j = lane; j < L; j += 64)
-    if (key[j] != kNone) sum += expf(logit(j) - norm);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  const float div = teacher_lse ? 1.0f : (sum == 0.0f ? 1.0f : sum);
+  const float div = teacher_lse || sum == 0.0f ? 1.0f : sum;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's own part of LDS
-  for (int j = lane; j < L; j += 64) {
-    const int k = key[j];
+  int seen = L - none;  // place of the next one that is none
+  for (int j0 = 0; j0 < L; j0 += 64) {
+    const int j = j0 + lane;
+    const uint32_t mine = j < L ? code[j] : 0u;
+    const uint64_t b = __ballot(j < L && mine == kNoCode);
     int rank = 0;
-    for (int i = 0; i < L; ++i) rank += (key[i] < k || (key[i] == k && i < j)) ? 1 : 0;
-    sorted[rank] = k;
-    keys[t * L + rank] = k;
-    wts[t * L + rank] = k == kNone ? 0.0f : expf(logit(j) - norm) / div;
+    for (int i = 0; i < L4; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(code + i);
+      rank += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
+    }
+    if (mine == kNoCode) rank = seen + __popcll(b & below);
+    seen += __popcll(b);
+    if (j < L) {
+      const int k = mine == kNoCode ? kNone : (int)(mine >> 10);
+      sorted[rank] = k;
+      keys[t * L + rank] = k;
+      wts[t * L + rank] = y[j] / div;
+    }
   }
   if (lane == 0) mass[t] = sum / div;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  for (int r = lane; r <= L; r += 64) {  // buckets behind entry r - 1's, up to entry r's
-    int b = 0, end = buckets;
-    if (r > 0) b = sorted[r - 1] == kNone ? buckets : (sorted[r - 1] >> shift) + 1;
-    if (r < L && sorted[r] != kNone) end = (sorted[r] >> shift) + 1;
-    for (; b < end; ++b) first[t * buckets + b] = (uint16_t)r;
+  for (int b = lane; b < buckets; b += 64) {
+    int lo = 0, hi = L;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sorted[mid] < b << shift) lo = mid + 1;
+      else hi = mid;
+    }
+    first[t * buckets + b] = (uint16_t)lo;
   }
 }
 
@@ -570,7 +595,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       return;
     }
     const int64_t base = (int64_t)tok[j] * p.L;
-    constexpr int U = 4;  // entries read at once: lists are dense where ids are frequent ones
+    constexpr int U = 8;  // entries read at once: lists are dense where ids are frequent ones
     for (int e = ent[j]; e < p.L; e += U) {
       int key[U];
       float w[U];
@@ -834,35 +859,48 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const VocabTile p, fl
 }
 
 // dX of all tokens: the splits' sums in order (a split's parts of G one after the other),
-// rounded once; zeros for masked tokens. A wave takes 256 values of a token, eight sums at
-// once, so that a few tokens still fill the chip.
-__global__ __launch_bounds__(64) void vocab_dx_kernel(const float* __restrict__ part, int splits, int64_t rows,
-                                                      int64_t K, const int* __restrict__ inv,
-                                                      const int* __restrict__ nv, int twice,
-                                                      uint16_t* __restrict__ dX, int64_t lddx) {
+// rounded once; zeros for masked tokens. A block takes 256 values of a token, its waves (at
+// most kDxWaves) a run of the sums each, eight at once, which are added in order.
+constexpr int kDxWaves = 8;
+__global__ __launch_bounds__(64 * kDxWaves) void vocab_dx_kernel(const float* __restrict__ part, int splits,
+                                                                 int64_t rows, int64_t K,
+                                                                 const int* __restrict__ inv,
+                                                                 const int* __restrict__ nv, int twice,
+                                                                 uint16_t* __restrict__ dX, int64_t lddx) {
+  __shared__ float4 red[kDxWaves][64];
   const int64_t t = blockIdx.x, c = inv[t], h = 256 * (int64_t)blockIdx.y + 4 * threadIdx.x;
-  if (h >= K) return;
   const int n = *nv, parts = n <= twice ? 2 : 1, sums = splits * parts;
-  float v[4] = {};
-  if (c >= 0) {
+  const int waves = blockDim.y, wave = threadIdx.y;
+  const int run = (sums + waves - 1) / waves, end = run * (wave + 1) < sums ? run * (wave + 1) : sums;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (c >= 0 && h < K) {
     constexpr int U = 8;
-    for (int s0 = 0; s0 < sums; s0 += U) {
+    for (int s0 = run * wave; s0 < end; s0 += U) {
       float4 a[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int s = s0 + u < sums ? s0 + u : sums - 1;
+        const int s = s0 + u < end ? s0 + u : end - 1;
         const int64_t row = (parts == 2 ? s >> 1 : s) * rows + c + (parts == 2 ? (s & 1) * n : 0);
         a[u] = *reinterpret_cast<const float4*>(part + row * K + h);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool in = s0 + u < sums;
-        v[0] += in ? a[u].x : 0.0f; v[1] += in ? a[u].y : 0.0f;
-        v[2] += in ? a[u].z : 0.0f; v[3] += in ? a[u].w : 0.0f;
+        const bool in = s0 + u < end;
+        v.x += in ? a[u].x : 0.0f; v.y += in ? a[u].y : 0.0f;
+        v.z += in ? a[u].z : 0.0f; v.w += in ? a[u].w : 0.0f;
       }
     }
   }
-  *reinterpret_cast<uint2*>(dX + t * lddx + h) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+  if (waves > 1) {
+    red[wave][threadIdx.x] = v;
+    __syncthreads();
+    if (wave > 0) return;
+    for (int w = 1; w < waves; ++w) {
+      const float4 o = red[w][threadIdx.x];
+      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+    }
+  }
+  if (h < K) *reinterpret_cast<uint2*>(dX + t * lddx + h) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
 }
 
 // dW where there are no tokens at all.
@@ -1037,7 +1075,7 @@ T* at(void* ws, size_t off) {
 hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, bool direct, hipStream_t st) {
   if (p.index) {
     const dim3 grid((unsigned)ceil_div(p.M, 4));
-    const size_t lds = (size_t)p.L * 8 * sizeof(int);
+    const size_t lds = (size_t)(ceil_div(p.L, 4) * 4) * 12 * sizeof(int);
     if (p.teacher_bf16)
       hipLaunchKernelGGL((vocab_list_kernel<true>), grid, dim3(256), lds, st, p.index, p.teacher, p.teacher_lse,
                          p.M, p.N, (int)p.L, p.scale, at<int>(ws, w.keys), at<float>(ws, w.wts),
@@ -1184,9 +1222,12 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     else e = launch_one<kDW, 256, 256, 2, 4, 2>(y, ids, st);
     if (e != hipSuccess) return e;
   }
-  if (p.dX)
-    hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M, (unsigned)ceil_div(p.K, 256)), dim3(64), 0, st, at<float>(ws, w.dx), w.splits, rows,
-                       p.K, at<int>(ws, w.inv), at<int>(ws, w.nv), kTwice, p.dX, p.lddx);
+  if (p.dX) {
+    const int waves = w.splits <= 4 ? 1 : w.splits <= 4 * kDxWaves ? (w.splits + 3) / 4 : kDxWaves;
+    hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M, (unsigned)ceil_div(p.K, 256)), dim3(64, (unsigned)waves),
+                       0, st, at<float>(ws, w.dx), w.splits, rows, p.K, at<int>(ws, w.inv), at<int>(ws, w.nv), kTwice,
+                       p.dX, p.lddx);
+  }
   return hipGetLastError();
 }
 
