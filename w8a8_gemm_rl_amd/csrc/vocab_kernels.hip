@@ -23,7 +23,7 @@
 namespace qr {
 namespace {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
@@ -235,6 +235,10 @@ __global__ __launch_bounds__(256) void vocab_gather_kernel(const VocabCompact p)
 // ---------------------------------------------------------------------------
 enum { kSums, kGrad, kDX, kDW };
 
+// Lambdas of a kernel share its state in registers only where they are inlined.
+#define QR_INLINE __attribute__((always_inline))
+
+
 struct VocabTile {
   const uint16_t *A, *B;
   int64_t lda, ldb;
@@ -320,7 +324,7 @@ template <int MODE, int BN, int BM, int WN, int WM, int S>
 __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_t* smem) {
   constexpr bool TA = MODE == kDX || MODE == kDW, TB = MODE == kDW;
   constexpr int NW = WN * WM, KS = 64;
-  constexpr int WTN = BN / WN, WTM = BM / WM, FN = WTN / 32, FM = WTM / 32;
+  constexpr int WTN = BN / WN, WTM = BM / WM, FN = WTN / 16, FM = WTM / 16;
   constexpr int IA = (BN / 8 + NW - 1) / NW * NW, IB = (BM / 8 + NW - 1) / NW * NW;
   constexpr int NA = IA / NW, NB = IB / NW, GA = (NA + 3) / 4, GB = (NB + 3) / 4, NI = NA + NB;
   constexpr int STAGE = (IA + IB) * 1024;
@@ -334,7 +338,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   // A few tokens need no launch to number them: each block does, and copies from X itself.
-  const bool direct = MODE == kSums && p.direct != 0;
+  const bool direct = MODE == kSums && BM <= 128 && p.direct != 0;
   const int nv = direct ? vocab_number(p, wid, lane, NW, smem) : *p.nv;
   const int* const rowmap = reinterpret_cast<const int*>(smem);  // direct: token of a compact one
   const bool twice = nv <= p.twice;       // G in two parts of bf16
@@ -362,13 +366,20 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * (split + 1) / p.splits)) - ks0;
 
   const int wn = wid % WN, wm = wid / WN;
-  const int lr = lane & 31, lg = lane >> 5;
+  const int lr = lane & 15, lg = lane >> 4;
   const int64_t a0 = (int64_t)ta * BN, b0 = (int64_t)tb * BM;
 
   // Copies. Lanes whose 16 bytes lie outside the operand take an offset past the
   // buffer: zeros.
   constexpr uint32_t kBig = 0x80000000u;
   const int ll = lane >> 3, pc = lane & 7;
+  // The lane for code behind the products: what is computed from it stays there instead of
+  // occupying registers during them.
+  auto fresh_lane = [&]() QR_INLINE {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l & 63;
+  };
   // row of K (columns) or chunk of 8 elements of K (rows) that copy I of an operand takes
   auto rows_of = [&](int I, int& row, int& chunk) {
     row = I * 8 + ll;
@@ -377,7 +388,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   auto cols_of = [&](int I, int rowbytes, int& k, int& chunk) {
     const int cpr = rowbytes / 16;  // chunks of a row: 32 or 16
     k = I * (64 / cpr) + lane / cpr;
-    chunk = (lane % cpr) ^ ((k & 3) << 2);
+    chunk = (lane % cpr) ^ ((k & 3) << 2 | (k >> 3 & 1) << 1);
   };
   auto offset = [&](bool cols, int I, int rowbytes, int tile_rows, int64_t ld, int64_t left) {
     if (cols) {
@@ -455,70 +466,61 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     else dma_group<1, false>(lds, vo, r, soff);
   };
 
-  // Operand reads of K step h (16 elements): lane (lr, lg) takes row or column lr of a
+  // Operand reads of K step h (32 elements): lane (lr, lg) takes row or column lr of a
   // fragment and elements 8 lg .. 8 lg + 7.
-  const int jl = lane & 15, tk = 8 * lg + (jl >> 2);  // columns: K row of the lane's address
-  const int tc = 32 * ((lane >> 4) & 1) + 8 * (jl & 3);
+  const int tk = 8 * lg + (lr >> 2);  // columns: K row of the lane's address, and its byte's
+  const int tc = 8 * (lr & 3), tx = (lr >> 2) << 6 | (lg & 1) << 5;
   auto read = [&](bool cols, const uint8_t* base, int w0, int i, int h, int rowbytes) {
     if (cols) {
-      const int c = ((w0 + 32 * i) * 2 + tc) ^ ((jl >> 2) << 6);
-      const uint8_t* s = base + (16 * h + tk) * rowbytes + c;
+      const uint8_t* s = base + (32 * h + tk) * rowbytes + (((w0 + 16 * i) * 2 + tc) ^ tx);
       typedef __attribute__((address_space(3))) v4s* lds_v4s;
       const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s));
       const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(s + 4 * rowbytes));
       const v8s v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
       return __builtin_bit_cast(v8b, v);
     }
-    const int r = w0 + 32 * i + lr;
-    return *reinterpret_cast<const v8b*>(base + r * 128 + (((2 * h + lg) ^ ((lr >> 1) & 7)) << 4));
+    const int r = w0 + 16 * i + lr;
+    return *reinterpret_cast<const v8b*>(base + r * 128 + (((4 * h + lg) ^ ((lr >> 1) & 7)) << 4));
   };
-  v16f acc[FN][FM];
+  v4f acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = v16f{};
-  v8b fa[2][FN], fb[2][FM];
+    for (int j = 0; j < FM; ++j) acc[i][j] = v4f{};
+  v8b fa[2][FN], fb[2][FM];  // operands of two K steps
+  auto load_a = [&](const uint8_t* st, int h, int buf, int i) { fa[buf][i] = read(TA, st, wn * WTN, i, h, RA); };
+  auto load_b = [&](const uint8_t* st, int h, int buf, int j) {
+    fb[buf][j] = read(TB, st + IA * 1024, wm * WTM, j, h, RB);
+  };
   auto load_ops = [&](const uint8_t* st, int h, int buf) {
 #pragma unroll
-    for (int i = 0; i < FN; ++i) fa[buf][i] = read(TA, st, wn * WTN, i, h, RA);
+    for (int i = 0; i < FN; ++i) load_a(st, h, buf, i);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) fb[buf][j] = read(TB, st + IA * 1024, wm * WTM, j, h, RB);
+    for (int j = 0; j < FM; ++j) load_b(st, h, buf, j);
   };
   auto multiply_row = [&](int buf, int i) {
 #pragma unroll
     for (int j = 0; j < FM; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[buf][i], fb[buf][j], acc[i][j], 0, 0, 0);
-  };
-  auto interleave = [&]() {
-    constexpr int NR = FN * (TA ? 2 : 1) + FM * (TB ? 2 : 1), NM = FN * FM;
-#pragma unroll
-    for (int q = 0; q < NM; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, (NR + NM - 1) / NM, 0);
-    }
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[buf][i], fb[buf][j], acc[i][j], 0, 0, 0);
   };
 
   // Compact tokens of the lane, and where their lists enter the wave's ids.
   const int64_t id_lo = p.id0 + a0 + wn * WTN;
   const int own = (int)(p.ids - a0 - wn * WTN < WTN ? p.ids - a0 - wn * WTN : WTN);  // ids of the wave
   int tok[FM], ent[FM];  // ent: a list's one id, or its first entry that may be the wave's
-  float gt[FM], l2[FM], ga[FM];
-  if constexpr (MODE == kSums || MODE == kGrad) {
+  auto token = [&](int j) QR_INLINE {
+    const int64_t c = b0 + wm * WTM + 16 * j + lr;
+    tok[j] = c < nv ? (direct ? rowmap[c] : p.map[c]) : -1;
+    ent[j] = kNone;
+    if (tok[j] < 0 || own <= 0) return;
+    if (p.L > 1) ent[j] = p.first[(int64_t)tok[j] * p.buckets + (id_lo >> p.shift)];
+    else ent[j] = direct && p.target ? (int)p.target[tok[j]] : p.keys[tok[j]];
+  };
+  // before the products where registers allow
+  constexpr bool EARLY = BM <= 128;
+  if constexpr (EARLY && (MODE == kSums || MODE == kGrad)) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int64_t c = b0 + wm * WTM + 32 * j + lr;
-      tok[j] = c < nv ? (direct ? rowmap[c] : p.map[c]) : -1;
-      ent[j] = kNone;
-      gt[j] = l2[j] = ga[j] = 0.0f;
-      if (tok[j] >= 0) {
-        if (p.L == 1) ent[j] = direct && p.target ? (int)p.target[tok[j]] : p.keys[tok[j]];
-        if constexpr (MODE == kGrad) {
-          gt[j] = p.g[tok[j]] * p.scale * p.sign;
-          ga[j] = p.mass ? gt[j] * p.mass[tok[j]] : gt[j];
-          l2[j] = p.lse[tok[j]] * kLog2e;
-        }
-      }
-    }
+    for (int j = 0; j < FM; ++j) token(j);
     if (direct) __syncthreads();  // the map's place is the ring's
   }
 #pragma unroll
@@ -528,15 +530,6 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       for (int g = 0; g < NG; ++g) issue_group(g, s, ks0 + s, false);
     }
 
-  if constexpr (MODE == kSums || MODE == kGrad) {
-    if (p.L > 1) {
-      const int64_t bucket = id_lo >> p.shift;
-#pragma unroll
-      for (int j = 0; j < FM; ++j)
-        if (tok[j] >= 0 && own > 0) ent[j] = p.first[(int64_t)tok[j] * p.buckets + bucket];
-    }
-  }
-
   // One stage. The next one opens when its copies have landed and no wave reads this one
   // any more (the last step's operands are in registers); its slot is refilled at once. The
   // three kinds of stage are bodies of their own: waits merged over a branch would be
@@ -544,31 +537,39 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   int cs = 0, it = 0;
   auto stage = [&](auto refill, auto last) {
     const int ns = cs + 1 == S ? 0 : cs + 1;
+    const uint8_t *here = smem + cs * STAGE, *next = smem + ns * STAGE;
+    // the next step's reads behind the first rows' products: RPR fragments a row
+    constexpr int NF = FN + FM, RPR = (NF + (FN > 2 ? FN * 3 / 4 : FN) - 1) / (FN > 2 ? FN * 3 / 4 : FN);
+    auto reads = [&](const uint8_t* st, int h, int buf, int row) QR_INLINE {
 #pragma unroll
-    for (int h = 0; h < 3; ++h) {
-      load_ops(smem + cs * STAGE, h + 1, (h + 1) & 1);
+      for (int f = row * RPR; f < (row + 1) * RPR && f < NF; ++f) {
+        if (f < FM) load_b(st, h, buf, f);
+        else load_a(st, h, buf, f - FM);
+      }
+    };
 #pragma unroll
-      for (int i = 0; i < FN; ++i) multiply_row(h & 1, i);
-      interleave();
+    for (int i = 0; i < FN; ++i) {
+      reads(here, 1, 1, i);
+      multiply_row(0, i);
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!decltype(last)::value) {
       if constexpr (decltype(refill)::value != 0) wait_vm<(S - 2) * NI>();
       else wait_stages<NI, S - 2>(nk - 2 - it);
       __syncthreads();
-      load_ops(smem + ns * STAGE, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int i = 0; i < (FN > NG ? FN : NG); ++i) {
-      if (i < FN) multiply_row(1, i);
-      if constexpr (decltype(refill)::value != 0) {
+      if (i < FN) {
+        if constexpr (!decltype(last)::value) reads(next, 0, 0, i);
+        multiply_row(1, i);
         __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (decltype(refill)::value != 0) {
         if (i < NG) issue_group(i, cs, ks0 + it + S, decltype(refill)::value == 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
     cs = ns;
   };
   if (nk > 0) {
@@ -583,35 +584,49 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   }
 
   // Entries of the lists among the wave's ids: f(entry, its weight, register of its id).
-  auto hit = [&](int64_t e, int key, float w, auto f) {
-    const int d = (int)(key - id_lo);
-    if (((d >> 2) & 1) == lg) f(e, w, (d >> 5) * 16 + ((d >> 3) & 3) * 4 + (d & 3));
-  };
-  auto hits = [&](int j, auto f) {
-    if (tok[j] < 0 || own <= 0) return;
+  // All lanes of the wave go along: f(whether the lane has one, ...).
+  auto hits = [&](int j, auto f) QR_INLINE {
+    auto hit = [&](int64_t e, int key, float w) QR_INLINE {
+      const int d = (int)(key - id_lo);
+      const bool mine = key >= id_lo && key < id_lo + own && ((d >> 2) & 3) == lg;
+      if (__any(mine)) f(mine, e, w, (d >> 4) * 4 + (d & 3));
+    };
     if (p.L == 1) {
-      const float w = MODE == kGrad && p.wts ? p.wts[tok[j]] : 1.0f;
-      if (ent[j] >= id_lo && ent[j] < id_lo + own) hit(tok[j], ent[j], w, f);
+      hit(tok[j], ent[j], MODE == kGrad && p.wts && tok[j] >= 0 ? p.wts[tok[j]] : 1.0f);
       return;
     }
     const int64_t base = (int64_t)tok[j] * p.L;
-    constexpr int U = 8;  // entries read at once: lists are dense where ids are frequent ones
-    for (int e = ent[j]; e < p.L; e += U) {
+    constexpr int U = 4;  // entries read at once: lists are dense where ids are frequent ones
+    int e = tok[j] < 0 || own <= 0 ? p.L : ent[j];
+    while (__any(e < p.L)) {
       int key[U];
       float w[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = e + u < p.L ? e + u : p.L - 1;
-        key[u] = e + u < p.L ? p.keys[base + i] : kNone;
-        w[u] = MODE == kGrad ? p.wts[base + i] : 0.0f;
+        const bool in = e + u < p.L;
+        key[u] = in ? p.keys[base + e + u] : kNone;
+        w[u] = MODE == kGrad && in ? p.wts[base + e + u] : 0.0f;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (key[u] >= id_lo && key[u] < id_lo + own) hit(base + e + u, key[u], w[u], f);
-      if (key[U - 1] >= id_lo + own) break;
+      for (int u = 0; u < U; ++u) hit(base + e + u, key[u], w[u]);
+      e = key[U - 1] >= id_lo + own ? p.L : e + U;
     }
   };
   const float c2 = p.scale * kLog2e;
+
+  // What follows takes a B fragment at a time: its values v[4 i + r], A side 16 i + 4 lg + r.
+  auto values = [&](int j, float* v) QR_INLINE {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[4 * i + r] = acc[i][j][r];
+  };
+  auto beyond = [&](float* v, float to) QR_INLINE {  // ids that are not the piece's
+    if (own >= WTN) return;
+#pragma unroll
+    for (int e = 0; e < 4 * FN; ++e) v[e] = 16 * (e >> 2) + 4 * lg + (e & 3) >= own ? to : v[e];
+  };
 
   if constexpr (MODE == kSums) {
     // base-2 maximum and sum of each token over the tile's ids
@@ -619,35 +634,28 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     float2* red = reinterpret_cast<float2*>(smem);  // [WN][BM]
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      hits(j, [&](int64_t e, float, int reg) {
-        float v = 0.0f;
+      float v[4 * FN];
+      values(j, v);
+      if constexpr (!EARLY) token(j);
+      hits(j, [&](bool mine, int64_t e, float, int reg) QR_INLINE {
+        float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) v = reg == i * 16 + r ? acc[i][j][r] : v;
-        p.zl[e] = v * p.scale;
+        for (int k = 0; k < 4 * FN; ++k) z = reg == k ? v[k] : z;
+        if (mine) p.zl[e] = z * p.scale;
       });
+      beyond(v, -INFINITY);
       float m = -INFINITY, s = 0.0f;
-      if (own < WTN) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= own) acc[i][j][r] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
+      for (int k = 0; k < 4 * FN; ++k) m = fmaxf(m, v[k]);
+      m = fmaxf(m, __shfl_xor(m, 16, 64));
       m = fmaxf(m, __shfl_xor(m, 32, 64));
       m = m == -INFINITY ? m : m * c2;
       const float sub = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -sub));
+      for (int k = 0; k < 4 * FN; ++k) s += __builtin_amdgcn_exp2f(__builtin_fmaf(v[k], c2, -sub));
+      s += __shfl_xor(s, 16, 64);
       s += __shfl_xor(s, 32, 64);
-      if (lg == 0) red[wn * BM + wm * WTM + 32 * j + lr] = make_float2(m, s);
+      if (lg == 0) red[wn * BM + wm * WTM + 16 * j + lr] = make_float2(m, s);
     }
     __syncthreads();
     for (int c = tid; c < BM; c += 64 * NW) {
@@ -660,115 +668,94 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       for (int w = 0; w < WN; ++w) s += red[w * BM + c].y * __builtin_amdgcn_exp2f(red[w * BM + c].x - sub);
       p.part[(int64_t)ta * p.ldpart + b0 + c] = make_float2(m, s);
     }
-    return;
-  }
-
-  if constexpr (MODE == kGrad) {
-    // G in fp32. The matrix cores take bf16: up to `twice` tokens, where the products are
-    // bound by memory, G is held in two parts (its rounding to bf16 and what that left: 2^-16 of
-    // each element); beyond, rounded once (2^-8, as much as the results' own rounding).
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-#pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          acc[i][j][r] = ga[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], c2, -l2[j]));
-      if (own < WTN) {
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (32 * i + 8 * (r >> 2) + 4 * lg + (r & 3) >= own) acc[i][j][r] = 0.0f;
-      }
-      hits(j, [&](int64_t, float w, int reg) {
-        const float b = gt[j] * w;
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] -= reg == i * 16 + r ? b : 0.0f;
-      });
-    }
   }
 
   if constexpr (MODE == kDX) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      const int64_t c = b0 + wm * WTM + 32 * j + lr;
+      const int64_t c = b0 + wm * WTM + 16 * j + lr;
       if (c >= ext_b) continue;
       float* row = p.out32 + ((int64_t)split * p.rows32 + c) * p.K;
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t h = a0 + wn * WTN + 32 * i + 8 * q + 4 * lg;
-          if (h >= p.K) continue;
-          const v16f& v = acc[i][j];
-          float4 o = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          float4* d = reinterpret_cast<float4*>(row + h);
-          if (p.add) {
-            const float4 w = *d;
-            o.x += w.x; o.y += w.y; o.z += w.z; o.w += w.w;
-          }
-          *d = o;
+      for (int i = 0; i < FN; ++i) {
+        const int64_t h = a0 + wn * WTN + 16 * i + 4 * lg;
+        if (h >= p.K) continue;
+        float4 o = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        float4* d = reinterpret_cast<float4*>(row + h);
+        if (p.add) {
+          const float4 w = *d;
+          o.x += w.x; o.y += w.y; o.z += w.z; o.w += w.w;
         }
+        *d = o;
+      }
     }
-    return;
   }
 
   // bf16 outputs leave through the ring, each wave its own part, so that stores run along
   // the B side's rows, 16 bytes a lane.
   if constexpr (MODE == kGrad || MODE == kDW) {
     __syncthreads();
-    constexpr int LD = WTN * 2 + 16;
-    static_assert(NW * 32 * LD <= S * STAGE, "a fragment per wave fits");
-    uint8_t* so = smem + wid * (32 * LD);
+    const int l = fresh_lane();
+    constexpr int LD = WTN * 2 + 16, CPR = WTN / 8;
+    static_assert(NW * 16 * LD <= S * STAGE, "a fragment per wave fits");
+    uint8_t* so = smem + wid * (16 * LD);
     const int64_t row0 = b0 + wm * WTM, lim = MODE == kGrad ? nv : p.ids;
     const int64_t col0 = a0 + wn * WTN, left = MODE == kGrad ? WTN : p.K - col0;
-    constexpr int CPR = WTN / 8;
-    auto rows_out = [&](int j, uint16_t* out, auto nt) {
+    auto rows_out = [&](int j, const float* v, uint16_t* out, auto nt) QR_INLINE {
 #pragma unroll
       for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v16f& v = acc[i][j];
-          *reinterpret_cast<uint2*>(so + lr * LD + (32 * i + 8 * q + 4 * lg) * 2) =
-              make_uint2(bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]));
-        }
+        *reinterpret_cast<uint2*>(so + (l & 15) * LD + (16 * i + 4 * (l >> 4)) * 2) =
+            make_uint2(bf16_pair(v[4 * i], v[4 * i + 1]), bf16_pair(v[4 * i + 2], v[4 * i + 3]));
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int k = 0; k < 32 * CPR / 64; ++k) {
-        const int c = lane + 64 * k, ml = c / CPR, nl = 8 * (c % CPR);
-        const int64_t m = row0 + 32 * j + ml;
+      for (int k = 0; k < 16 * CPR / 64; ++k) {
+        const int c = l + 64 * k, ml = c / CPR, nl = 8 * (c % CPR);
+        const int64_t m = row0 + 16 * j + ml;
         if (m >= lim || nl >= left) continue;
         typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-        const u4 v = *reinterpret_cast<const u4*>(so + ml * LD + nl * 2);
+        const u4 q = *reinterpret_cast<const u4*>(so + ml * LD + nl * 2);
         u4* dst = reinterpret_cast<u4*>(out + m * p.ldo + col0 + nl);
-        if constexpr (decltype(nt)::value) __builtin_nontemporal_store(v, dst);
-        else *dst = v;
+        if constexpr (decltype(nt)::value) __builtin_nontemporal_store(q, dst);
+        else *dst = q;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
-    // (the branch around the loop: around the store the two are merged, without nt)
-    if (MODE == kDW && p.stream) {
-#pragma unroll
-      for (int j = 0; j < FM; ++j) rows_out(j, p.out16, std::true_type{});
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < FM; ++j) rows_out(j, p.out16, std::false_type{});
-    if constexpr (MODE == kGrad) {
-      if (!twice) return;
+    auto all_out = [&](auto nt) QR_INLINE {
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
+        float v[4 * FN];
+        values(j, v);
+        if constexpr (MODE == kGrad) {
+          // G in fp32. The matrix cores take bf16: up to `twice` tokens, where the products are
+          // bound by memory, G is held in two parts (its rounding to bf16 and what that left:
+          // 2^-16 of each element); beyond, rounded once (2^-8, as much as the results' own).
+          if constexpr (!EARLY) token(j);
+          float gt = 0.0f, ga = 0.0f, l2 = 0.0f;
+          if (tok[j] >= 0) {
+            gt = p.g[tok[j]] * p.scale * p.sign;
+            ga = p.mass ? gt * p.mass[tok[j]] : gt;
+            l2 = p.lse[tok[j]] * kLog2e;
+          }
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+          for (int k = 0; k < 4 * FN; ++k) v[k] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(v[k], c2, -l2));
+          beyond(v, 0.0f);
+          hits(j, [&](bool mine, int64_t, float w, int reg) QR_INLINE {
+            const float b = mine ? gt * w : 0.0f;
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            acc[i][j][r] -= __uint_as_float(bf16_pair(0.0f, acc[i][j][r]) & 0xffff0000u);
-        rows_out(j, p.out16 + nv * p.ldo, std::false_type{});
+            for (int k = 0; k < 4 * FN; ++k) v[k] -= reg == k ? b : 0.0f;
+          });
+        }
+        rows_out(j, v, p.out16, nt);
+        if (MODE == kGrad && twice) {
+#pragma unroll
+          for (int k = 0; k < 4 * FN; ++k) v[k] -= __uint_as_float(bf16_pair(0.0f, v[k]) & 0xffff0000u);
+          rows_out(j, v, p.out16 + nv * p.ldo, nt);
+        }
       }
-    }
+    };
+    // (the branch around the loop: around the store the two are merged, without nt)
+    if (MODE == kDW && p.stream) all_out(std::true_type{});
+    else all_out(std::false_type{});
   }
 }
 
@@ -786,7 +773,7 @@ __global__ __launch_bounds__(512, 1) void vocab_grads_kernel(const VocabTile x, 
   constexpr int A = ring_bytes<256, BM, 8, S>(), C = ring_bytes<256, 256, 8, 2>();
   __shared__ __attribute__((aligned(1024))) uint8_t smem[A > C ? A : C];
   if ((int)blockIdx.x < dx_blocks) vocab_tile<kDX, 256, BM, WN, WM, S>(x, blockIdx.x, smem);
-  else vocab_tile<kDW, 256, 256, 2, 4, 2>(w, blockIdx.x - dx_blocks, smem);
+  else vocab_tile<kDW, 256, 256, 4, 2, 2>(w, blockIdx.x - dx_blocks, smem);
 }
 
 // Sums of the tiles' parts, a wave a compact token: lse, and sum_j p (log p - (z_j - lse))
@@ -982,7 +969,7 @@ hipError_t launch_logits(const VocabTile& p, const LogitTile& t, int64_t M, hipS
     case 32: return launch_one<MODE, 256, 32, 8, 1, 4>(p, M, st);
     case 64: return launch_one<MODE, 256, 64, 4, 2, 3>(p, M, st);
     case 128: return launch_one<MODE, 256, 128, 4, 2, 3>(p, M, st);
-    default: return launch_one<MODE, 256, 256, 2, 4, 2>(p, M, st);
+    default: return launch_one<MODE, 256, 256, 4, 2, 2>(p, M, st);
   }
 }
 
@@ -998,7 +985,7 @@ hipError_t launch_dx(const VocabTile& x, int64_t rows, hipStream_t st) {
     case 32: return launch_one<kDX, 256, 32, 8, 1, 4>(x, rows, st);
     case 64: return launch_one<kDX, 256, 64, 4, 2, 3>(x, rows, st);
     case 128: return launch_one<kDX, 256, 128, 4, 2, 3>(x, rows, st);
-    default: return launch_one<kDX, 256, 256, 2, 4, 2>(x, rows, st);
+    default: return launch_one<kDX, 256, 256, 4, 2, 2>(x, rows, st);
   }
 }
 
@@ -1007,7 +994,7 @@ hipError_t launch_both(const VocabTile& x, const VocabTile& w, int64_t rows, hip
     case 32: return launch_grads<32, 8, 1, 4>(x, w, rows, st);
     case 64: return launch_grads<64, 4, 2, 3>(x, w, rows, st);
     case 128: return launch_grads<128, 4, 2, 3>(x, w, rows, st);
-    default: return launch_grads<256, 2, 4, 2>(x, w, rows, st);
+    default: return launch_grads<256, 4, 2, 2>(x, w, rows, st);
   }
 }
 
@@ -1146,10 +1133,10 @@ void vocab_plan(int64_t M, int64_t N, int64_t K, int* ids, int* tokens, int* row
 
 hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
   const Layout w = layout(p.M, p.N, p.K, p.L, p.index != nullptr, false);
-  const bool direct = p.M <= kVocabDirect;
+  const LogitTile& tile = logit_tile(p.M, p.N, p.K);
+  const bool direct = p.M <= kVocabDirect && tile.bm <= 128;
   hipError_t e = prepare(p, w, ws, direct, st);
   if (e != hipSuccess) return e;
-  const LogitTile& tile = logit_tile(p.M, p.N, p.K);
   VocabTile t = common(p, w, ws);
   t.lda = p.ldw;
   t.direct = direct ? (int)p.M : 0;
@@ -1219,7 +1206,7 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     y.ldo = p.lddw;
     if (p.dX && p.dW) e = launch_both(x, y, rows, st);
     else if (p.dX) e = launch_dx(x, rows, st);
-    else e = launch_one<kDW, 256, 256, 2, 4, 2>(y, ids, st);
+    else e = launch_one<kDW, 256, 256, 4, 2, 2>(y, ids, st);
     if (e != hipSuccess) return e;
   }
   if (p.dX) {
