@@ -213,12 +213,11 @@ def _check_large(X, W, got, lse, grads, g, ids, p, live, sign, e_p):
     assert not bool(grads[0][~live].any())
 
 
-@pytest.mark.parametrize("M,N,K", LARGE)
-def test_large_sizes(M, N, K):
+def _large(M, N, K, keep):
     r = torch.Generator().manual_seed(M + N + K)
     X = torch.randn((M, K), generator=r).to(torch.bfloat16).to(DEV)
     W = (torch.randn((N, K), generator=r) * (1.5 / K ** 0.5)).to(torch.bfloat16).to(DEV)
-    live = (torch.rand(M, generator=r) < 0.9).to(DEV)
+    live = (torch.rand(M, generator=r) < keep).to(DEV)
     live[M // 2] = True
     g = torch.randn(M, generator=r).to(DEV)
     target = torch.randint(0, N, (M,), generator=r).to(DEV)
@@ -239,6 +238,19 @@ def test_large_sizes(M, N, K):
     p = torch.softmax(teacher.double().masked_fill(~ok, -1e9), 1) * ok
     e_p = 2 * (6 * float(teacher.abs().max()) + L + 10) * U
     _check_large(X, W, loss, lse, grads, g, index, p, live, 1.0, e_p)
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_sizes(M, N, K):
+    _large(M, N, K, 0.9)
+
+
+@pytest.mark.parametrize("M,N,K,keep", [(200, 100003, 264, 0.9), (200, 100003, 264, 0.3), (700, 40300, 264, 0.1),
+                                        (2000, 3001, 136, 0.05), (2000, 20001, 72, 0.0)])
+def test_few_of_many_tokens_count(M, N, K, keep):
+    """Tiles of 256 tokens with fewer, G in two parts among many masked tokens."""
+    assert M > 1000 or B.vocab_plan(M, N, K)[1] == 256
+    _large(M, N, K, keep)
 
 
 @pytest.mark.parametrize("L", [0, 6])

@@ -9,9 +9,14 @@
 // their count nv known to the GPU only) and their rows of X copied together, so masked
 // rows cost nothing and what they hold reaches no sum.
 //
-// Four products share one kernel (vocab_tile_kernel): the logits' softmax sums; the same
-// logits again with G as output, a piece of the vocabulary at a time; that piece's part
-// of dX and its rows of dW.
+// Four products share one kernel (vocab_tile): the logits' softmax sums; the same logits
+// again with G as output, a piece of the vocabulary at a time; that piece's part of dX
+// and its rows of dW. The sums need 2 M N K operations and W once, the gradient 6 M N K and
+// W twice (its logits are computed again: held, they would be M N values) beside dW. Up to
+// about 128 tokens memory bounds both (W of 131072 x 3584 for 1 token: 145 us, 6.5 TB/s), beyond
+// about 512 the matrix cores and the power that they take: 4096 tokens of 131072 ids, 3584 wide,
+// take 3.05 ms for the sums (1.26 PFLOP/s), 8.83 ms for the gradient (1.31), 5120 wide 3.96 ms
+// (1.39); a library product alone of the sums' shape reaches 1.38 - 1.42.
 #include <cmath>
 #include <type_traits>
 
@@ -153,9 +158,10 @@ __device__ __forceinline__ void vocab_take_row(const VocabCompact& p, int64_t t,
   }
 }
 
-// Compact numbers and rows in one launch, a block a token that counts the live ones itself
-// (M reads a block: up to kVocabCount tokens less than another launch).
-constexpr int64_t kVocabCount = 2048;
+// Compact numbers and rows in one launch, a block a token that counts the live ones itself.
+// M reads a block: up to kVocabCount tokens less than another launch (gradients, 5000 ids: 1 token
+// 21 us, in two launches 22, 300 tokens 38 and 39, 1024 66 and 67; 2048 101 and 100, 4096 224 and 217).
+constexpr int64_t kVocabCount = 512;
 __global__ __launch_bounds__(256) void vocab_compact_kernel(const VocabCompact p) {
   __shared__ int below[4], all[4];
   const int64_t t = blockIdx.x;
@@ -238,7 +244,6 @@ enum { kSums, kGrad, kDX, kDW };
 // Lambdas of a kernel share its state in registers only where they are inlined.
 #define QR_INLINE __attribute__((always_inline))
 
-
 struct VocabTile {
   const uint16_t *A, *B;
   int64_t lda, ldb;
@@ -275,7 +280,9 @@ struct VocabTile {
   int twice;       // up to so many compact tokens G is held in two parts
 };
 
-// Tokens that a launch's blocks number themselves (vocab_number).
+// Tokens that a launch's blocks number themselves (vocab_number): 16 tokens of 5000 ids,
+// 512 wide, take 13 us, numbered by a launch of their own 15; 128 of 32768, 1024 wide, 27 and 31;
+// 256 of 5000 17 and 19.
 constexpr int kVocabDirect = 256;
 
 // The compact tokens of p.direct tokens into LDS (int [nv] from the start); their count. All
@@ -300,26 +307,35 @@ __device__ __forceinline__ int vocab_number(const VocabTile& p, int wid, int lan
   return __builtin_amdgcn_readfirstlane(n);
 }
 
-// A block: BN x BM outputs, A side by B side, over K steps of 64 through a ring of S
-// stages in LDS, filled by LDS-DMA copies; 8 waves of 32x32x16 MFMAs. An operand is
-// either K-contiguous ("rows": its rows run along K; LDS rows of 64 elements, 16-byte
-// chunk q of row r at q ^ (r / 2 % 8)) or has its rows along the other axis ("columns": LDS
-// holds 64 rows of K, read with the transposing load, whose 16 lanes take four rows of
-// K by 16 columns; 64-byte pieces of row k at p ^ (k % 4), so that the four rows meet
-// different banks).
-//          A side            B side             K
-//   kSums  ids (W, rows)     tokens (X, rows)   hidden
-//   kGrad  ids (W, rows)     tokens (X, rows)   hidden
-//   kDX    hidden (W, cols)  tokens (G, rows)   ids
-//   kDW    hidden (X, cols)  ids (G, cols)      tokens
-// Register 4 q + r of a fragment: A side 8 q + 4 lg + r, B side lane % 32.
-//
-// `block` and the grid it belongs to may be a part of the launch's.
 template <int BN, int BM, int NW, int S>
 constexpr int ring_bytes() {  // copies of 8 rows (1 KB), as many by each wave
   return S * ((BN / 8 + NW - 1) / NW + (BM / 8 + NW - 1) / NW) * NW * 1024;
 }
 
+// A block: BN x BM outputs, A side by B side, over K steps of 64 through a ring of S
+// stages in LDS, filled by LDS-DMA copies; WN x WM waves. An operand is either K-contiguous
+// ("rows": its rows run along K; LDS rows of 64 elements, 16-byte chunk q of row r at
+// q ^ (r / 2 % 8)) or has its rows along the other axis ("columns": LDS holds 64 rows of K,
+// read with the transposing load, whose 16 lanes take four rows of K by 16 columns; the 16-byte
+// chunks of row k at q ^ (4 (k % 4) + 2 (k / 8 % 2)), so that the rows that a load takes at
+// once meet different banks: none of its reads conflict).
+//          A side            B side             K
+//   kSums  ids (W, rows)     tokens (X, rows)   hidden
+//   kGrad  ids (W, rows)     tokens (X, rows)   hidden
+//   kDX    hidden (W, cols)  tokens (G, rows)   ids
+//   kDW    hidden (X, cols)  ids (G, cols)      tokens
+//
+// Products are 16 x 16 x 32: with all CUs busy they are bound by power (the clock falls to 1.5 -
+// 1.6 GHz, the matrix cores busy for 69% of it), and from registers alone these reach 2.06
+// PFLOP/s, 32 x 32 x 16 1.87. In the kernel: 4096 tokens of 131072 ids, 3584 wide, 3.05 ms and
+// 3.20, 5120 wide 3.96 and 4.14, the first's gradient 8.83 and 9.00. Register r of fragment
+// (i, j): A side 16 i + 4 (lane / 16) + r, B side 16 j + lane % 16.
+//
+// A wave's tile in the 256 x 256 block is 64 x 128 (four by two waves; two by four spill registers, and
+// four waves of 128 x 128 took 8% longer). A block's reads of LDS and copies fit beside its products there;
+// with fewer tokens a tile's copies (about 21 bytes a clock for a CU) bind it.
+//
+// `block` and the grid it belongs to may be a part of the launch's.
 template <int MODE, int BN, int BM, int WN, int WM, int S>
 __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_t* smem) {
   constexpr bool TA = MODE == kDX || MODE == kDW, TB = MODE == kDW;
@@ -583,8 +599,8 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     stage(std::integral_constant<int, 0>{}, std::true_type{});
   }
 
-  // Entries of the lists among the wave's ids: f(entry, its weight, register of its id).
-  // All lanes of the wave go along: f(whether the lane has one, ...).
+  // Entries of the lists among the wave's ids: f(whether the lane has one, the entry, its
+  // weight, its id's value among the fragment's). All lanes of the wave go along.
   auto hits = [&](int j, auto f) QR_INLINE {
     auto hit = [&](int64_t e, int key, float w) QR_INLINE {
       const int d = (int)(key - id_lo);
@@ -726,9 +742,9 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
         float v[4 * FN];
         values(j, v);
         if constexpr (MODE == kGrad) {
-          // G in fp32. The matrix cores take bf16: up to `twice` tokens, where the products are
-          // bound by memory, G is held in two parts (its rounding to bf16 and what that left:
-          // 2^-16 of each element); beyond, rounded once (2^-8, as much as the results' own).
+          // G in fp32. The matrix cores take bf16: up to `twice` tokens G is held in two parts
+          // (its rounding to bf16 and what that left: 2^-16 of each element); beyond, rounded
+          // once (2^-8 of each, as much as the rounding of the results).
           if constexpr (!EARLY) token(j);
           float gt = 0.0f, ga = 0.0f, l2 = 0.0f;
           if (tok[j] >= 0) {
@@ -766,7 +782,8 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const Vocab
 }
 
 // A piece's part of dX (the first `dx_blocks` blocks) and rows of dW in one launch: dX has
-// few tiles of many stages, which seldom fill the CUs, dW many of few.
+// few tiles of many stages, which seldom fill the CUs, dW many of few (gradients, in one launch | in two:
+// 2048 tokens of 131072 ids, 5120 wide, 6.83 | 7.52 ms; 64 of 5000, 1024 wide, 31 | 39 us).
 template <int BM, int WN, int WM, int S>
 __global__ __launch_bounds__(512, 1) void vocab_grads_kernel(const VocabTile x, const VocabTile w, int dx_blocks) {
   static_assert(WN * WM == 8, "one block size");
@@ -905,7 +922,10 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 constexpr int64_t kMaxBlocks = (int64_t)1 << 21;
 constexpr int64_t kMall = (int64_t)256 << 20;
 
-// Up to so many tokens that count G is held in two parts of bf16.
+// Up to so many tokens that count G is held in two parts of bf16: relative errors of the
+// gradients are 0.0017 then (their own rounding), 0.0024 with one part. While memory bounds the products
+// that is cheap, at most 30% at 128 tokens of 131072 ids, 3584 wide (780 and 600 us); 14% at
+// 33 of 32768 (160 and 141), nothing at 1; beyond, the products would take twice as long.
 constexpr int kTwice = 128;
 int64_t grad_rows(int64_t M) { return M <= kTwice ? 2 * M : (M < 2 * kTwice ? 2 * kTwice : M); }
 
@@ -930,10 +950,14 @@ hipError_t launch_grads(VocabTile x, VocabTile w, int64_t rows, hipStream_t st) 
 }
 
 // Tiles of the logits' products, and what a round of them takes: us a stage and beside
-// the stages, measured where the matrix cores and copies bind (one card; 257 tokens of 100003
-// ids, 3584 wide: 64 x 32 tiles 641 us, 64 x 64 427, 64 x 128 385, 256 x 32 604, 256 x 64 352, 256 x 128 307,
-// 256 x 256 381; 64 tokens of 5000 ids: 26, 26, 29, 35, 38, 48, 76; 64 of 131072: 249, 193, 211, 207, 171, 177, 229).
-// What memory bounds takes the same on every tile.
+// the stages, measured where the matrix cores and copies bind. Sums on every tile in turn (us, one
+// card, 3584 wide; what memory bounds takes the same on every tile that holds all tokens):
+//                              64 x 32   64   128   256 x 32   64   128   256
+//   1 token of 131072 ids          151  146   184        145  145   154   211
+//   64 tokens of 5000 ids           23   27    33         46   51    57    91
+//   64 of 131072                   244  174   199        205  148   155   222
+//   257 of 100003                  627  378   372        617  342   283   356
+//   1024 of 32768                  543  402   341        582  320   231   192
 struct LogitTile {
   int bn, bm;     // ids, tokens
   int per_round;  // tiles that the CUs hold at once
@@ -973,16 +997,18 @@ hipError_t launch_logits(const VocabTile& p, const LogitTile& t, int64_t M, hipS
   }
 }
 
-// Rows of G in a tile of dX
+// Rows of G (twice the tokens up to kTwice) in a tile of dX: the fewest that hold all, up to 64
+// (16 tokens of 32768 ids, 3584 wide: 86 us, on 128 rows 88; 32 rows gain nothing), else the
+// cheaper by the measured costs of 128 and 256 (us, dX with its logits, 3584 wide, 128 | 256: 33
+// tokens of 32768 93 | 106, 128 of 131072 467 | 451, 257 of 100003 545 | 576, 600 of 32768 324 | 320,
+// 512 of 131072 950 | 872, 2048 of 131072, 5120 wide, 5620 | 5130).
 int dx_tile(int64_t rows) {
-  if (rows <= 32) return 32;
   if (rows <= 64) return 64;
   return ceil_div(rows, 128) * 55 < ceil_div(rows, 256) * 92 ? 128 : 256;
 }
 
 hipError_t launch_dx(const VocabTile& x, int64_t rows, hipStream_t st) {
   switch (dx_tile(rows)) {
-    case 32: return launch_one<kDX, 256, 32, 8, 1, 4>(x, rows, st);
     case 64: return launch_one<kDX, 256, 64, 4, 2, 3>(x, rows, st);
     case 128: return launch_one<kDX, 256, 128, 4, 2, 3>(x, rows, st);
     default: return launch_one<kDX, 256, 256, 4, 2, 2>(x, rows, st);
@@ -991,7 +1017,6 @@ hipError_t launch_dx(const VocabTile& x, int64_t rows, hipStream_t st) {
 
 hipError_t launch_both(const VocabTile& x, const VocabTile& w, int64_t rows, hipStream_t st) {
   switch (dx_tile(rows)) {
-    case 32: return launch_grads<32, 8, 1, 4>(x, w, rows, st);
     case 64: return launch_grads<64, 4, 2, 3>(x, w, rows, st);
     case 128: return launch_grads<128, 4, 2, 3>(x, w, rows, st);
     default: return launch_grads<256, 4, 2, 2>(x, w, rows, st);
