@@ -134,6 +134,25 @@ __device__ __forceinline__ bool vocab_live(const int64_t* target, const int* key
   return id >= 0 && id < N;
 }
 
+// Parts of a piece's ids whose sums of dX are kept apart: as fill the CUs, unless the sums (4 bytes
+// each, written and read at about 4 TB/s) take longer than the stages that another part saves (the least
+// of stages us / s + s sums). The tokens that count decide, whom the GPU numbers.
+struct DxPlan {
+  int tiles_a, bm;  // tiles of the hidden values, rows of a tile
+  int stages;       // of a piece
+  int cap;          // rows of sums that the workspace holds
+  float worth;      // stages us / (time of a row of sums)
+  __host__ __device__ int splits(int64_t rows) const {
+    if (rows <= 0 || cap <= 0) return 1;
+    int64_t s = 256 / (tiles_a * ((rows + bm - 1) / bm));
+    const float best = sqrtf(worth / (float)rows);
+    if ((float)s > best) s = (int64_t)best;
+    if (s > stages / 2) s = stages / 2;
+    if (s > cap / rows) s = cap / rows;
+    return (int)(s < 1 ? 1 : s);
+  }
+};
+
 struct VocabCompact {
   const int64_t* target;  // NULL: lists
   int* keys;              // [M][L]; written (L = 1) with `target`
@@ -142,9 +161,15 @@ struct VocabCompact {
   const uint16_t* X;
   uint16_t* Xc;  // rows of the compact tokens; twice over where nv <= twice
   int twice;
-  int *nv, *map, *inv;
+  DxPlan dx;  // gradients
+  int *nv, *map, *inv;  // nv: their count, and dX's splits
   float *value, *lse;  // losses: masked tokens' results
 };
+
+__device__ __forceinline__ void vocab_count(const VocabCompact& p, int n) {
+  p.nv[0] = n;
+  p.nv[1] = p.dx.splits(n <= p.twice ? 2 * n : n);
+}
 
 // Token t (live, compact number c of n): its entries of the tables, its rows of Xc. One block.
 __device__ __forceinline__ void vocab_take_row(const VocabCompact& p, int64_t t, int c, int n) {
@@ -185,7 +210,7 @@ __global__ __launch_bounds__(256) void vocab_compact_kernel(const VocabCompact p
   const bool live = __syncthreads_or(mine);
   const int c = below[0] + below[1] + below[2] + below[3], n = all[0] + all[1] + all[2] + all[3];
   if (threadIdx.x == 0) {
-    if (t == 0) *p.nv = n;
+    if (t == 0) vocab_count(p, n);
     if (p.target) p.keys[t] = live ? (int)p.target[t] : kNone;
     p.inv[t] = live ? c : -1;
     if (live) {
@@ -228,7 +253,7 @@ __global__ __launch_bounds__(1024) void vocab_scan_kernel(const VocabCompact p) 
     }
     base += all;
   }
-  if (threadIdx.x == 0) *p.nv = base;
+  if (threadIdx.x == 0) vocab_count(p, base);
 }
 
 __global__ __launch_bounds__(256) void vocab_gather_kernel(const VocabCompact p) {
@@ -255,7 +280,7 @@ struct VocabTile {
   int64_t ids;     // ids of the piece
   int64_t id0;     // its first id
   int64_t K;
-  int tiles_a, splits;
+  int tiles_a;
   const int* map;
   const int* keys;
   const float *wts, *mass, *lse, *g;
@@ -268,8 +293,7 @@ struct VocabTile {
   float* zl;       // kSums: logits of the lists' ids
   uint16_t* out16; // kGrad: G [nv][ldo]; kDW: dW + id0 ldo
   int64_t ldo;
-  float* out32;    // kDX: [splits][rows32][K]
-  int64_t rows32;
+  float* out32;    // kDX: [splits][rows of G][K]
   int add;         // kDX: add to what is there
   // kSums, kGrad, kDX: W's copies carry the non-temporal hint; kDW: stores do. Where a
   // tile holds all tokens nothing of W is read again, and dW is written to be read later (us
@@ -365,7 +389,8 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
 
   // An XCD takes one contiguous part of the tiles; groups of up to 8 B tiles share A tiles.
   const int tiles_b = (int)((ext_b + BM - 1) / BM);
-  const int tiles = p.tiles_a * tiles_b, total = tiles * p.splits, xcd = block & 7;
+  const int splits = MODE == kDX ? p.nv[1] : 1;
+  const int tiles = p.tiles_a * tiles_b, total = tiles * splits, xcd = block & 7;
   const int end = (int)((int64_t)total * (xcd + 1) / 8);
   int cur = (int)((int64_t)total * xcd / 8) + (block >> 3);
   if (cur >= end) return;
@@ -378,8 +403,8 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     tb = __builtin_amdgcn_readfirstlane(b0 + cur % gb);
     ta = __builtin_amdgcn_readfirstlane(cur / gb);
   }
-  const int ks0 = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * split / p.splits));
-  const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * (split + 1) / p.splits)) - ks0;
+  const int ks0 = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * split / splits));
+  const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)stages * (split + 1) / splits)) - ks0;
 
   const int wn = wid % WN, wm = wid / WN;
   const int lr = lane & 15, lg = lane >> 4;
@@ -691,7 +716,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     for (int j = 0; j < FM; ++j) {
       const int64_t c = b0 + wm * WTM + 16 * j + lr;
       if (c >= ext_b) continue;
-      float* row = p.out32 + ((int64_t)split * p.rows32 + c) * p.K;
+      float* row = p.out32 + ((int64_t)split * rows + c) * p.K;
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
         const int64_t h = a0 + wn * WTN + 16 * i + 4 * lg;
@@ -866,14 +891,14 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const VocabTile p, fl
 // rounded once; zeros for masked tokens. A block takes 256 values of a token, its waves (at
 // most kDxWaves) a run of the sums each, eight at once, which are added in order.
 constexpr int kDxWaves = 8;
-__global__ __launch_bounds__(64 * kDxWaves) void vocab_dx_kernel(const float* __restrict__ part, int splits,
-                                                                 int64_t rows, int64_t K,
+__global__ __launch_bounds__(64 * kDxWaves) void vocab_dx_kernel(const float* __restrict__ part, int64_t K,
                                                                  const int* __restrict__ inv,
                                                                  const int* __restrict__ nv, int twice,
                                                                  uint16_t* __restrict__ dX, int64_t lddx) {
   __shared__ float4 red[kDxWaves][64];
   const int64_t t = blockIdx.x, c = inv[t], h = 256 * (int64_t)blockIdx.y + 4 * threadIdx.x;
-  const int n = *nv, parts = n <= twice ? 2 : 1, sums = splits * parts;
+  const int n = nv[0], parts = n <= twice ? 2 : 1, sums = nv[1] * parts;
+  const int64_t rows = (int64_t)n * parts;
   const int waves = blockDim.y, wave = threadIdx.y;
   const int run = (sums + waves - 1) / waves, end = run * (wave + 1) < sums ? run * (wave + 1) : sums;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -929,22 +954,24 @@ constexpr int64_t kMall = (int64_t)256 << 20;
 constexpr int kTwice = 128;
 int64_t grad_rows(int64_t M) { return M <= kTwice ? 2 * M : (M < 2 * kTwice ? 2 * kTwice : M); }
 
-// Blocks of a product, a multiple of 8 (an XCD's share each).
+// Blocks of a product, a multiple of 8 (an XCD's share each). dX: its splits give 256 at most.
+template <int MODE>
 int64_t product_blocks(VocabTile& p, int64_t max_b, int BN, int BM) {
   p.tiles_a = (int)ceil_div(p.ext_a, BN);
-  return ceil_div(p.tiles_a * ceil_div(max_b, BM) * p.splits, 8) * 8;
+  const int64_t tiles = p.tiles_a * ceil_div(max_b, BM);
+  return MODE == kDX && tiles < 256 ? 256 : ceil_div(tiles, 8) * 8;
 }
 
 template <int MODE, int BN, int BM, int WN, int WM, int S>
 hipError_t launch_one(VocabTile p, int64_t max_b, hipStream_t st) {
-  const dim3 grid((unsigned)product_blocks(p, max_b, BN, BM));
+  const dim3 grid((unsigned)product_blocks<MODE>(p, max_b, BN, BM));
   hipLaunchKernelGGL((vocab_tile_kernel<MODE, BN, BM, WN, WM, S>), grid, dim3(64 * WN * WM), 0, st, p);
   return hipGetLastError();
 }
 
 template <int BM, int WN, int WM, int S>
 hipError_t launch_grads(VocabTile x, VocabTile w, int64_t rows, hipStream_t st) {
-  const int64_t nx = product_blocks(x, rows, 256, BM), nw = product_blocks(w, w.ids, 256, 256);
+  const int64_t nx = product_blocks<kDX>(x, rows, 256, BM), nw = product_blocks<kDW>(w, w.ids, 256, 256);
   hipLaunchKernelGGL((vocab_grads_kernel<BM, WN, WM, S>), dim3((unsigned)(nx + nw)), dim3(512), 0, st, x, w, (int)nx);
   return hipGetLastError();
 }
@@ -1027,7 +1054,7 @@ struct Layout {
   size_t nv, map, inv, keys, wts, mass, first, zl, xc, part, g, dx, bytes;
   int buckets, shift;  // of ids, for lists
   int64_t piece;  // ids of a piece of the gradient
-  int splits;     // parts of a piece's ids whose sums of dX are kept apart
+  DxPlan sums;
 };
 
 Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad) {
@@ -1038,7 +1065,7 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad)
     at += align256(n);
     return o;
   };
-  w.nv = take(4);
+  w.nv = take(8);
   w.map = take((size_t)M * 4);
   w.inv = take((size_t)M * 4);
   w.keys = take((size_t)(M * L) * 4);
@@ -1061,18 +1088,22 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad)
     const int64_t want = ((int64_t)128 << 20) / rows / 256 * 256;
     w.piece = want < 4096 ? 4096 : want;
     if (w.piece > N) w.piece = ceil_div(N, 256) * 256;
-    const int64_t tiles = ceil_div(K, 256) * ceil_div(rows, dx_tile(rows));
-    // as fill the CUs, unless their sums (4 bytes each, written and read at about 4 TB/s) take
-    // longer than the stages that another split saves: the least of stages * us / s + s * sums
-    int64_t s = 256 / tiles;
-    const int64_t stages = w.piece / 64;
-    const double us = dx_tile(rows) <= 64 ? 0.4 : dx_tile(rows) <= 128 ? 0.6 : 1.0;
-    const double best = std::sqrt((double)stages * us / ((double)rows * (double)K * 8.0 / 4.0e6));
-    if ((double)s > best) s = (int64_t)best;
-    if (s > stages / 2) s = stages / 2;
-    w.splits = (int)(s < 1 ? 1 : s);
+    DxPlan& d = w.sums;
+    d.bm = dx_tile(rows);
+    d.tiles_a = (int)ceil_div(K, 256);
+    d.stages = (int)(w.piece / 64);
+    d.worth = (float)d.stages * (d.bm <= 64 ? 0.4f : d.bm <= 128 ? 0.6f : 1.0f) * 5.0e5f / (float)K;
+    d.cap = 0x7fffffff;
+    // room for the splits of all tokens and of fewer
+    int64_t cap = rows;
+    for (int64_t n = d.bm < rows ? d.bm : rows;; n = 2 * n < rows ? 2 * n : rows) {
+      const int64_t sums = n * d.splits(n);
+      cap = sums > cap ? sums : cap;
+      if (n == rows) break;
+    }
+    d.cap = (int)cap;
     w.g = take((size_t)(rows * w.piece) * 2);
-    w.dx = take((size_t)(w.splits * rows * K) * 4);
+    w.dx = take((size_t)(cap * K) * 4);
   }
   w.bytes = at;
   return w;
@@ -1106,6 +1137,7 @@ hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, bool direct, h
   c.X = p.X;
   c.Xc = at<uint16_t>(ws, w.xc);
   c.twice = p.lse_out ? -1 : kTwice;
+  c.dx = w.sums;
   c.nv = at<int>(ws, w.nv);
   c.map = at<int>(ws, w.map);
   c.inv = at<int>(ws, w.inv);
@@ -1136,7 +1168,6 @@ VocabTile common(const VocabArgs& p, const Layout& w, void* ws) {
   }
   t.L = (int)p.L;
   t.scale = p.scale;
-  t.splits = 1;
   t.twice = p.lse_out ? -1 : kTwice;
   return t;
 }
@@ -1219,9 +1250,7 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     x.B = y.B = G;
     x.ldb = y.ldb = w.piece;
     x.ext_a = y.ext_a = p.K;
-    x.splits = w.splits;
     x.out32 = at<float>(ws, w.dx);
-    x.rows32 = rows;
     x.add = id0 > 0;
     x.stream = rows <= dx_tile(rows);
     y.stream = rows <= 2 * kTwice;
@@ -1235,9 +1264,10 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (p.dX) {
-    const int waves = w.splits <= 4 ? 1 : w.splits <= 4 * kDxWaves ? (w.splits + 3) / 4 : kDxWaves;
+    const int splits = w.sums.splits(rows);
+    const int waves = splits <= 4 ? 1 : splits <= 4 * kDxWaves ? (splits + 3) / 4 : kDxWaves;
     hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M, (unsigned)ceil_div(p.K, 256)), dim3(64, (unsigned)waves),
-                       0, st, at<float>(ws, w.dx), w.splits, rows, p.K, at<int>(ws, w.inv), at<int>(ws, w.nv), kTwice,
+                       0, st, at<float>(ws, w.dx), p.K, at<int>(ws, w.inv), at<int>(ws, w.nv), kTwice,
                        p.dX, p.lddx);
   }
   return hipGetLastError();
