@@ -659,6 +659,8 @@ int qr_mxfp4_plan(int64_t M, int64_t N, int64_t K, int xfmt, int* tile_n, int* t
  *   *tile_ids, *tile_tokens  ids and tokens of a tile of the logits,
  *   *dx_rows  rows of a tile of dX (tokens, or up to 128 of them in two parts),
  *   *piece    ids that a gradient's workspace holds at once.
+ * Of masked tokens nothing is known when a call is enqueued: where few of M count, the kernels
+ * take tiles of 128 tokens instead of 256 and split dX's sums for those that do.
  * Pure host function; returns QR_OK or the calls' error for the shape.
  */
 int qr_vocab_plan(int64_t M, int64_t N, int64_t K, int* tile_ids, int* tile_tokens, int* dx_rows, int64_t* piece);

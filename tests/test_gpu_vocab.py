@@ -246,9 +246,11 @@ def test_large_sizes(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K,keep", [(200, 100003, 264, 0.9), (200, 100003, 264, 0.3), (700, 40300, 264, 0.1),
+                                        (700, 20001, 72, 0.25),
                                         (2000, 3001, 136, 0.05), (2000, 20001, 72, 0.0)])
 def test_few_of_many_tokens_count(M, N, K, keep):
-    """Tiles of 256 tokens with fewer, G in two parts among many masked tokens."""
+    """Plans for tiles of 256 tokens where one or two tiles of 128 hold all that count, G in two parts
+    among many masked tokens, none at all."""
     assert M > 1000 or B.vocab_plan(M, N, K)[1] == 256
     _large(M, N, K, keep)
 

@@ -266,6 +266,12 @@ __global__ __launch_bounds__(256) void vocab_gather_kernel(const VocabCompact p)
 // ---------------------------------------------------------------------------
 enum { kSums, kGrad, kDX, kDW };
 
+// Up to so many tokens that count G is held in two parts of bf16: relative errors of the
+// gradients are 0.0017 then (their own rounding), 0.0024 with one part. While memory bounds the products
+// that is cheap, at most 30% at 128 tokens of 131072 ids, 3584 wide (780 and 600 us); 14% at
+// 33 of 32768 (160 and 141), nothing at 1; beyond, the products would take twice as long.
+constexpr int kTwice = 128;
+
 // Lambdas of a kernel share its state in registers only where they are inlined.
 #define QR_INLINE __attribute__((always_inline))
 
@@ -295,8 +301,8 @@ struct VocabTile {
   int64_t ldo;
   float* out32;    // kDX: [splits][rows of G][K]
   int add;         // kDX: add to what is there
-  // kSums, kGrad, kDX: W's copies carry the non-temporal hint; kDW: stores do. Where a
-  // tile holds all tokens nothing of W is read again, and dW is written to be read later (us
+  // kSums, kGrad, kDX: W's copies may carry the non-temporal hint; kDW: stores may. They do where a
+  // tile holds all tokens that count: nothing of W is read again, and dW is written to be read later (us
   // with / without, 3584 wide, W past the MALL or not there yet): logp 1 x 131072 145 / 164, 128 x
   // 131072 166 / 181, 1 x 32768 45 / 50; gradient 1 x 131072 466 / 575, 33 x 32768 148 / 183. kGrad reads
   // without it where kDX will find W in the MALL (33 x 32768: 3 us).
@@ -386,6 +392,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
   const int64_t ext_b = MODE == kDW ? p.ids : (MODE == kDX ? rows : nv);
   const int64_t klen = MODE == kDW ? rows : (MODE == kDX ? p.ids : p.K);
   const int stages = (int)((klen + KS - 1) / KS);
+  const bool stream = p.stream && (MODE == kDW ? rows <= 2 * kTwice : ext_b <= BM);
 
   // An XCD takes one contiguous part of the tiles; groups of up to 8 B tiles share A tiles.
   const int tiles_b = (int)((ext_b + BM - 1) / BM);
@@ -493,7 +500,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       }
     }
     if constexpr (MODE != kDW && BM <= 128) {
-      if (isA && p.stream) {
+      if (isA && stream) {
         if (cnt == 4) dma_group<4, true>(lds, vo, r, soff);
         else if (cnt == 3) dma_group<3, true>(lds, vo, r, soff);
         else if (cnt == 2) dma_group<2, true>(lds, vo, r, soff);
@@ -795,7 +802,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
       }
     };
     // (the branch around the loop: around the store the two are merged, without nt)
-    if (MODE == kDW && p.stream) all_out(std::true_type{});
+    if (MODE == kDW && stream) all_out(std::true_type{});
     else all_out(std::false_type{});
   }
 }
@@ -804,6 +811,22 @@ template <int MODE, int BN, int BM, int WN, int WM, int S>
 __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const VocabTile p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[ring_bytes<BN, BM, WN * WM, S>()];
   vocab_tile<MODE, BN, BM, WN, WM, S>(p, blockIdx.x, smem);
+}
+
+// The logits' tiles of 256 x 256 are planned for all tokens; where few of them count, tiles of
+// 256 x 128 take less time (a round of the CUs 0.6 of the other's), if the launch has blocks for them:
+// 200 tokens of 2048, 32768 ids, 3584 wide, 83 -> 63 us, their gradient 272 -> 241; 120 of 250, 131072 ids,
+// 225 -> 161 and 805 -> 747.
+template <int MODE>
+__global__ __launch_bounds__(512, 1) void vocab_wide_kernel(const VocabTile p) {
+  constexpr int A = ring_bytes<256, 256, 8, 2>(), C = ring_bytes<256, 128, 8, 3>();
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[A > C ? A : C];
+  const uint32_t nv = (uint32_t)*p.nv, a = (uint32_t)p.tiles_a;
+  const uint32_t half = a * ((nv + 127) / 128), whole = a * ((nv + 255) / 256);
+  if (half <= gridDim.x && (half + 255) / 256 * 2 < (whole + 255) / 256 * 3)
+    vocab_tile<MODE, 256, 128, 4, 2, 3>(p, blockIdx.x, smem);
+  else
+    vocab_tile<MODE, 256, 256, 4, 2, 2>(p, blockIdx.x, smem);
 }
 
 // A piece's part of dX (the first `dx_blocks` blocks) and rows of dW in one launch: dX has
@@ -947,11 +970,6 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 constexpr int64_t kMaxBlocks = (int64_t)1 << 21;
 constexpr int64_t kMall = (int64_t)256 << 20;
 
-// Up to so many tokens that count G is held in two parts of bf16: relative errors of the
-// gradients are 0.0017 then (their own rounding), 0.0024 with one part. While memory bounds the products
-// that is cheap, at most 30% at 128 tokens of 131072 ids, 3584 wide (780 and 600 us); 14% at
-// 33 of 32768 (160 and 141), nothing at 1; beyond, the products would take twice as long.
-constexpr int kTwice = 128;
 int64_t grad_rows(int64_t M) { return M <= kTwice ? 2 * M : (M < 2 * kTwice ? 2 * kTwice : M); }
 
 // Blocks of a product, a multiple of 8 (an XCD's share each). dX: its splits give 256 at most.
@@ -1020,8 +1038,12 @@ hipError_t launch_logits(const VocabTile& p, const LogitTile& t, int64_t M, hipS
     case 32: return launch_one<MODE, 256, 32, 8, 1, 4>(p, M, st);
     case 64: return launch_one<MODE, 256, 64, 4, 2, 3>(p, M, st);
     case 128: return launch_one<MODE, 256, 128, 4, 2, 3>(p, M, st);
-    default: return launch_one<MODE, 256, 256, 4, 2, 2>(p, M, st);
+    default: break;
   }
+  VocabTile w = p;
+  const int64_t blocks = product_blocks<MODE>(w, M, 256, 256);
+  hipLaunchKernelGGL((vocab_wide_kernel<MODE>), dim3((unsigned)(blocks < 256 ? 256 : blocks)), dim3(512), 0, st, w);
+  return hipGetLastError();
 }
 
 // Rows of G (twice the tokens up to kTwice) in a tile of dX: the fewest that hold all, up to 64
@@ -1202,7 +1224,7 @@ hipError_t launch_vocab_loss(const VocabArgs& p, void* ws, hipStream_t st) {
   t.ldb = direct ? p.ldx : p.K;
   t.ldpart = p.M;
   t.zl = at<float>(ws, w.zl);
-  t.stream = p.M <= tile.bm;
+  t.stream = true;
   float2* const part = at<float2>(ws, w.part);
   // a launch's blocks times their threads stay in 32 bits
   const int64_t ids = kMaxBlocks / ceil_div(p.M, tile.bm) * tile.bn;
@@ -1244,7 +1266,7 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     t.out16 = G;
     t.ldo = w.piece;
     const LogitTile& tile = logit_tile(p.M, ids, p.K);
-    t.stream = p.M <= tile.bm && (!p.dX || ids * p.K * 2 > kMall);
+    t.stream = !p.dX || ids * p.K * 2 > kMall;
     if ((e = launch_logits<kGrad>(t, tile, p.M, st)) != hipSuccess) return e;
     VocabTile x = t, y = t;  // dX, dW
     x.B = y.B = G;
@@ -1252,8 +1274,7 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     x.ext_a = y.ext_a = p.K;
     x.out32 = at<float>(ws, w.dx);
     x.add = id0 > 0;
-    x.stream = rows <= dx_tile(rows);
-    y.stream = rows <= 2 * kTwice;
+    x.stream = y.stream = true;
     y.A = at<uint16_t>(ws, w.xc);
     y.lda = p.K;
     y.out16 = p.dW + (p.dW ? id0 * p.lddw : 0);
