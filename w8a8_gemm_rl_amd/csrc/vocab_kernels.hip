@@ -356,14 +356,15 @@ constexpr int ring_bytes() {  // copies of 8 rows (1 KB), as many by each wave
 //   kDW    hidden (X, cols)  ids (G, cols)      tokens
 //
 // Products are 16 x 16 x 32: with all CUs busy they are bound by power (the clock falls to 1.5 -
-// 1.6 GHz, the matrix cores busy for 69% of it), and from registers alone these reach 2.06
+// 1.9 GHz, the matrix cores busy for 69% of it), and from registers alone these reach 2.06
 // PFLOP/s, 32 x 32 x 16 1.87. In the kernel: 4096 tokens of 131072 ids, 3584 wide, 3.05 ms and
 // 3.20, 5120 wide 3.96 and 4.14, the first's gradient 8.83 and 9.00. Register r of fragment
 // (i, j): A side 16 i + 4 (lane / 16) + r, B side 16 j + lane % 16.
 //
 // A wave's tile in the 256 x 256 block is 64 x 128 (four by two waves; two by four spill registers, and
-// four waves of 128 x 128 took 8% longer). A block's reads of LDS and copies fit beside its products there;
-// with fewer tokens a tile's copies (about 21 bytes a clock for a CU) bind it.
+// four waves of 128 x 128 took 8% longer). Copies bind smaller tiles: a CU takes in about 21 - 23 bytes a
+// clock, 12 bytes for 1000 operations on 256 x 128 (matrix cores 42 - 50% busy), 8 on 256 x 256. Tiles of
+// 192 x 320 and 128 x 384, 8 and 10 bytes, gain 13% at best and lose elsewhere.
 //
 // `block` and the grid it belongs to may be a part of the launch's.
 template <int MODE, int BN, int BM, int WN, int WM, int S>
