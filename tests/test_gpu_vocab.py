@@ -611,6 +611,46 @@ def test_captured_chain_from_hidden_states_and_back():
     _check_backward(d, lse, g, want[0][3], want[0][4])
 
 
+def test_captured_calls_follow_the_masks():
+    """One graph of the calls, replayed with all, some, few and none of the tokens counting: what the
+    kernels choose for those that count is chosen anew each time."""
+    M, N, K, L = 700, 20001, 136, 5
+    r = torch.Generator().manual_seed(12)
+    X = torch.randn((M, K), generator=r).to(torch.bfloat16).to(DEV)
+    W = (torch.randn((N, K), generator=r) * 0.1).to(torch.bfloat16).to(DEV)
+    g = torch.randn(M, generator=r).to(DEV)
+    teacher = torch.randn((M, L), generator=r).to(DEV)
+    ids = torch.randint(0, N, (M, L), generator=r)
+    masks = [torch.rand(M, generator=r) < keep for keep in (1.0, 0.5, 0.2, 0.1, 0.0)]
+    lists = [torch.where(m[:, None], ids, torch.tensor(-1)).to(DEV) for m in masks]
+
+    def calls(index, target):
+        logp, lse = B.vocab_logp(X, W, target)
+        grads = B.vocab_logp_grad(X, W, target, lse, g)
+        loss, dlse = B.vocab_distill(X, W, index, teacher)
+        return (logp, lse, loss, dlse) + tuple(grads) + tuple(B.vocab_distill_grad(X, W, index, teacher, dlse, g))
+
+    want = [[t.clone() for t in calls(i, i[:, 0].contiguous())] for i in lists]
+    index, target = lists[0].clone(), lists[0][:, 0].contiguous()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        calls(index, target)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = calls(index, target)
+    for k in (0, 3, 1, 4, 2, 0, 4, 3):
+        index.copy_(lists[k])
+        target.copy_(lists[k][:, 0])
+        graph.replay()
+        eager = calls(lists[k], lists[k][:, 0].contiguous())
+        torch.cuda.synchronize()
+        for i, (a, b, c) in enumerate(zip(out, want[k], eager)):
+            assert torch.equal(a, b) and torch.equal(c, b), (k, i)
+    assert not bool(want[4][4].any()) and not bool(want[4][5].any())
+
+
 def test_refused_calls():
     d = _inputs(4, 100, 64, L=3, seed=1)
     t = torch.zeros(4, dtype=torch.int64, device=DEV)
