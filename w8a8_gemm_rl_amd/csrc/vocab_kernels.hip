@@ -367,8 +367,8 @@ constexpr int ring_bytes() {  // copies of 8 rows (1 KB), as many by each wave
 // 192 x 320 and 128 x 384, 8 and 10 bytes, gain 13% at best and lose elsewhere.
 //
 // `block` and the grid it belongs to may be a part of the launch's.
-template <int MODE, int BN, int BM, int WN, int WM, int S>
-__device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_t* smem) {
+template <int MODE, int BN, int BM, int WN, int WM, int S, bool HINT>
+__device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, uint8_t* smem) {
   constexpr bool TA = MODE == kDX || MODE == kDW, TB = MODE == kDW;
   constexpr int NW = WN * WM, KS = 64;
   constexpr int WTN = BN / WN, WTM = BM / WM, FN = WTN / 16, FM = WTM / 16;
@@ -500,7 +500,7 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
         if (a >= left) vo[e] = kBig - 1024u * (uint32_t)e;
       }
     }
-    if constexpr (MODE != kDW && BM <= 128) {
+    if constexpr (MODE != kDW && HINT) {
       if (isA && stream) {
         if (cnt == 4) dma_group<4, true>(lds, vo, r, soff);
         else if (cnt == 3) dma_group<3, true>(lds, vo, r, soff);
@@ -805,6 +805,20 @@ __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_
     // (the branch around the loop: around the store the two are merged, without nt)
     if (MODE == kDW && stream) all_out(std::true_type{});
     else all_out(std::false_type{});
+  }
+}
+
+// Copies that may carry the non-temporal hint take a branch each: tiles of 256 tokens have a body with
+// it for where one holds all that count (200 tokens of 131072 ids, 3584 wide, 239 -> 230 us, their
+// gradient 794 -> 768), and one without (4096 tokens: 1% faster).
+template <int MODE, int BN, int BM, int WN, int WM, int S>
+__device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_t* smem) {
+  if constexpr (MODE == kDW || BM <= 128) {
+    vocab_tile_body<MODE, BN, BM, WN, WM, S, true>(p, block, smem);
+  } else {
+    const int nv = *p.nv, rows = MODE == kDX && nv <= p.twice ? 2 * nv : nv;
+    if (p.stream && rows <= BM) vocab_tile_body<MODE, BN, BM, WN, WM, S, true>(p, block, smem);
+    else vocab_tile_body<MODE, BN, BM, WN, WM, S, false>(p, block, smem);
   }
 }
 
