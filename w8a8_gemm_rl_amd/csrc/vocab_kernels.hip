@@ -305,7 +305,8 @@ struct VocabTile {
   // tile holds all tokens that count: nothing of W is read again, and dW is written to be read later (us
   // with / without, 3584 wide, W past the MALL or not there yet): logp 1 x 131072 145 / 164, 128 x
   // 131072 166 / 181, 1 x 32768 45 / 50; gradient 1 x 131072 466 / 575, 33 x 32768 148 / 183. kGrad reads
-  // without it where kDX will find W in the MALL (33 x 32768: 3 us).
+  // without it where kDX will find W in the MALL (33 x 32768: 3 us), kDX where it finds it in the L2s
+  // (gradient, 200 tokens, 3584 wide or 1808: 10000 ids 108 / 110, 5000 68 / 70, 4112 x 1808 50 / 46).
   bool stream;
   int twice;       // up to so many compact tokens G is held in two parts
 };
@@ -983,7 +984,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 constexpr int64_t kMaxBlocks = (int64_t)1 << 21;
-constexpr int64_t kMall = (int64_t)256 << 20;
+constexpr int64_t kMall = (int64_t)256 << 20, kL2s = (int64_t)32 << 20;
 
 int64_t grad_rows(int64_t M) { return M <= kTwice ? 2 * M : (M < 2 * kTwice ? 2 * kTwice : M); }
 
@@ -1289,7 +1290,8 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     x.ext_a = y.ext_a = p.K;
     x.out32 = at<float>(ws, w.dx);
     x.add = id0 > 0;
-    x.stream = y.stream = true;
+    x.stream = ids * p.K * 2 > kL2s;
+    y.stream = true;
     y.A = at<uint16_t>(ws, w.xc);
     y.lda = p.K;
     y.out16 = p.dW + (p.dW ? id0 * p.lddw : 0);
