@@ -811,6 +811,8 @@ def _head_args(X, W):
     """(M, N, K, row strides) of bf16 hidden states X [M, K] and head W [N, K]."""
     if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
         raise ValueError("X and W must be bfloat16")
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be 2-D")
     ldx, ldw = _ld(X, "X"), _ld(W, "W")
     if W.shape[1] != X.shape[1]:
         raise ValueError("X and W disagree on K")
