@@ -46,3 +46,28 @@ def test_abi_tests_under_host_sanitizers():
     assert r.returncode == 0, out[-4000:]
     assert "AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
     assert " passed" in out
+
+
+def test_vocabulary_losses_under_host_sanitizers():
+    """The same for the losses over a vocabulary: refusals, workspace sizes and plans."""
+    from w8a8_gemm_rl_amd import build
+
+    sources = [os.path.join(d, f) for d in (build.CSRC, os.path.join(ROOT, "include")) for f in os.listdir(d)]
+    lib = build.SAN_LIB
+    if not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(f) for f in sources):
+        lib = build.build_sanitized()
+    env = dict(os.environ,
+               LD_PRELOAD=build.sanitizer_runtime(),
+               ASAN_OPTIONS="detect_leaks=0:halt_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1",
+               QR_LIB_PATH=lib)
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider",
+                        os.path.join(ROOT, "tests", "test_oracle_vocab.py"),
+                        os.path.join(ROOT, "tests", "test_vocab_host.py"),
+                        "-k", "refusals or workspace or plans or matrices"],
+                       env=env, cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                       text=True, timeout=900)
+    out = r.stdout
+    assert r.returncode == 0, out[-4000:]
+    assert "AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
+    assert "8 passed" in out, out[-4000:]

@@ -16,3 +16,24 @@ def test_hidden_states_and_head_are_matrices():
                  (X, W.new_zeros((100, 64, 64))), (X, W.view(-1)), (X.new_zeros(()), W)):
         with pytest.raises(ValueError):
             B._head_args(x, w)
+
+
+def test_workspaces_up_to_the_limits():
+    """Sizes and plans over the whole documented range: room for the copied rows of X at least (twice
+    over where G may be in two parts), the list's tables, and the gradient's piece and sums of dX."""
+    r = torch.Generator().manual_seed(3)
+    shapes = [(1 << 22, (1 << 22) - 1, 1 << 16, 1024), (1 << 22, 1, 8, 1), (1, (1 << 22) - 1, 1 << 16, 1024),
+              (1, 1, 8, 1), (128, 100, 8, 7), (129, 100, 8, 7)]
+    for _ in range(3000):
+        u = torch.rand(4, generator=r)
+        shapes.append((int(2 ** (22 * u[0])), min(int(2 ** (22 * u[1])), (1 << 22) - 1),
+                       max(8, int(2 ** (16 * u[2])) // 8 * 8), int(2 ** (10 * u[3]))))
+    for M, N, K, L in shapes:
+        piece = B.vocab_plan(M, N, K)[3]
+        rows = 2 * M if M <= 128 else M
+        assert 1 <= piece <= N and (piece == N or piece >= 4096)
+        for fn, entries in (("qr_vocab_logp", 1), ("qr_vocab_distill", L)):
+            size = B.workspace_size(fn, M, N, K, entries)
+            assert size >= 2 * M * K + 8 * M * entries and size % 256 == 0
+            size = B.workspace_size(fn + "_grad", M, N, K, entries)
+            assert size >= rows * (2 * K + 2 * piece + 4 * K) + 4 * M * entries and size % 256 == 0
