@@ -1,5 +1,5 @@
 """GPU tests of the losses over a vocabulary that hold more than their general bounds (those of
-test_gpu_vocab.py, whose u = 2^-24 and helpers are used here)."""
+test_gpu_vocab.py; u = 2^-24, half a step of fp32)."""
 
 import numpy as np
 import pytest
@@ -8,7 +8,8 @@ import torch
 from w8a8_gemm_rl_amd import binding as B
 
 from gpu_helpers import DEV
-from test_gpu_vocab import U
+import vocab_bounds as V
+from vocab_bounds import U
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,68 @@ def test_logp_of_certain_ids_is_never_positive(M, N, K, scale, top):
     assert bool((got <= 0).all()), float(got.max())
     assert bool(((got - want).abs() <= lim).all()), float(((got - want).abs() - lim).max())
     assert torch.equal(loss, -logp)
+
+
+def _gradients(M, N, K, live, L, seed, dtype="fp32", scale=1.0, need_dX=True, need_dW=True):
+    """Both calls of a problem of which `live` tokens count, held to the bounds for as many parts of G as
+    the header promises. Masked rows of X hold NaN, as do their lse and incoming gradients."""
+    r = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, K), generator=r).to(torch.bfloat16).to(DEV)
+    w = (torch.randn((N, K), generator=r) * (2.0 / K ** 0.5)).to(torch.bfloat16).to(DEV)
+    g = torch.randn(M, generator=r).to(DEV)
+    on = torch.zeros(M, dtype=torch.bool)
+    on[torch.randperm(M, generator=r)[:live]] = True
+    on = on.to(DEV)
+    n = max(L, 1)
+    ids = torch.randint(0, N, (M, n), generator=r).to(DEV)
+    ids[:, 0] = torch.randint(0, N, (M,), generator=r).to(DEV)
+    ids[~on] = -1
+    X = x.clone()
+    X[~on] = float("nan")
+    kw = dict(scale=scale)
+    e_p = 0.0
+    if L:
+        teacher = (torch.randn((M, n), generator=r) * 2).to(torch.float32 if dtype == "fp32" else torch.bfloat16)
+        teacher = teacher.to(DEV)
+        kw.update(index=ids, teacher=teacher)
+        _, lse = B.vocab_distill(X, w, **kw)
+        y = float(scale) * teacher.double()
+        p = torch.softmax(y, 1)
+        # exp(y - top) / sum: arguments off by 3 u (|y| + |top|), the rest a few u, the sum L u
+        e_p = 2 * (6 * float(y.abs().max()) + n + 10) * U
+    else:
+        kw.update(target=ids[:, 0].contiguous())
+        _, lse = B.vocab_logp(X, w, **kw)
+        p = torch.ones((M, 1), dtype=torch.float64, device=DEV)
+    lse, gi = lse.clone(), g.clone()
+    lse[~on] = float("nan")
+    gi[~on] = float("nan")
+    call = B.vocab_distill_grad if L else B.vocab_logp_grad
+    got = call(X, w, lse=lse, **{"dloss" if L else "dlogp": gi}, need_dX=need_dX, need_dW=need_dW, **kw)
+    i = on.nonzero()[:, 0]
+    x64, w64 = x[i].double(), w.double()
+    G, err = V.gradient_of_logits(x64, w64, ids[i], p[i], g[i].double() * scale, lse[i].double(), scale,
+                                  1.0 if L else -1.0, e_p)
+    for which, (out, (want, lim)) in enumerate(zip(got, V.gradient_bounds(x64, w64, G, err,
+                                                                          2 if live <= V.TWICE else 1))):
+        if out is None:
+            continue
+        if which == 0:
+            assert not bool(out[~on].any())
+            out = out[i]
+        bad = ~((out.double() - want).abs() <= lim)
+        assert not bool(bad.any()), ("dX", "dW")[which] + f": {int(bad.sum())}, {bad.nonzero()[:4].tolist()}"
+
+
+# (tokens, ids, hidden, tokens that count): all of them on tiles of every kind, and both sides of 128
+PARTS = [(1, 256, 64, 1), (2, 7, 16, 2), (31, 255, 56, 31), (33, 300, 128, 33), (64, 1000, 136, 64),
+         (100, 700, 200, 100), (128, 256, 264, 128), (32, 100001, 520, 32), (64, 66000, 72, 64),
+         (127, 40001, 584, 127), (60, 20001, 1160, 60), (128, 5003, 2056, 128),
+         (129, 513, 72, 129), (129, 513, 72, 128), (300, 1031, 520, 129), (300, 1031, 520, 128), (300, 1031, 520, 1),
+         (700, 40300, 72, 129), (700, 40300, 72, 128), (1000, 3001, 264, 65), (2000, 20001, 136, 33)]
+
+
+@pytest.mark.parametrize("M,N,K,live", PARTS)
+@pytest.mark.parametrize("L,dtype", [(0, "fp32"), (6, "fp32"), (6, "bf16")])
+def test_gradients_to_the_parts_of_G(M, N, K, live, L, dtype):
+    _gradients(M, N, K, live, L, seed=M + N + K + live, dtype=dtype, scale=0.75 if L else 1.0)

@@ -6,6 +6,8 @@ import torch
 
 from w8a8_gemm_rl_amd import binding as B
 
+import vocab_bounds as V
+
 
 def test_hidden_states_and_head_are_matrices():
     """Contiguous tensors of other ranks, whose second size may well agree with the head's."""
@@ -37,3 +39,29 @@ def test_workspaces_up_to_the_limits():
             assert size >= 2 * M * K + 8 * M * entries and size % 256 == 0
             size = B.workspace_size(fn + "_grad", M, N, K, entries)
             assert size >= rows * (2 * K + 2 * piece + 4 * K) + 4 * M * entries and size % 256 == 0
+
+
+def _problem(M, N, K, L, seed):
+    """(x, w, ids, p, a, lse) in float64, of values that bf16 holds."""
+    r = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, K), generator=r).bfloat16().double()
+    w = (torch.randn((N, K), generator=r) * (2 / K ** 0.5)).bfloat16().double()
+    ids = torch.stack([torch.randperm(N, generator=r)[:L] for _ in range(M)])
+    p = torch.softmax(torch.randn((M, L), generator=r).double() * 2, 1)
+    return x, w, ids, p, torch.randn(M, generator=r).double(), torch.logsumexp(x @ w.T, 1)
+
+
+@pytest.mark.parametrize("M,N,K,L", [(1, 256, 64, 1), (31, 255, 56, 1), (64, 1000, 136, 5), (100, 700, 200, 1),
+                                     (128, 256, 264, 5), (128, 2003, 72, 20)])
+def test_bounds_of_the_gradients_see_a_lost_part(M, N, K, L):
+    """Gradients from G in two parts are within the bounds for two, those from G in one part are not, in
+    dX and in dW; within the bounds for one part they are."""
+    x, w, ids, p, a, lse = _problem(M, N, K, L, M + N)
+    G, err = V.gradient_of_logits(x, w, ids, p, a, lse, 1.0, 1.0)
+    hi = G.float().bfloat16()
+    lo = (G.float() - hi.float()).bfloat16().double()
+    one, two = hi.double(), hi.double() + lo
+    for parts, H, ok in ((2, two, True), (1, one, True), (2, one, False)):
+        for got, (want, lim) in zip((H @ w, H.T @ x), V.gradient_bounds(x, w, G, err, parts)):
+            bad = int(((got.float().bfloat16().double() - want).abs() > lim).sum())
+            assert (bad == 0) == ok, (parts, ok, bad, got.numel())
