@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from w8a8_gemm_rl_amd import binding as B
 
 from gpu_helpers import DEV
@@ -119,3 +120,76 @@ PARTS = [(1, 256, 64, 1), (2, 7, 16, 2), (31, 255, 56, 31), (33, 300, 128, 33), 
 @pytest.mark.parametrize("L,dtype", [(0, "fp32"), (6, "fp32"), (6, "bf16")])
 def test_gradients_to_the_parts_of_G(M, N, K, live, L, dtype):
     _gradients(M, N, K, live, L, seed=M + N + K + live, dtype=dtype, scale=0.75 if L else 1.0)
+
+
+def _value_errors(X, W, lists):
+    """Bound of each token's loss: that of test_gpu_vocab.py (logits twice, the sum, the weights)."""
+    K = X.shape[1]
+    z, lse = O.vocab_logits(X, W, 1.0)
+    value, _ = O.vocab_loss(X, W, **lists)
+    ids, p, _ = O.vocab_lists(scale=1.0, N=W.shape[0], **lists)
+    e = (np.abs(X) @ np.abs(W).T * (2 * K + 2) * U).max(axis=1)
+    e_lse = e + (4 * np.abs(z).max(axis=1) + 600) * U + np.abs(lse) * U
+    if "target" in lists:
+        return e + e_lse + np.abs(value) * U
+    e_p = 2 * (6 * np.abs(lists["teacher"]).max() + ids.shape[1] + 10) * U
+    zi = np.take_along_axis(z, ids, axis=1) - lse[:, None]
+    return (p * (e + e_lse)[:, None] + p * (np.abs(np.log(p)) + np.abs(zi) + 1) * (e_p + 8 * U)).sum(axis=1) \
+        + np.abs(value) * U
+
+
+@pytest.mark.parametrize("M", [24, 160])
+@pytest.mark.parametrize("L", [0, 4])
+@pytest.mark.parametrize("which", ["dX", "dW"])
+def test_gradients_against_differences_of_the_calls(which, L, M):
+    """The calls' own losses at hidden states or weights shifted by +-h along D, D the signs of some of the
+    gradient's entries: (f(+h) - f(-h)) / 2 h against <gradient, D>. Allowed: what the difference quotient
+    itself is off by (from the oracle's in float64), the losses' errors over h, the gradient's bounds;
+    in all less than a twentieth of <gradient, D>, so that a gradient that is lost, negated, doubled or
+    off by a tenth fails."""
+    N, K = 300, 64
+    h = 1.0 / 8 if which == "dX" else 1.0 / 32  # losses bend less along D of X
+    r = np.random.default_rng(M + L)
+    X = np.round(r.standard_normal((M, K)).clip(-3.5, 3.5) * 32) / 32   # shifts by h stay exact in bf16
+    W = np.round(r.standard_normal((N, K)) * 0.25 * 64) / 64
+    if L:
+        teacher = (r.standard_normal((M, L)) * 2).astype(np.float32).astype(np.float64)
+        lists = dict(index=np.stack([r.permutation(N)[:L] for _ in range(M)]), teacher=teacher)
+        dev = dict(index=torch.from_numpy(lists["index"]).to(DEV), teacher=torch.from_numpy(teacher).float().to(DEV))
+    else:
+        lists = dict(target=r.integers(0, N, M))
+        dev = dict(target=torch.from_numpy(lists["target"]).to(DEV))
+    g = r.choice([-1.0, -0.5, 0.5, 1.0], M)
+
+    def bf16(a):
+        t = torch.from_numpy(a).to(torch.bfloat16)
+        assert np.array_equal(t.double().numpy(), a)
+        return t.to(DEV)
+
+    def both(s, D):
+        x, w = (X + s * D, W) if which == "dX" else (X, W + s * D)
+        value, lse = (B.vocab_distill if L else B.vocab_logp)(bf16(x), bf16(w), **dev)
+        return float((value.double().cpu().numpy() * g).sum()), O.vocab_loss(x, w, **lists)[0] @ g, lse, \
+            float((_value_errors(x, w, lists) * np.abs(g)).sum())
+
+    lse = both(0.0, 0.0)[2]
+    call = B.vocab_distill_grad if L else B.vocab_logp_grad
+    grads = call(bf16(X), bf16(W), lse=lse, **{"dloss" if L else "dlogp": torch.from_numpy(g).float().to(DEV)}, **dev)
+    grad = grads[0 if which == "dX" else 1].double().cpu().numpy()
+    ids, p, _ = O.vocab_lists(scale=1.0, N=N, **lists)
+    x, w = torch.from_numpy(X), torch.from_numpy(W)
+    e_p = 2 * (6 * float(np.abs(lists["teacher"]).max()) + L + 10) * U if L else 0.0
+    G, err = V.gradient_of_logits(x, w, torch.from_numpy(ids), torch.from_numpy(p), torch.from_numpy(g),
+                                  lse.double().cpu(), 1.0, 1.0 if L else -1.0, e_p)
+    exact, lim = (t.numpy() for t in V.gradient_bounds(x, w, G, err, 2 if M <= V.TWICE else 1)[which == "dW"])
+    order = np.argsort(-np.abs(exact).ravel())
+    for some in (order[:40], order[40:400:7]):
+        D = np.zeros(exact.size)
+        D[some] = np.sign(exact.ravel()[some])
+        D = D.reshape(exact.shape)
+        up, up64, _, e_up = both(h, D)
+        down, down64, _, e_down = both(-h, D)
+        size = float((exact * D).sum())
+        slack = abs((up64 - down64) / (2 * h) - size) + (e_up + e_down) / (2 * h) + float((lim * np.abs(D)).sum())
+        assert slack < size / 20, (slack, size)
+        assert abs((up - down) / (2 * h) - float((grad * D).sum())) <= slack
