@@ -11,6 +11,7 @@ from w8a8_gemm_rl_amd import binding as B
 from gpu_helpers import DEV
 import vocab_bounds as V
 from vocab_bounds import U
+from vocab_shapes import STREAMED, TILES
 
 pytestmark = pytest.mark.gpu
 
@@ -57,9 +58,10 @@ def test_logp_of_certain_ids_is_never_positive(M, N, K, scale, top):
     assert torch.equal(loss, -logp)
 
 
-def _gradients(M, N, K, live, L, seed, dtype="fp32", scale=1.0, need_dX=True, need_dW=True):
-    """Both calls of a problem of which `live` tokens count, held to the bounds for as many parts of G as
-    the header promises. Masked rows of X hold NaN, as do their lse and incoming gradients."""
+def _calls(M, N, K, live, L, seed, dtype="fp32", scale=1.0, needs=((True, True),)):
+    """The calls of a problem of which `live` tokens count, gradients as in each of `needs` (dX, dW), held
+    to the bounds: of the losses those of test_gpu_vocab.py, of the gradients those for as many parts of G
+    as the header promises. Masked rows of X hold NaN, as do their lse and incoming gradients."""
     r = torch.Generator().manual_seed(seed)
     x = torch.randn((M, K), generator=r).to(torch.bfloat16).to(DEV)
     w = (torch.randn((N, K), generator=r) * (2.0 / K ** 0.5)).to(torch.bfloat16).to(DEV)
@@ -79,33 +81,46 @@ def _gradients(M, N, K, live, L, seed, dtype="fp32", scale=1.0, need_dX=True, ne
         teacher = (torch.randn((M, n), generator=r) * 2).to(torch.float32 if dtype == "fp32" else torch.bfloat16)
         teacher = teacher.to(DEV)
         kw.update(index=ids, teacher=teacher)
-        _, lse = B.vocab_distill(X, w, **kw)
+        value, lse = B.vocab_distill(X, w, **kw)
         y = float(scale) * teacher.double()
         p = torch.softmax(y, 1)
         # exp(y - top) / sum: arguments off by 3 u (|y| + |top|), the rest a few u, the sum L u
         e_p = 2 * (6 * float(y.abs().max()) + n + 10) * U
     else:
         kw.update(target=ids[:, 0].contiguous())
-        _, lse = B.vocab_logp(X, w, **kw)
+        value, lse = B.vocab_logp(X, w, **kw)
         p = torch.ones((M, 1), dtype=torch.float64, device=DEV)
+    i = on.nonzero()[:, 0]
+    assert not bool(value[~on].any()) and not bool(lse[~on].any())
+    x64, w64, p, ids = x[i].double(), w.double(), p[i], ids[i]
+    z = scale * (x64 @ w64.T)
+    l64 = torch.logsumexp(z, 1)
+    e = scale * (x64.abs() @ w64.abs().T).amax(1) * ((2 * K + 2) * U)
+    e_lse = e + (4 * z.abs().amax(1) + 600) * U + l64.abs() * U
+    assert bool(((lse[i].double() - l64).abs() <= e_lse).all())
+    zi = z.gather(1, ids) - l64[:, None]
+    want = (p * (p.log() - zi)).sum(1) if L else zi[:, 0]
+    lim = (p * ((e + e_lse)[:, None] + (p.log().abs() + zi.abs() + 1) * (e_p + 8 * U))).sum(1) + want.abs() * U
+    assert bool(((value[i].double() - want).abs() <= lim).all())
+    del z
     lse, gi = lse.clone(), g.clone()
     lse[~on] = float("nan")
     gi[~on] = float("nan")
     call = B.vocab_distill_grad if L else B.vocab_logp_grad
-    got = call(X, w, lse=lse, **{"dloss" if L else "dlogp": gi}, need_dX=need_dX, need_dW=need_dW, **kw)
-    i = on.nonzero()[:, 0]
-    x64, w64 = x[i].double(), w.double()
-    G, err = V.gradient_of_logits(x64, w64, ids[i], p[i], g[i].double() * scale, lse[i].double(), scale,
+    G, err = V.gradient_of_logits(x64, w64, ids, p, g[i].double() * scale, lse[i].double(), scale,
                                   1.0 if L else -1.0, e_p)
-    for which, (out, (want, lim)) in enumerate(zip(got, V.gradient_bounds(x64, w64, G, err,
-                                                                          2 if live <= V.TWICE else 1))):
-        if out is None:
-            continue
-        if which == 0:
-            assert not bool(out[~on].any())
-            out = out[i]
-        bad = ~((out.double() - want).abs() <= lim)
-        assert not bool(bad.any()), ("dX", "dW")[which] + f": {int(bad.sum())}, {bad.nonzero()[:4].tolist()}"
+    bounds = V.gradient_bounds(x64, w64, G, err, 2 if live <= V.TWICE else 1)
+    for need in needs:
+        got = call(X, w, lse=lse, **{"dloss" if L else "dlogp": gi}, need_dX=need[0], need_dW=need[1], **kw)
+        for name, out, (want, lim) in zip(("dX", "dW"), got, bounds):
+            assert (out is not None) == need[name == "dW"]
+            if out is None:
+                continue
+            if name == "dX":
+                assert not bool(out[~on].any())
+                out = out[i]
+            bad = ~((out.double() - want).abs() <= lim)
+            assert not bool(bad.any()), (name, need, int(bad.sum()), bad.nonzero()[:4].tolist())
 
 
 # (tokens, ids, hidden, tokens that count): all of them on tiles of every kind, and both sides of 128
@@ -119,7 +134,15 @@ PARTS = [(1, 256, 64, 1), (2, 7, 16, 2), (31, 255, 56, 31), (33, 300, 128, 33), 
 @pytest.mark.parametrize("M,N,K,live", PARTS)
 @pytest.mark.parametrize("L,dtype", [(0, "fp32"), (6, "fp32"), (6, "bf16")])
 def test_gradients_to_the_parts_of_G(M, N, K, live, L, dtype):
-    _gradients(M, N, K, live, L, seed=M + N + K + live, dtype=dtype, scale=0.75 if L else 1.0)
+    _calls(M, N, K, live, L, seed=M + N + K + live, dtype=dtype, scale=0.75 if L else 1.0)
+
+
+@pytest.mark.parametrize("M,N,K,live", TILES + STREAMED)
+@pytest.mark.parametrize("L", [0, 6])
+def test_every_body_at_its_edges(M, N, K, live, L):
+    """Each tile with few K steps and last tiles of one id or token, with both gradients or one: without
+    dX the logits' second pass, too, reads W past the caches."""
+    _calls(M, N, K, live, L, seed=M + N + K, needs=((True, True), (True, False), (False, True)))
 
 
 def _value_errors(X, W, lists):

@@ -1,12 +1,15 @@
 """Host side of the losses over a vocabulary: what the binding refuses before any device is looked at,
 and that the bounds of the GPU tests can fail (CPU)."""
 
+import random
+
 import pytest
 import torch
 
 from w8a8_gemm_rl_amd import binding as B
 
 import vocab_bounds as V
+import vocab_shapes as S
 
 
 def test_hidden_states_and_head_are_matrices():
@@ -65,3 +68,21 @@ def test_bounds_of_the_gradients_see_a_lost_part(M, N, K, L):
         for got, (want, lim) in zip((H @ w, H.T @ x), V.gradient_bounds(x, w, G, err, parts)):
             bad = int(((got.float().bfloat16().double() - want).abs() > lim).sum())
             assert (bad == 0) == ok, (parts, ok, bad, got.numel())
+
+
+def test_gpu_tests_run_every_body():
+    """What calls of a sweep of shapes and masks run on, the GPU tests' shapes run: tiles, the choice
+    among them that is left to the GPU, and the hint, each with both gradients or one."""
+    kinds = [(True, True), (True, False), (False, True)]
+    run = {b for s in S.TILES + S.STREAMED for k in kinds for b in S.bodies(B.vocab_plan, *s, *k)}
+    r = random.Random(5)
+    met = set()
+    for _ in range(20000):
+        M, N = int(2 ** r.uniform(0, 13)), int(2 ** r.uniform(0, 18))
+        K = max(8, int(2 ** r.uniform(3, 13)) // 8 * 8)
+        live = r.choice([M, M, r.randint(0, M), min(M, r.randint(0, 300))])
+        met |= {b for k in kinds for b in S.bodies(B.vocab_plan, M, N, K, live, *k)}
+    assert met <= run, sorted(met - run)
+    for what in ("sums", "G"):  # every tile, with the hint and without
+        tiles = {b for b in run if b[0].startswith(what)}
+        assert len(tiles) == 16

@@ -9,3 +9,48 @@ SMALL = [(1, 1, 8), (1, 256, 64), (2, 7, 16), (31, 255, 56), (32, 257, 72), (33,
 # enough ids for the wide tiles, each with a last tile that is not whole
 LARGE = [(32, 100001, 520), (64, 66000, 72), (127, 40001, 584), (129, 70000, 264), (500, 70001, 520),
          (700, 40300, 648), (60, 20001, 1160), (128, 5003, 2056), (1000, 3001, 264)]
+
+# every tile of the logits with few K steps (one, two, five or nine copies of 64) and a last tile of one id or
+# one short, one token, one short or whole; the last member: tokens that count
+TILES = [(31, 255, 72, 31), (63, 257, 8, 63), (33, 255, 520, 33),
+         (63, 16385, 8, 63), (65, 11263, 72, 65), (128, 8447, 520, 128),
+         (127, 16385, 8, 127), (129, 13311, 264, 129), (640, 3327, 72, 640), (639, 3327, 520, 639),
+         (31, 32769, 8, 31), (65, 17407, 72, 65), (32, 33791, 520, 32),
+         (63, 32769, 8, 63), (129, 17407, 72, 129), (64, 33791, 520, 64),
+         (127, 32769, 8, 127), (129, 26623, 72, 129), (128, 32769, 264, 128), (639, 6655, 520, 639),
+         (255, 32769, 8, 255), (257, 26623, 72, 257), (256, 33791, 520, 256), (300, 40001, 136, 127),
+         (300, 40001, 136, 129), (700, 40300, 72, 100), (700, 40300, 72, 300)]
+
+# heads beyond the 256 MiB up to which the logits' second pass leaves them in the cache, and beyond the 32
+# MiB up to which dX does
+STREAMED = [(33, 131001, 1032, 33), (200, 131001, 1032, 200), (200, 131001, 1032, 100), (60, 20001, 1160, 60),
+            (300, 131001, 1032, 300), (16, 131001, 1032, 16), (127, 131001, 1032, 127), (64, 131001, 1032, 64)]
+
+
+def bodies(plan, M, N, K, live, need_dX=True, need_dW=True):
+    """(product, ids, tokens or rows, hint) of the kernel bodies that a call of the losses and one of the
+    gradients run; `plan` as binding.vocab_plan. "hint": W's copies, dW's stores, leave the caches alone."""
+    def ceil(a, b):
+        return -(-a // b)
+
+    def logits(what, ids, stream):
+        bn, bm = plan(M, ids, K)[:2]
+        if bm == 256:  # where tiles of 128 tokens take fewer rounds, they run
+            a, grid = ceil(ids, 256), max(256, ceil(ceil(ids, 256) * ceil(M, 256), 8) * 8)
+            half, whole = a * ceil(live, 128), a * ceil(live, 256)
+            if half <= grid and ceil(half, 256) * 2 < ceil(whole, 256) * 3:
+                bm = 128
+            return (what + " wide", bn, bm, stream and live <= bm)
+        return (what, bn, bm, stream and live <= bm)
+
+    out = {logits("sums", N, True)}
+    dx_rows, piece = plan(M, N, K)[2:]
+    rows = 2 * live if live <= 128 else live
+    for id0 in range(0, N, piece):
+        ids = min(piece, N - id0)
+        out.add(logits("G", ids, not need_dX or ids * K * 2 > 1 << 28))
+        if need_dX:
+            out.add(("dX" if need_dW else "dX alone", 256, dx_rows, ids * K * 2 > 1 << 25 and rows <= dx_rows))
+        if need_dW:
+            out.add(("dW" if need_dX else "dW alone", 256, 256, rows <= 256))
+    return out
