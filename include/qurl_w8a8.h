@@ -253,7 +253,8 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  *   z[t,v]  = scale * sum_k X[t,k] W[v,k]     (bf16 products, fp32 sums)
  *   lse[t]  = log sum_v exp(z[t,v])            (fp32 over 256 ids, then float64)
  *
- * qr_vocab_logp -- softmax cross entropy (its negative): logp[t] = z[t, target[t]] - lse[t].
+ * qr_vocab_logp -- softmax cross entropy (its negative): logp[t] = z[t, target[t]] - lse[t],
+ *   never above 0 (formed before lse is rounded to fp32).
  *   A target outside [0, N) masks its token: logp and lse are 0 there.
  * qr_vocab_logp_grad -- with g = dlogp:
  *   G[t,v]  = scale g[t] ([v = target[t]] - exp(z[t,v] - lse[t])), in two parts of bf16 (to
@@ -275,7 +276,9 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  *   G[t,v]  = scale g[t] (P[t] exp(z[t,v] - lse[t]) - sum_j p[t,j] [v = index[t,j]]),
  *   and dX, dW from it as above.
  *
- * All results are the same bits on every run.
+ * All results are the same bits on every run. Another batch may give a token other last bits: M, N
+ * and K choose the tiles, the number of tokens that are not masked the parts of G, the tiles among
+ * them and how the sums of dX are split, whichever tokens they are and wherever they stand.
  *
  *   X        [M, ldx] bf16 hidden states, W [N, ldw] bf16 head (read); rows on 16-byte
  *            boundaries, strides at most 2^21. M at most 2^22, N in [1, 2^22 - 1], K a
@@ -288,7 +291,8 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  *   dX       NULL or [M, lddx], dW NULL or [N, lddw] bf16 (written, not accumulated); one
  *            of them at least.
  *   workspace  qr_workspace_size(fn, M, N, K, L) bytes (L is ignored for the logp
- *            functions), 256-byte aligned, contents irrelevant.
+ *            functions), 256-byte aligned, contents irrelevant; a gradient's is the
+ *            same for dX, dW or both.
  * Hidden states of tokens that are not masked, weights and teacher logits (but for -inf)
  * must be finite: else the results of that token, and gradients, are unspecified.
  */

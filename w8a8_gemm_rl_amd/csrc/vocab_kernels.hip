@@ -266,10 +266,15 @@ __global__ __launch_bounds__(256) void vocab_gather_kernel(const VocabCompact p)
 // ---------------------------------------------------------------------------
 enum { kSums, kGrad, kDX, kDW };
 
-// Up to so many tokens that count G is held in two parts of bf16: relative errors of the
-// gradients are 0.0017 then (their own rounding), 0.0024 with one part. While memory bounds the products
-// that is cheap, at most 30% at 128 tokens of 131072 ids, 3584 wide (780 and 600 us); 14% at
-// 33 of 32768 (160 and 141), nothing at 1; beyond, the products would take twice as long.
+// Up to so many tokens that count G is held in two parts of bf16, which leave the gradients no error but
+// their own rounding: 0.0017 of them against float64, in norm, as the plain fp32 form's. In one part it is
+// 0.0023 - 0.0024: one rounding more of the size of the results' own (2^-8 of an element at most),
+// to nearest and element by element, so it does not grow with the ids or tokens that are added up; a
+// trainer that keeps its logits' gradient in bf16 rounds at the same place. The matrix cores take bf16 or less
+// (fp16 would lose G's range), so a second part is a second product: us in one part and in two, 32768 ids,
+// 3584 wide, 1 token 123 and 123, 33 130 and 143, 128 176 and 212; 131072 ids, 128 584 and 741, 256 795
+// and 1191, 1024 2415 and 4000, 4096 9048 and 15265. Up to 128 tokens memory hides most of it;
+// beyond, it would cost half the gradient's time and more.
 constexpr int kTwice = 128;
 
 // Lambdas of a kernel share its state in registers only where they are inlined.
@@ -784,7 +789,7 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
         if constexpr (MODE == kGrad) {
           // G in fp32. The matrix cores take bf16: up to `twice` tokens G is held in two parts
           // (its rounding to bf16 and what that left: 2^-16 of each element); beyond, rounded
-          // once (2^-8 of each, as much as the rounding of the results).
+          // once (2^-8 of each, as much as the rounding of the results; why, at kTwice).
           if constexpr (!EARLY) token(j);
           float gt = 0.0f, ga = 0.0f, l2 = 0.0f;
           if (tok[j] >= 0) {
@@ -1311,6 +1316,11 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (p.dX) {
+    // Waves for the splits where all tokens count. Where few of many do, the GPU takes more splits and a wave
+    // adds up as many as 128 sums (gradient of 131072 ids, 1024 wide, 5 tokens alone 2 x 64 sums on eight
+    // waves; 5 of 4096 229 us, with eight waves 215), but waves that a launch has for that case only cost more
+    // than they save where all count (4096 tokens of 5000 ids, 3584 wide, 405 -> 426 us, 2048, 1024 wide,
+    // 95 -> 98), and sums read 16 or 32 at once gain nothing (229 -> 226 - 232).
     const int splits = w.sums.splits(rows);
     const int waves = splits <= 4 ? 1 : splits <= 4 * kDxWaves ? (splits + 3) / 4 : kDxWaves;
     hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M, (unsigned)ceil_div(p.K, 256)), dim3(64, (unsigned)waves),
