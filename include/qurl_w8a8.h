@@ -257,11 +257,14 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  *   never above 0 (formed before lse is rounded to fp32).
  *   A target outside [0, N) masks its token: logp and lse are 0 there.
  * qr_vocab_logp_grad -- with g = dlogp:
- *   G[t,v]  = scale g[t] ([v = target[t]] - exp(z[t,v] - lse[t])), in two parts of bf16 (to
- *             2^-16) where at most 128 tokens are not masked, else rounded to bf16
+ *   G[t,v]  = scale g[t] ([v = target[t]] - exp(z[t,v] - lse[t]))
  *   dX[t,:] = bf16_rne(sum_v G[t,v] W[v,:]),  dW[v,:] = bf16_rne(sum_t G[t,v] X[t,:])
- *   (fp32 sums). Masked tokens: a zero row of dX, no part in dW, whatever X, lse and
- *   g hold there.
+ *   (fp32 sums). Masked tokens: a zero row of dX, no part in dW, whatever X, lse and g hold
+ *   there.
+ *   Where at most 128 tokens are not masked, G is held in two parts of bf16 (to 2^-16 of each
+ *   element). For more, the products are in fp16: G over scale g P (P below; 1 here) to 2^-11
+ *   of itself or 2^-39; W exactly down to 2^-28 of its largest value, to 2^-38 of that below;
+ *   scale g P X to 2^-11 of itself or 2^-39 of its largest value.
  *
  * qr_vocab_distill -- divergence from a teacher whose top logits are known. Entry j of
  *   token t is the id index[t,j] with the teacher's logit teacher[t,j]; ids outside
@@ -277,17 +280,19 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  *   and dX, dW from it as above.
  *
  * All results are the same bits on every run. Another batch may give a token other last bits: M, N
- * and K choose the tiles, the number of tokens that are not masked the parts of G, the tiles among
+ * and K choose the tiles, the number of tokens that are not masked what G is held in, the tiles among
  * them and how the sums of dX are split, whichever tokens they are and wherever they stand.
  *
  *   X        [M, ldx] bf16 hidden states, W [N, ldw] bf16 head (read); rows on 16-byte
  *            boundaries, strides at most 2^21. M at most 2^22, N in [1, 2^22 - 1], K a
  *            multiple of 8 in [8, 65536].
- *   scale    finite, > 0: the logits' scale, 1 / temperature (scaled logits stay in fp32's
- *            range; scaled teacher logits below it count as -inf).
+ *   scale    finite, > 0: the logits' scale, 1 / temperature (scaled logits, and scale
+ *            times an incoming gradient, stay in fp32's range; scaled teacher logits below it
+ *            count as -inf).
  *   target   [M] int64;  index [M, L] int64, 1 <= L <= 1024;  teacher [M, L] fp32
  *            (teacher_bf16 = 0) or bf16 (1);  teacher_lse NULL or [M] fp32 (read).
- *   logp, loss, lse  [M] fp32 (written). The gradients read the lse of their forward call.
+ *   logp, loss, lse  [M] fp32 (written). The gradients read the lse of their forward call
+ *            (an exponential of 4 or more is beyond their fp16).
  *   dX       NULL or [M, lddx], dW NULL or [N, lddw] bf16 (written, not accumulated); one
  *            of them at least.
  *   workspace  qr_workspace_size(fn, M, N, K, L) bytes (L is ignored for the logp

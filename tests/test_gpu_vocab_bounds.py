@@ -11,7 +11,7 @@ from w8a8_gemm_rl_amd import binding as B
 from gpu_helpers import DEV
 import vocab_bounds as V
 from vocab_bounds import U
-from vocab_shapes import STREAMED, TILES
+from vocab_shapes import HALF, STREAMED, TILES, TWICE
 
 pytestmark = pytest.mark.gpu
 
@@ -60,8 +60,8 @@ def test_logp_of_certain_ids_is_never_positive(M, N, K, scale, top):
 
 def _calls(M, N, K, live, L, seed, dtype="fp32", scale=1.0, needs=((True, True),)):
     """The calls of a problem of which `live` tokens count, gradients as in each of `needs` (dX, dW), held
-    to the bounds: of the losses those of test_gpu_vocab.py, of the gradients those for as many parts of G
-    as the header promises. Masked rows of X hold NaN, as do their lse and incoming gradients."""
+    to the bounds: of the losses those of test_gpu_vocab.py, of the gradients those of what the header says
+    that G is held as. Masked rows of X hold NaN, as do their lse and incoming gradients."""
     r = torch.Generator().manual_seed(seed)
     x = torch.randn((M, K), generator=r).to(torch.bfloat16).to(DEV)
     w = (torch.randn((N, K), generator=r) * (2.0 / K ** 0.5)).to(torch.bfloat16).to(DEV)
@@ -109,7 +109,8 @@ def _calls(M, N, K, live, L, seed, dtype="fp32", scale=1.0, needs=((True, True),
     call = B.vocab_distill_grad if L else B.vocab_logp_grad
     G, err = V.gradient_of_logits(x64, w64, ids, p, g[i].double() * scale, lse[i].double(), scale,
                                   1.0 if L else -1.0, e_p)
-    bounds = V.gradient_bounds(x64, w64, G, err, 2 if live <= V.TWICE else 1)
+    weight = None if live <= TWICE else g[i].double().abs() * scale * p.sum(1)
+    bounds = V.gradient_bounds(x64, w64, G, err, weight)
     for need in needs:
         got = call(X, w, lse=lse, **{"dloss" if L else "dlogp": gi}, need_dX=need[0], need_dW=need[1], **kw)
         for name, out, (want, lim) in zip(("dX", "dW"), got, bounds):
@@ -123,7 +124,7 @@ def _calls(M, N, K, live, L, seed, dtype="fp32", scale=1.0, needs=((True, True),
             assert not bool(bad.any()), (name, need, int(bad.sum()), bad.nonzero()[:4].tolist())
 
 
-# (tokens, ids, hidden, tokens that count): all of them on tiles of every kind, and both sides of 128
+# (tokens, ids, hidden, tokens that count): all of them on tiles of every kind, and few among others
 PARTS = [(1, 256, 64, 1), (2, 7, 16, 2), (31, 255, 56, 31), (33, 300, 128, 33), (64, 1000, 136, 64),
          (100, 700, 200, 100), (128, 256, 264, 128), (32, 100001, 520, 32), (64, 66000, 72, 64),
          (127, 40001, 584, 127), (60, 20001, 1160, 60), (128, 5003, 2056, 128),
@@ -131,13 +132,13 @@ PARTS = [(1, 256, 64, 1), (2, 7, 16, 2), (31, 255, 56, 31), (33, 300, 128, 33), 
          (700, 40300, 72, 129), (700, 40300, 72, 128), (1000, 3001, 264, 65), (2000, 20001, 136, 33)]
 
 
-@pytest.mark.parametrize("M,N,K,live", PARTS)
+@pytest.mark.parametrize("M,N,K,live", PARTS + HALF)
 @pytest.mark.parametrize("L,dtype", [(0, "fp32"), (6, "fp32"), (6, "bf16")])
-def test_gradients_to_the_parts_of_G(M, N, K, live, L, dtype):
+def test_gradients_to_what_G_is_held_as(M, N, K, live, L, dtype):
     _calls(M, N, K, live, L, seed=M + N + K + live, dtype=dtype, scale=0.75 if L else 1.0)
 
 
-@pytest.mark.parametrize("M,N,K,live", TILES + STREAMED)
+@pytest.mark.parametrize("M,N,K,live", TILES + STREAMED + HALF[:8])
 @pytest.mark.parametrize("L", [0, 6])
 def test_every_body_at_its_edges(M, N, K, live, L):
     """Each tile with few K steps and last tiles of one id or token, with both gradients or one: without
@@ -161,20 +162,20 @@ def _value_errors(X, W, lists):
         + np.abs(value) * U
 
 
-@pytest.mark.parametrize("M", [24, 160])
+@pytest.mark.parametrize("M,N,K", [(24, 300, 64), (160, 300, 64)])
 @pytest.mark.parametrize("L", [0, 4])
 @pytest.mark.parametrize("which", ["dX", "dW"])
-def test_gradients_against_differences_of_the_calls(which, L, M):
+def test_gradients_against_differences_of_the_calls(which, L, M, N, K):
     """The calls' own losses at hidden states or weights shifted by +-h along D, D the signs of some of the
     gradient's entries: (f(+h) - f(-h)) / 2 h against <gradient, D>. Allowed: what the difference quotient
-    itself is off by (from the oracle's in float64), the losses' errors over h, the gradient's bounds;
+    itself is off by (from the oracle's in float64), the losses' errors over h (but for tokens that are the
+    same at both ends: the same bits), the gradient's bounds;
     in all less than a twentieth of <gradient, D>, so that a gradient that is lost, negated, doubled or
     off by a tenth fails."""
-    N, K = 300, 64
     h = 1.0 / 8 if which == "dX" else 1.0 / 32  # losses bend less along D of X
     r = np.random.default_rng(M + L)
     X = np.round(r.standard_normal((M, K)).clip(-3.5, 3.5) * 32) / 32   # shifts by h stay exact in bf16
-    W = np.round(r.standard_normal((N, K)) * 0.25 * 64) / 64
+    W = np.round(r.standard_normal((N, K)) * (2.0 / np.sqrt(K)) * 64) / 64
     if L:
         teacher = (r.standard_normal((M, L)) * 2).astype(np.float32).astype(np.float64)
         lists = dict(index=np.stack([r.permutation(N)[:L] for _ in range(M)]), teacher=teacher)
@@ -193,9 +194,9 @@ def test_gradients_against_differences_of_the_calls(which, L, M):
         x, w = (X + s * D, W) if which == "dX" else (X, W + s * D)
         value, lse = (B.vocab_distill if L else B.vocab_logp)(bf16(x), bf16(w), **dev)
         return float((value.double().cpu().numpy() * g).sum()), O.vocab_loss(x, w, **lists)[0] @ g, lse, \
-            float((_value_errors(x, w, lists) * np.abs(g)).sum())
+            float((_value_errors(x, w, lists) * np.abs(g) * ((s * D).any(axis=1) if which == "dX" else 1.0)).sum())
 
-    lse = both(0.0, 0.0)[2]
+    lse = both(0.0, np.zeros_like(X if which == "dX" else W))[2]
     call = B.vocab_distill_grad if L else B.vocab_logp_grad
     grads = call(bf16(X), bf16(W), lse=lse, **{"dloss" if L else "dlogp": torch.from_numpy(g).float().to(DEV)}, **dev)
     grad = grads[0 if which == "dX" else 1].double().cpu().numpy()
@@ -204,7 +205,7 @@ def test_gradients_against_differences_of_the_calls(which, L, M):
     e_p = 2 * (6 * float(np.abs(lists["teacher"]).max()) + L + 10) * U if L else 0.0
     G, err = V.gradient_of_logits(x, w, torch.from_numpy(ids), torch.from_numpy(p), torch.from_numpy(g),
                                   lse.double().cpu(), 1.0, 1.0 if L else -1.0, e_p)
-    exact, lim = (t.numpy() for t in V.gradient_bounds(x, w, G, err, 2 if M <= V.TWICE else 1)[which == "dW"])
+    exact, lim = (t.numpy() for t in V.gradient_bounds(x, w, G, err)[which == "dW"])
     order = np.argsort(-np.abs(exact).ravel())
     for some in (order[:40], order[40:400:7]):
         D = np.zeros(exact.size)
@@ -216,3 +217,112 @@ def test_gradients_against_differences_of_the_calls(which, L, M):
         slack = abs((up64 - down64) / (2 * h) - size) + (e_up + e_down) / (2 * h) + float((lim * np.abs(D)).sum())
         assert slack < size / 20, (slack, size)
         assert abs((up - down) / (2 * h) - float((grad * D).sum())) <= slack
+
+
+def _fp16_case(M, N, K, seed):
+    r = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, K), generator=r)
+    w = torch.randn((N, K), generator=r) * (2.0 / K ** 0.5)
+    return x, w, torch.randn(M, generator=r), torch.randint(0, N, (M,), generator=r).to(DEV)
+
+
+def _check_fp16(x, w, g, target, scale=1.0):
+    """The gradients of log-probabilities of more than 128 tokens, all of which count, to their bounds."""
+    x, w, g = x.to(torch.bfloat16).to(DEV), w.to(torch.bfloat16).to(DEV), g.to(DEV)
+    _, lse = B.vocab_logp(x, w, target, scale=scale)
+    got = B.vocab_logp_grad(x, w, target, lse, g, scale=scale)
+    x64, w64, a = x.double(), w.double(), g.double() * scale
+    ones = torch.ones((x.shape[0], 1), dtype=torch.float64, device=DEV)
+    G, err = V.gradient_of_logits(x64, w64, target[:, None], ones, a, lse.double(), scale, -1.0)
+    for name, out, (want, lim) in zip(("dX", "dW"), got, V.gradient_bounds(x64, w64, G, err, a)):
+        bad = ~((out.double() - want).abs() <= lim)
+        assert not bool(bad.any()), (name, int(bad.sum()), bad.nonzero()[:4].tolist())
+    return got
+
+
+@pytest.mark.parametrize("x_by,w_by,g_by", [(0, -100, 0), (30, -40, 0), (-20, 8, -60), (0, 0, 90), (0, 0, -90),
+                                            (-60, 50, 30), (14, -10, 0), (60, -70, -100)])
+def test_fp16_takes_any_size_of_the_operands(x_by, w_by, g_by):
+    """Hidden states, weights and incoming gradients of other powers of two, far outside fp16's range: the
+    exponents follow the largest values, also where W has to come down (rows of X that are 0 among them). Scale times
+    gradient stays in fp32's range, as the header asks."""
+    x, w, g, target = _fp16_case(200, 700, 136, 7)
+    x[5] = 0.0
+    w[9] = 0.0
+    x, w, g = x * 2.0 ** x_by, w * 2.0 ** w_by, g * 2.0 ** g_by
+    _check_fp16(x, w, g, target, scale=2.0 ** -(x_by + w_by) if abs(x_by + w_by) < 100 else 1.0)
+
+
+def test_fp16_with_values_far_apart():
+    """Single hidden values, rows of W and incoming gradients 2^10 to 2^30 above the others; tokens whose
+    gradient is 0 or next to nothing; logits from flat to certain."""
+    x, w, g, target = _fp16_case(300, 1100, 200, 8)
+    x[:, 3] *= 2.0 ** 12
+    w[:, 3] *= 2.0 ** -14
+    w[17] *= 2.0 ** -20
+    x[40] *= 2.0 ** -16
+    g[::7] *= 2.0 ** -30
+    g[::11] = 0.0
+    g[50] *= 2.0 ** 10
+    x[100:120] *= 6.0
+    dX, _ = _check_fp16(x, w, g, target)
+    assert not bool(dX[::11].any())
+    # a token's dX does not depend on how large another's gradient is
+    g2 = g.clone()
+    g2[51] *= 2.0 ** 40
+    dX2, _ = _check_fp16(x, w, g2, target)
+    rest = torch.arange(300) != 51
+    assert torch.equal(dX[rest.to(DEV)], dX2[rest.to(DEV)])
+
+
+def test_fp16_of_unlikely_ids():
+    """Tokens that are certain of one id: what the others get, 2^-30 to 2^-60 of the token's weight, is below
+    fp16's normal numbers or 0. dX and dW within the bounds, which count 2^-39 for each."""
+    M, N, K = 160, 900, 64
+    r = torch.Generator().manual_seed(9)
+    x = torch.randn((M, K), generator=r)
+    w = torch.randn((N, K), generator=r) * 0.1
+    ids = torch.randint(0, N, (M,), generator=r)
+    x = x * 0.2 + w[ids] * (torch.rand((M, 1), generator=r) * 25 + 5) / w[ids].square().sum(1, keepdim=True)
+    target = torch.where(torch.arange(M) % 3 == 0, torch.randint(0, N, (M,), generator=r), ids).to(DEV)
+    _check_fp16(x, w, torch.randn(M, generator=r), target)
+
+
+def test_fp16_of_nothing():
+    """A head of zeros, incoming gradients of zeros, hidden states of zeros."""
+    x, w, g, target = _fp16_case(150, 300, 64, 10)
+    for a, b, c in ((x, w * 0, g), (x, w, g * 0), (x * 0, w, g)):
+        dX, dW = _check_fp16(a, b, c, target)
+        assert bool(dX.any()) == bool(b.any() and c.any()) and bool(dW.any()) == bool(a.any() and c.any())
+
+
+def test_fp16_in_a_graph_that_two_masks_replay():
+    """One captured gradient of 400 tokens, replayed with 400, 129, 128 and no tokens that count, eager calls on
+    another stream between."""
+    M, N, K = 400, 3001, 264
+    x, w, g, ids = _fp16_case(M, N, K, 11)
+    x, w, g = x.to(torch.bfloat16).to(DEV), w.to(torch.bfloat16).to(DEV), g.to(DEV)
+    targets = [torch.where(torch.arange(M, device=DEV) < n, ids, -1) for n in (400, 129, 128, 0)]
+    target = targets[0].clone()
+
+    def calls(t):
+        _, lse = B.vocab_logp(x, w, t)
+        return B.vocab_logp_grad(x, w, t, lse, g)
+
+    want = [[o.clone() for o in calls(t)] for t in targets]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        calls(target)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = calls(target)
+    for k in (1, 0, 2, 3, 0, 1):
+        target.copy_(targets[k])
+        graph.replay()
+        with torch.cuda.stream(s):
+            eager = calls(targets[k])
+        torch.cuda.synchronize()
+        for a, b, c in zip(out, want[k], eager):
+            assert torch.equal(a, b) and torch.equal(c, b), k

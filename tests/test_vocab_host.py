@@ -55,26 +55,31 @@ def _problem(M, N, K, L, seed):
 
 
 @pytest.mark.parametrize("M,N,K,L", [(1, 256, 64, 1), (31, 255, 56, 1), (64, 1000, 136, 5), (100, 700, 200, 1),
-                                     (128, 256, 264, 5), (128, 2003, 72, 20)])
-def test_bounds_of_the_gradients_see_a_lost_part(M, N, K, L):
-    """Gradients from G in two parts are within the bounds for two, those from G in one part are not, in
-    dX and in dW; within the bounds for one part they are."""
+                                     (128, 256, 264, 5), (128, 2003, 72, 20), (300, 1031, 520, 1)])
+def test_bounds_of_the_gradients_see_one_part_of_bf16(M, N, K, L):
+    """Gradients from G in two parts of bf16 and from G, X and W in fp16 are within their bounds; from G
+    in one part of bf16, as where the second were lost, they break both, in dX and in dW."""
     x, w, ids, p, a, lse = _problem(M, N, K, L, M + N)
     G, err = V.gradient_of_logits(x, w, ids, p, a, lse, 1.0, 1.0)
+    weight = a.abs() * p.sum(1)
     hi = G.float().bfloat16()
     lo = (G.float() - hi.float()).bfloat16().double()
-    one, two = hi.double(), hi.double() + lo
-    for parts, H, ok in ((2, two, True), (1, one, True), (2, one, False)):
-        for got, (want, lim) in zip((H @ w, H.T @ x), V.gradient_bounds(x, w, G, err, parts)):
-            bad = int(((got.float().bfloat16().double() - want).abs() > lim).sum())
-            assert (bad == 0) == ok, (parts, ok, bad, got.numel())
+    half = lambda t, k: (t * 2.0 ** k).float().half().double()  # noqa: E731
+    H, xf = half(G / weight[:, None], 14), x * weight[:, None]
+    kx, kw = (14 - int(torch.floor(torch.log2(t.abs().max()))) for t in (xf, w))
+    fp16 = ((H @ half(w, kw)) * weight[:, None] * 2.0 ** (-14 - kw), (H.T @ half(xf, kx)) * 2.0 ** (-14 - kx))
+    two, one = ((t @ w, t.T @ x) for t in (hi.double() + lo, hi.double()))
+    for got, kind, ok in ((two, None, True), (fp16, weight, True), (one, None, False), (one, weight, False)):
+        for g, (want, lim) in zip(got, V.gradient_bounds(x, w, G, err, kind)):
+            bad = int(((g.float().bfloat16().double() - want).abs() > lim).sum())
+            assert (bad == 0) == ok, (kind is None, ok, bad, g.numel())
 
 
 def test_gpu_tests_run_every_body():
     """What calls of a sweep of shapes and masks run on, the GPU tests' shapes run: tiles, the choice
     among them that is left to the GPU, and the hint, each with both gradients or one."""
     kinds = [(True, True), (True, False), (False, True)]
-    run = {b for s in S.TILES + S.STREAMED for k in kinds for b in S.bodies(B.vocab_plan, *s, *k)}
+    run = {b for s in S.TILES + S.STREAMED + S.HALF for k in kinds for b in S.bodies(B.vocab_plan, *s, *k)}
     r = random.Random(5)
     met = set()
     for _ in range(20000):
@@ -84,5 +89,4 @@ def test_gpu_tests_run_every_body():
         met |= {b for k in kinds for b in S.bodies(B.vocab_plan, M, N, K, live, *k)}
     assert met <= run, sorted(met - run)
     for what in ("sums", "G"):  # every tile, with the hint and without
-        tiles = {b for b in run if b[0].startswith(what)}
-        assert len(tiles) == 16
+        assert len({b[:4] for b in run if b[0].startswith(what)}) == 16

@@ -27,30 +27,45 @@ STREAMED = [(33, 131001, 1032, 33), (200, 131001, 1032, 200), (200, 131001, 1032
             (300, 131001, 1032, 300), (16, 131001, 1032, 16), (127, 131001, 1032, 127), (64, 131001, 1032, 64)]
 
 
+# more tokens than those whose G is held in two parts, on every tile, one more than a tile's among them, and
+# both sides of that number among masked ones
+HALF = [(5603, 89, 6272, 5603), (5067, 334, 1808, 5067), (5787, 377, 1408, 5787), (602, 3280, 3016, 602),
+        (1301, 6081, 480, 1301), (1260, 7826, 416, 1024), (3924, 24490, 32, 3924), (769, 10241, 1032, 769),
+        (641, 12801, 520, 641), (513, 40001, 264, 513), (1100, 3001, 1160, 128), (1100, 3001, 1160, 129),
+        (1000, 33333, 520, 128), (1000, 33333, 520, 129), (257, 100003, 392, 257), (2000, 9001, 1032, 414)]
+
+
+TWICE = 128  # tokens that count up to which a gradient holds G in two parts of bf16; beyond, in fp16
+
+
 def bodies(plan, M, N, K, live, need_dX=True, need_dW=True):
-    """(product, ids, tokens or rows, hint) of the kernel bodies that a call of the losses and one of the
-    gradients run; `plan` as binding.vocab_plan. "hint": W's copies, dW's stores, leave the caches alone."""
+    """(product, ids, tokens or rows, hint, fp16) of the kernel bodies that a call of the losses and one of
+    the gradients run; `plan` as binding.vocab_plan. "hint": W's copies, dW's stores, leave the caches alone."""
     def ceil(a, b):
         return -(-a // b)
 
-    def logits(what, ids, stream):
+    if live == 0:
+        return set()
+    half = live > TWICE
+
+    def logits(what, ids, stream, half):
         bn, bm = plan(M, ids, K)[:2]
         if bm == 256:  # where tiles of 128 tokens take fewer rounds, they run
             a, grid = ceil(ids, 256), max(256, ceil(ceil(ids, 256) * ceil(M, 256), 8) * 8)
-            half, whole = a * ceil(live, 128), a * ceil(live, 256)
-            if half <= grid and ceil(half, 256) * 2 < ceil(whole, 256) * 3:
+            part, whole = a * ceil(live, 128), a * ceil(live, 256)
+            if part <= grid and ceil(part, 256) * 2 < ceil(whole, 256) * 3:
                 bm = 128
-            return (what + " wide", bn, bm, stream and live <= bm)
-        return (what, bn, bm, stream and live <= bm)
+            what += " wide"
+        return (what, bn, bm, stream and live <= bm, half)
 
-    out = {logits("sums", N, True)}
+    out = {logits("sums", N, True, False)}
     dx_rows, piece = plan(M, N, K)[2:]
-    rows = 2 * live if live <= 128 else live
+    rows = live if half else 2 * live
     for id0 in range(0, N, piece):
         ids = min(piece, N - id0)
-        out.add(logits("G", ids, not need_dX or ids * K * 2 > 1 << 28))
+        out.add(logits("G", ids, not need_dX or ids * K * 2 > 1 << 28, half))
         if need_dX:
-            out.add(("dX" if need_dW else "dX alone", 256, dx_rows, ids * K * 2 > 1 << 25 and rows <= dx_rows))
+            out.add(("dX" if need_dW else "dX alone", 256, dx_rows, ids * K * 2 > 1 << 25 and rows <= dx_rows, half))
         if need_dW:
-            out.add(("dW" if need_dX else "dW alone", 256, 256, rows <= 256))
+            out.add(("dW", 256, 256, rows <= 256, half))
     return out

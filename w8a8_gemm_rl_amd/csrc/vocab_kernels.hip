@@ -4,6 +4,8 @@
 //   z[t,v] = c sum_k X[t,k] W[v,k],  lse[t] = log sum_v exp z[t,v]
 //   G[t,v] = a_t exp(z[t,v] - lse[t]) - sum_j b_tj [v = id_tj],  dX = G W,  dW = G^T X
 //
+// The sums and logits are products in bf16, dX and dW of G in two parts of bf16 or in fp16 (kTwice).
+//
 // A token has a list of ids with weights (one id of weight 1 for a log-probability).
 // Tokens without one are masked: the others are numbered in order ("compact" tokens,
 // their count nv known to the GPU only) and their rows of X copied together, so masked
@@ -32,10 +34,14 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453;
 constexpr int kNone = 0x7fffffff;  // list key of no entry: past every id
+
+// Lambdas of a kernel share its state in registers only where they are inlined.
+#define QR_INLINE __attribute__((always_inline))
 
 // ---------------------------------------------------------------------------
 // Lists and compact tokens
@@ -161,7 +167,16 @@ struct VocabCompact {
   const uint16_t* X;
   uint16_t* Xc;  // rows of the compact tokens; twice over where nv <= twice
   int twice;
-  DxPlan dx;  // gradients
+  // gradients
+  DxPlan dx;
+  const float *g, *mass;
+  float gscale;         // scale, with the gradient's sign
+  float *factor, *top;  // [M]: G of a compact token by its H, and the largest of its row times that
+  const uint16_t* W;
+  int64_t ldw;
+  float* peaks;
+  int peak_blocks, shift;
+  bool stream;
   int *nv, *map, *inv;  // nv: their count, and dX's splits
   float *value, *lse;  // losses: masked tokens' results
 };
@@ -171,16 +186,88 @@ __device__ __forceinline__ void vocab_count(const VocabCompact& p, int n) {
   p.nv[1] = p.dx.splits(n <= p.twice ? 2 * n : n);
 }
 
+// H, what G is held as in fp16: 2^kHalf G / (scale g P), P the weight of the token's list. |H| is at most
+// 2^kHalf; fp16 ends at 65504, so that an exponential may come out at 3.9 for 1.
+constexpr int kHalf = 14;
+constexpr int kPeaks = 2048;  // blocks that look for W's largest value, at most
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), h2));
+}
+
+__device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b) {  // of two pairs of 16 bits each
+  typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u2, a), __builtin_bit_cast(u2, b)));
+}
+
+// The largest of pairs of a block's four waves as bf16 without their signs, to all threads.
+__device__ __forceinline__ float block_top(uint32_t pair) {
+  __shared__ uint32_t tops[4];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) pair = max16(pair, __shfl_xor(pair, o, 64));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = pair;
+  __syncthreads();
+  const uint32_t m = max16(max16(tops[0], tops[1]), max16(tops[2], tops[3]));
+  return fmaxf(bf16_lo(m), bf16_hi(m));
+}
+
 // Token t (live, compact number c of n): its entries of the tables, its rows of Xc. One block.
 __device__ __forceinline__ void vocab_take_row(const VocabCompact& p, int64_t t, int c, int n) {
   const uint4* src = reinterpret_cast<const uint4*>(p.X + t * p.ldx);
   uint4* dst = reinterpret_cast<uint4*>(p.Xc + c * p.K);
   const int64_t again = n <= p.twice ? n * p.K / 8 : 0;
+  uint32_t top = 0;
   for (int64_t i = threadIdx.x; i < p.K >> 3; i += 256) {
     const uint4 v = src[i];
     dst[i] = v;
     if (again) dst[again + i] = v;
+    top = max16(max16(top, v.x & 0x7fff7fff), v.y & 0x7fff7fff);
+    top = max16(max16(top, v.z & 0x7fff7fff), v.w & 0x7fff7fff);
   }
+  if (!p.factor || n <= p.twice) return;
+  const float most = block_top(top);
+  if (threadIdx.x == 0) {
+    const float f = ldexpf(p.g[t] * p.gscale * (p.mass ? p.mass[t] : 1.0f), -kHalf);
+    p.factor[c] = f;
+    p.top[c] = fabsf(f) * most;
+  }
+}
+
+// The largest of W, for fp16 products: `block` of p.peak_blocks, rows of W 256 >> p.shift at a time. In the
+// launch that copies the tokens' rows. 131072 x 3584 takes 135 us, 7.0 TB/s, with non-temporal reads, 172
+// without; W that the MALL holds is read without, the logits find it there (gradient of 400 tokens of 5000 ids
+// 104 us, else 112).
+template <bool STREAM>
+__device__ __forceinline__ void vocab_peak(const VocabCompact& p, int block) {
+  constexpr int U = 4;
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  const int64_t step = (int64_t)p.peak_blocks * (256 >> p.shift);
+  const int c0 = threadIdx.x & ((1 << p.shift) - 1);
+  uint32_t top = 0;
+  for (int64_t r = block * (int64_t)(256 >> p.shift) + (threadIdx.x >> p.shift); r < p.N; r += U * step) {
+    for (int64_t c = c0; c < p.K >> 3; c += 1 << p.shift) {
+      u4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = r + u * step < p.N ? r + u * step : r;
+        const u4* src = reinterpret_cast<const u4*>(p.W + row * p.ldw + 8 * c);
+        v[u] = STREAM ? __builtin_nontemporal_load(src) : *src;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max16(top, v[u][e] & 0x7fff7fff);
+    }
+  }
+  const float most = block_top(top);
+  if (threadIdx.x == 0) p.peaks[block] = most;
+}
+
+__device__ __forceinline__ void vocab_peak(const VocabCompact& p, int block) {
+  if (p.stream) vocab_peak<true>(p, block);
+  else vocab_peak<false>(p, block);
 }
 
 // Compact numbers and rows in one launch, a block a token that counts the live ones itself.
@@ -209,6 +296,10 @@ __global__ __launch_bounds__(256) void vocab_compact_kernel(const VocabCompact p
   }
   const bool live = __syncthreads_or(mine);
   const int c = below[0] + below[1] + below[2] + below[3], n = all[0] + all[1] + all[2] + all[3];
+  if (t >= p.M) {
+    if (n > p.twice) vocab_peak(p, (int)(t - p.M));
+    return;
+  }
   if (threadIdx.x == 0) {
     if (t == 0) vocab_count(p, n);
     if (p.target) p.keys[t] = live ? (int)p.target[t] : kNone;
@@ -259,6 +350,60 @@ __global__ __launch_bounds__(1024) void vocab_scan_kernel(const VocabCompact p) 
 __global__ __launch_bounds__(256) void vocab_gather_kernel(const VocabCompact p) {
   const int c = blockIdx.x, n = *p.nv;
   if (c < n) vocab_take_row(p, p.map[c], c, n);
+  else if (c >= p.M && n > p.twice) vocab_peak(p, (int)(c - p.M));
+}
+
+// The power of two that brings values of up to `most` below 2^15.
+__device__ __forceinline__ int half_exponent(float most) {
+  if (!(most > 0.0f && most < INFINITY)) return 0;
+  const int e = 14 - ilogbf(most);
+  return e < 126 ? e : 126;
+}
+
+__device__ __forceinline__ float block_max(float v) {  // not negative, four waves
+  __shared__ float tops[4];
+  v = wave_max(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+}
+
+// Operands of the fp16 products: the exponents (0: W's, 1: that of X with the factors) and X with them.
+// Powers of two for a whole tensor keep all of bf16's bits down to 2^-28 of its largest value, and 2^-38 of
+// that below; the factors round X to fp16, 2^-11 of each value. One power for all tokens, and the factors with
+// X instead of G: dX of a token is then as exact however small its gradient is beside the others'.
+__global__ __launch_bounds__(256) void vocab_half_kernel(const uint16_t* __restrict__ Xc, int64_t K,
+                                                         const float* __restrict__ factor,
+                                                         const float* __restrict__ top, const float* __restrict__ peaks,
+                                                         int npeaks, const int* __restrict__ nv, int twice,
+                                                         int* __restrict__ expo, uint16_t* __restrict__ Xh) {
+  const int n = *nv;
+  if (n <= twice) return;
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, top[i]);
+  const int kx = half_exponent(block_max(m));
+  if (blockIdx.x == 0) {
+    float w = 0.0f;
+    for (int i = threadIdx.x; i < npeaks; i += 256) w = fmaxf(w, peaks[i]);
+    w = block_max(w);
+    if (threadIdx.x == 0) {
+      expo[0] = half_exponent(w);
+      expo[1] = kx;
+    }
+  }
+  if (!Xh) return;
+  for (int c = blockIdx.x; c < n; c += gridDim.x) {
+    const double f = ldexp((double)factor[c], kx);  // beyond fp32 where a row of X is small
+    for (int64_t i = threadIdx.x; i < K >> 3; i += 256) {
+      float x[8];
+      bf16x8(*reinterpret_cast<const uint4*>(Xc + c * K + 8 * i), x);
+      v8h h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = (_Float16)(float)((double)x[e] * f);
+      *reinterpret_cast<v8h*>(Xh + c * K + 8 * i) = h;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -266,19 +411,17 @@ __global__ __launch_bounds__(256) void vocab_gather_kernel(const VocabCompact p)
 // ---------------------------------------------------------------------------
 enum { kSums, kGrad, kDX, kDW };
 
-// Up to so many tokens that count G is held in two parts of bf16, which leave the gradients no error but
-// their own rounding: 0.0017 of them against float64, in norm, as the plain fp32 form's. In one part it is
-// 0.0023 - 0.0024: one rounding more of the size of the results' own (2^-8 of an element at most),
-// to nearest and element by element, so it does not grow with the ids or tokens that are added up; a
-// trainer that keeps its logits' gradient in bf16 rounds at the same place. The matrix cores take bf16 or less
-// (fp16 would lose G's range), so a second part is a second product: us in one part and in two, 32768 ids,
-// 3584 wide, 1 token 123 and 123, 33 130 and 143, 128 176 and 212; 131072 ids, 128 584 and 741, 256 795
-// and 1191, 1024 2415 and 4000, 4096 9048 and 15265. Up to 128 tokens memory hides most of it;
-// beyond, it would cost half the gradient's time and more.
+// Up to so many tokens that count G is held in two parts of bf16, beyond in fp16, with factors and powers of
+// two of its own (H, vocab_half_kernel). Either leaves the gradients next to no error but their own rounding to
+// bf16: 0.0017 of them against float64, in norm, as the plain fp32 form's; G in one part of bf16 leaves
+// 0.0023 - 0.0025. Two parts are two products, which memory hides for few tokens (us in one part and in
+// two, 32768 ids, 3584 wide: 1 token 123 and 123, 33 130 and 143, 128 176 and 212; 128 of 131072 584 and 741).
+// fp16 needs the largest value of W, a pass over it, and W's fragments converted on their way to the matrix
+// cores (5% of 4096 tokens' gradient; the products themselves take 3% more power and time): us in two parts and in
+// fp16, 131072 ids, 3584 wide, 140 tokens 937 and 870, 256 1185 and 960, 512 2094 and 1564, 4096 15265 and
+// 9875 (one part of bf16: 9110); 200 tokens of 5000 ids 78 and 80, 1000 182 and 159, 1000 tokens 512 wide
+// 75 and 65.
 constexpr int kTwice = 128;
-
-// Lambdas of a kernel share its state in registers only where they are inlined.
-#define QR_INLINE __attribute__((always_inline))
 
 struct VocabTile {
   const uint16_t *A, *B;
@@ -313,7 +456,9 @@ struct VocabTile {
   // without it where kDX will find W in the MALL (33 x 32768: 3 us), kDX where it finds it in the L2s
   // (gradient, 200 tokens, 3584 wide or 1808: 10000 ids 108 / 110, 5000 68 / 70, 4112 x 1808 50 / 46).
   bool stream;
-  int twice;       // up to so many compact tokens G is held in two parts
+  int twice;       // up to so many compact tokens G is held in two parts, beyond as H in fp16
+  const int* expo; // exponents of the fp16 operands
+  const uint16_t* Xh;  // kDW: A of fp16 products
 };
 
 // Tokens that a launch's blocks number themselves (vocab_number): 16 tokens of 5000 ids,
@@ -360,6 +505,7 @@ constexpr int ring_bytes() {  // copies of 8 rows (1 KB), as many by each wave
 //   kGrad  ids (W, rows)     tokens (X, rows)   hidden
 //   kDX    hidden (W, cols)  tokens (G, rows)   ids
 //   kDW    hidden (X, cols)  ids (G, cols)      tokens
+// F16: H in G's place, W converted behind its LDS reads, X as vocab_half_kernel leaves it.
 //
 // Products are 16 x 16 x 32: with all CUs busy they are bound by power (the clock falls to 1.5 -
 // 1.9 GHz, the matrix cores busy for 69% of it), and from registers alone these reach 2.06
@@ -373,7 +519,7 @@ constexpr int ring_bytes() {  // copies of 8 rows (1 KB), as many by each wave
 // 192 x 320 and 128 x 384, 8 and 10 bytes, gain 13% at best and lose elsewhere.
 //
 // `block` and the grid it belongs to may be a part of the launch's.
-template <int MODE, int BN, int BM, int WN, int WM, int S, bool HINT>
+template <int MODE, int BN, int BM, int WN, int WM, int S, bool HINT, bool F16>
 __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, uint8_t* smem) {
   constexpr bool TA = MODE == kDX || MODE == kDW, TB = MODE == kDW;
   constexpr int NW = WN * WM, KS = 64;
@@ -399,7 +545,7 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
   const int64_t ext_b = MODE == kDW ? p.ids : (MODE == kDX ? rows : nv);
   const int64_t klen = MODE == kDW ? rows : (MODE == kDX ? p.ids : p.K);
   const int stages = (int)((klen + KS - 1) / KS);
-  const bool stream = p.stream && (MODE == kDW ? rows <= 2 * kTwice : ext_b <= BM);
+  const bool stream = p.stream && (MODE == kDW ? rows <= 256 : ext_b <= BM);
 
   // An XCD takes one contiguous part of the tiles; groups of up to 8 B tiles share A tiles.
   const int tiles_b = (int)((ext_b + BM - 1) / BM);
@@ -473,7 +619,7 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
       }
     }
   }
-  const uint16_t* const pa = p.A + (TA ? a0 : a0 * p.lda);
+  const uint16_t* const pa = (MODE == kDW && F16 ? p.Xh : p.A) + (TA ? a0 : a0 * p.lda);
   const uint16_t* const pb = p.B + (TB ? b0 : direct ? 0 : b0 * p.ldb);
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
   constexpr int NG = GA + GB;
@@ -553,10 +699,31 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
 #pragma unroll
     for (int j = 0; j < FM; ++j) load_b(st, h, buf, j);
   };
+  // W in fp16, times its power of two: 20 instructions for a fragment (without the factor 12: 1.4% of 4096
+  // tokens' gradient less). Converted a row ahead, among the products before, it takes as long.
+  float half_scale = 1.0f;
+  if constexpr (F16 && MODE == kDX)
+    half_scale = __uint_as_float(__builtin_amdgcn_readfirstlane((int)__float_as_uint(ldexpf(1.0f, p.expo[0]))));
+  auto to_half = [&](v8b x) QR_INLINE {
+    const uint4 q = __builtin_bit_cast(uint4, x);
+    auto pair = [&](uint32_t w) QR_INLINE {
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(bf16_lo(w) * half_scale, bf16_hi(w) * half_scale));
+    };
+    return __builtin_bit_cast(v8h, make_uint4(pair(q.x), pair(q.y), pair(q.z), pair(q.w)));
+  };
   auto multiply_row = [&](int buf, int i) {
+    if constexpr (F16) {
+      v8h a;
+      if constexpr (MODE == kDX) a = to_half(fa[buf][i]);
+      else a = __builtin_bit_cast(v8h, fa[buf][i]);
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[buf][i], fb[buf][j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < FM; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(v8h, fb[buf][j]), acc[i][j], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[buf][i], fb[buf][j], acc[i][j], 0, 0, 0);
+    }
   };
 
   // Compact tokens of the lane, and where their lists enter the wave's ids.
@@ -762,11 +929,15 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
     uint8_t* so = smem + wid * (16 * LD);
     const int64_t row0 = b0 + wm * WTM, lim = MODE == kGrad ? nv : p.ids;
     const int64_t col0 = a0 + wn * WTN, left = MODE == kGrad ? WTN : p.K - col0;
-    auto rows_out = [&](int j, const float* v, uint16_t* out, auto nt) QR_INLINE {
+    auto rows_out = [&](int j, const float* v, uint16_t* out, auto nt, auto half) QR_INLINE {
+      auto pair = [&](float x, float y) QR_INLINE {
+        if constexpr (decltype(half)::value) return half_pair(x, y);
+        else return bf16_pair(x, y);
+      };
 #pragma unroll
       for (int i = 0; i < FN; ++i)
         *reinterpret_cast<uint2*>(so + (l & 15) * LD + (16 * i + 4 * (l >> 4)) * 2) =
-            make_uint2(bf16_pair(v[4 * i], v[4 * i + 1]), bf16_pair(v[4 * i + 2], v[4 * i + 3]));
+            make_uint2(pair(v[4 * i], v[4 * i + 1]), pair(v[4 * i + 2], v[4 * i + 3]));
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int k = 0; k < 16 * CPR / 64; ++k) {
@@ -781,36 +952,49 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
+    const int kx = MODE == kDW && F16 ? -__builtin_amdgcn_readfirstlane(p.expo[1]) : 0;
     auto all_out = [&](auto nt) QR_INLINE {
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
         float v[4 * FN];
         values(j, v);
         if constexpr (MODE == kGrad) {
-          // G in fp32. The matrix cores take bf16: up to `twice` tokens G is held in two parts
-          // (its rounding to bf16 and what that left: 2^-16 of each element); beyond, rounded
-          // once (2^-8 of each, as much as the rounding of the results; why, at kTwice).
+          // G in fp32, in two parts of bf16 (its rounding and what that left: 2^-16 of each element), or
+          // H for fp16 (2^-11 of each, 2^-39 of the list's weight where that is more).
           if constexpr (!EARLY) token(j);
-          float gt = 0.0f, ga = 0.0f, l2 = 0.0f;
+          float gt = 0.0f, ga = 0.0f, l2 = 0.0f, mass = 1.0f;
           if (tok[j] >= 0) {
-            gt = p.g[tok[j]] * p.scale * p.sign;
-            ga = p.mass ? gt * p.mass[tok[j]] : gt;
+            if (p.mass) mass = p.mass[tok[j]];
+            if (twice) {
+              gt = p.g[tok[j]] * p.scale * p.sign;
+              ga = gt * mass;
+            } else {
+              ga = mass > 0.0f ? (float)(1 << kHalf) : 0.0f;
+            }
             l2 = p.lse[tok[j]] * kLog2e;
           }
 #pragma unroll
           for (int k = 0; k < 4 * FN; ++k) v[k] = ga * __builtin_amdgcn_exp2f(__builtin_fmaf(v[k], c2, -l2));
           beyond(v, 0.0f);
           hits(j, [&](bool mine, int64_t, float w, int reg) QR_INLINE {
-            const float b = mine ? gt * w : 0.0f;
+            const float b = !mine ? 0.0f : twice ? gt * w : ga == 0.0f ? 0.0f : w / mass * ga;
 #pragma unroll
             for (int k = 0; k < 4 * FN; ++k) v[k] -= reg == k ? b : 0.0f;
           });
+          if (!twice) {
+            rows_out(j, v, p.out16, nt, std::true_type{});
+            continue;
+          }
         }
-        rows_out(j, v, p.out16, nt);
-        if (MODE == kGrad && twice) {
+        if constexpr (MODE == kDW && F16) {
+#pragma unroll
+          for (int k = 0; k < 4 * FN; ++k) v[k] = __builtin_ldexpf(v[k], kx);
+        }
+        rows_out(j, v, p.out16, nt, std::false_type{});
+        if constexpr (MODE == kGrad) {
 #pragma unroll
           for (int k = 0; k < 4 * FN; ++k) v[k] -= __uint_as_float(bf16_pair(0.0f, v[k]) & 0xffff0000u);
-          rows_out(j, v, p.out16 + nv * p.ldo, nt);
+          rows_out(j, v, p.out16 + nv * p.ldo, nt, std::false_type{});
         }
       }
     };
@@ -825,13 +1009,26 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
 // gradient 794 -> 768), and one without (4096 tokens: 1% faster).
 template <int MODE, int BN, int BM, int WN, int WM, int S>
 __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_t* smem) {
-  if constexpr (MODE == kDW || BM <= 128) {
-    vocab_tile_body<MODE, BN, BM, WN, WM, S, true>(p, block, smem);
-  } else {
-    const int nv = *p.nv, rows = MODE == kDX && nv <= p.twice ? 2 * nv : nv;
-    if (p.stream && rows <= BM) vocab_tile_body<MODE, BN, BM, WN, WM, S, true>(p, block, smem);
-    else vocab_tile_body<MODE, BN, BM, WN, WM, S, false>(p, block, smem);
+  auto body = [&](auto half) QR_INLINE {
+    constexpr bool F16 = decltype(half)::value;
+    if constexpr (F16 && MODE == kDX && BM == 128) {
+      // one wave converts a fragment of W instead of two (gradient of 300 tokens of 131072 ids 1369 -> 1278 us)
+      vocab_tile_body<MODE, BN, BM, 8, 1, S, true, F16>(p, block, smem);
+    } else if constexpr (MODE == kDW || BM <= 128) {
+      vocab_tile_body<MODE, BN, BM, WN, WM, S, true, F16>(p, block, smem);
+    } else {
+      const int nv = *p.nv, rows = MODE == kDX && nv <= p.twice ? 2 * nv : nv;
+      if (p.stream && rows <= BM) vocab_tile_body<MODE, BN, BM, WN, WM, S, true, F16>(p, block, smem);
+      else vocab_tile_body<MODE, BN, BM, WN, WM, S, false, F16>(p, block, smem);
+    }
+  };
+  if constexpr (MODE == kDW || (MODE == kDX && BM > 64)) {  // (64 rows: two parts of up to 32 tokens)
+    if (*p.nv > p.twice) {
+      body(std::true_type{});
+      return;
+    }
   }
+  body(std::false_type{});
 }
 
 template <int MODE, int BN, int BM, int WN, int WM, int S>
@@ -941,12 +1138,14 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const VocabTile p, fl
 }
 
 // dX of all tokens: the splits' sums in order (a split's parts of G one after the other),
-// rounded once; zeros for masked tokens. A block takes 256 values of a token, its waves (at
+// times what fp16 products leave out, rounded once; zeros for masked tokens. A block takes 256 values of a token, its waves (at
 // most kDxWaves) a run of the sums each, eight at once, which are added in order.
 constexpr int kDxWaves = 8;
 __global__ __launch_bounds__(64 * kDxWaves) void vocab_dx_kernel(const float* __restrict__ part, int64_t K,
                                                                  const int* __restrict__ inv,
                                                                  const int* __restrict__ nv, int twice,
+                                                                 const float* __restrict__ factor,
+                                                                 const int* __restrict__ expo,
                                                                  uint16_t* __restrict__ dX, int64_t lddx) {
   __shared__ float4 red[kDxWaves][64];
   const int64_t t = blockIdx.x, c = inv[t], h = 256 * (int64_t)blockIdx.y + 4 * threadIdx.x;
@@ -981,6 +1180,11 @@ __global__ __launch_bounds__(64 * kDxWaves) void vocab_dx_kernel(const float* __
       const float4 o = red[w][threadIdx.x];
       v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
     }
+  }
+  if (c >= 0 && n > twice) {  // the sums are of fp16 products
+    const float f = factor[c];
+    const int k = -expo[0];
+    v = make_float4(ldexpf(v.x * f, k), ldexpf(v.y * f, k), ldexpf(v.z * f, k), ldexpf(v.w * f, k));
   }
   if (h < K) *reinterpret_cast<uint2*>(dX + t * lddx + h) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
 }
@@ -1017,9 +1221,10 @@ hipError_t launch_one(VocabTile p, int64_t max_b, hipStream_t st) {
   return hipGetLastError();
 }
 
+// rows: of dX, or 0 for dW alone.
 template <int BM, int WN, int WM, int S>
 hipError_t launch_grads(VocabTile x, VocabTile w, int64_t rows, hipStream_t st) {
-  const int64_t nx = product_blocks<kDX>(x, rows, 256, BM), nw = product_blocks<kDW>(w, w.ids, 256, 256);
+  const int64_t nx = rows ? product_blocks<kDX>(x, rows, 256, BM) : 0, nw = product_blocks<kDW>(w, w.ids, 256, 256);
   hipLaunchKernelGGL((vocab_grads_kernel<BM, WN, WM, S>), dim3((unsigned)(nx + nw)), dim3(512), 0, st, x, w, (int)nx);
   return hipGetLastError();
 }
@@ -1076,7 +1281,7 @@ hipError_t launch_logits(const VocabTile& p, const LogitTile& t, int64_t M, hipS
   return hipGetLastError();
 }
 
-// Rows of G (twice the tokens up to kTwice) in a tile of dX: the fewest that hold all, up to 64
+// Rows of G (twice the tokens where it is held in two parts) in a tile of dX: the fewest that hold all, up to 64
 // (16 tokens of 32768 ids, 3584 wide: 86 us, on 128 rows 88; 32 rows gain nothing), else the
 // cheaper by the measured costs of 128 and 256 (us, dX with its logits, 3584 wide, 128 | 256: 33
 // tokens of 32768 93 | 106, 128 of 131072 467 | 451, 257 of 100003 545 | 576, 600 of 32768 324 | 320,
@@ -1103,7 +1308,7 @@ hipError_t launch_both(const VocabTile& x, const VocabTile& w, int64_t rows, hip
 }
 
 struct Layout {
-  size_t nv, map, inv, keys, wts, mass, first, zl, xc, part, g, dx, bytes;
+  size_t nv, map, inv, keys, wts, mass, first, zl, xc, part, g, dx, factor, top, peaks, expo, xh, bytes;
   int buckets, shift;  // of ids, for lists
   int64_t piece;  // ids of a piece of the gradient
   DxPlan sums;
@@ -1156,6 +1361,13 @@ Layout layout(int64_t M, int64_t N, int64_t K, int64_t L, bool lists, bool grad)
     d.cap = (int)cap;
     w.g = take((size_t)(rows * w.piece) * 2);
     w.dx = take((size_t)(cap * K) * 4);
+    if (M > kTwice) {  // fp16
+      w.factor = take((size_t)M * 4);
+      w.top = take((size_t)M * 4);
+      w.peaks = take((size_t)kPeaks * 4);
+      w.expo = take(8);
+      w.xh = take((size_t)(M * K) * 2);
+    }
   }
   w.bytes = at;
   return w;
@@ -1189,19 +1401,39 @@ hipError_t prepare(const VocabArgs& p, const Layout& w, void* ws, bool direct, h
   c.X = p.X;
   c.Xc = at<uint16_t>(ws, w.xc);
   c.twice = p.lse_out ? -1 : kTwice;
+  if (!p.lse_out && p.M > kTwice) {
+    c.g = p.g;
+    c.mass = p.index ? at<float>(ws, w.mass) : nullptr;
+    c.gscale = p.index ? p.scale : -p.scale;
+    c.factor = at<float>(ws, w.factor);
+    c.top = at<float>(ws, w.top);
+  }
   c.dx = w.sums;
   c.nv = at<int>(ws, w.nv);
   c.map = at<int>(ws, w.map);
   c.inv = at<int>(ws, w.inv);
   c.value = p.value;
   c.lse = p.lse_out;
-  const dim3 grid((unsigned)p.M);
+  if (c.factor && p.dX) {  // fp16 products, if so many tokens count
+    c.W = p.W;
+    c.ldw = p.ldw;
+    while (c.shift < 8 && ((int64_t)1 << c.shift) < p.K >> 3) ++c.shift;  // threads of a row
+    const int64_t blocks = ceil_div(p.N, 256 >> c.shift);
+    c.peak_blocks = (int)(blocks < kPeaks ? blocks : kPeaks);
+    c.peaks = at<float>(ws, w.peaks);
+    c.stream = p.N * p.K * 2 > kMall;
+  }
+  const dim3 grid((unsigned)(p.M + c.peak_blocks));
   if (p.M <= kVocabCount) {
     hipLaunchKernelGGL(vocab_compact_kernel, grid, dim3(256), 0, st, c);
   } else {
     hipLaunchKernelGGL(vocab_scan_kernel, dim3(1), dim3(1024), 0, st, c);
     hipLaunchKernelGGL(vocab_gather_kernel, grid, dim3(256), 0, st, c);
   }
+  if (c.factor)
+    hipLaunchKernelGGL(vocab_half_kernel, dim3((unsigned)(p.M < 1024 ? p.M : 1024)), dim3(256), 0, st, c.Xc, p.K,
+                       c.factor, c.top, c.peaks, c.peak_blocks, c.nv, c.twice, at<int>(ws, w.expo),
+                       p.dW ? at<uint16_t>(ws, w.xh) : nullptr);
   return hipGetLastError();
 }
 
@@ -1221,6 +1453,7 @@ VocabTile common(const VocabArgs& p, const Layout& w, void* ws) {
   t.L = (int)p.L;
   t.scale = p.scale;
   t.twice = p.lse_out ? -1 : kTwice;
+  t.expo = at<int>(ws, w.expo);
   return t;
 }
 
@@ -1308,11 +1541,12 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     y.stream = true;
     y.A = at<uint16_t>(ws, w.xc);
     y.lda = p.K;
+    y.Xh = at<uint16_t>(ws, w.xh);
     y.out16 = p.dW + (p.dW ? id0 * p.lddw : 0);
     y.ldo = p.lddw;
     if (p.dX && p.dW) e = launch_both(x, y, rows, st);
     else if (p.dX) e = launch_dx(x, rows, st);
-    else e = launch_one<kDW, 256, 256, 4, 2, 2>(y, ids, st);
+    else e = launch_grads<64, 4, 2, 3>(x, y, 0, st);
     if (e != hipSuccess) return e;
   }
   if (p.dX) {
@@ -1324,8 +1558,8 @@ hipError_t launch_vocab_grad(const VocabArgs& p, void* ws, hipStream_t st) {
     const int splits = w.sums.splits(rows);
     const int waves = splits <= 4 ? 1 : splits <= 4 * kDxWaves ? (splits + 3) / 4 : kDxWaves;
     hipLaunchKernelGGL(vocab_dx_kernel, dim3((unsigned)p.M, (unsigned)ceil_div(p.K, 256)), dim3(64, (unsigned)waves),
-                       0, st, at<float>(ws, w.dx), p.K, at<int>(ws, w.inv), at<int>(ws, w.nv), kTwice,
-                       p.dX, p.lddx);
+                       0, st, at<float>(ws, w.dx), p.K, at<int>(ws, w.inv), at<int>(ws, w.nv),
+                       kTwice, at<float>(ws, w.factor), at<int>(ws, w.expo), p.dX, p.lddx);
   }
   return hipGetLastError();
 }
