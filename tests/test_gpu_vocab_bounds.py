@@ -296,7 +296,7 @@ def test_fp16_of_nothing():
         assert bool(dX.any()) == bool(b.any() and c.any()) and bool(dW.any()) == bool(a.any() and c.any())
 
 
-def test_fp16_in_a_graph_that_two_masks_replay():
+def test_fp16_in_a_graph_replayed_with_other_masks():
     """One captured gradient of 400 tokens, replayed with 400, 129, 128 and no tokens that count, eager calls on
     another stream between."""
     M, N, K = 400, 3001, 264
@@ -326,3 +326,28 @@ def test_fp16_in_a_graph_that_two_masks_replay():
         torch.cuda.synchronize()
         for a, b, c in zip(out, want[k], eager):
             assert torch.equal(a, b) and torch.equal(c, b), k
+
+
+def test_fp16_below_its_normal_numbers():
+    """Certain ids whose tokens leave the others 2^-29 to 2^-36: in fp16, times 2^14, all below 2^-14. The
+    others' rows of dW are sums of nothing else, and must not come out as 0."""
+    M, N, K = 200, 1000, 64
+    r = np.random.default_rng(12)
+    a = torch.from_numpy(r.uniform(20.2, 24.9, M).astype(np.float32)).to(torch.bfloat16)
+    slot = torch.from_numpy(r.integers(0, K, M))
+    ids = torch.from_numpy(r.permutation(N)[:K])
+    x = torch.zeros((M, K))
+    x[torch.arange(M), slot] = a.float()
+    w = torch.zeros((N, K))
+    w[ids, torch.arange(K)] = 1.0
+    g = torch.from_numpy(r.uniform(0.5, 2.0, M).astype(np.float32))
+    _, dW = _check_fp16(x, w, g, ids[slot].to(DEV))
+    others = torch.ones(N, dtype=torch.bool)
+    others[ids] = False
+    used = torch.zeros(K, dtype=torch.bool)
+    used[slot] = True
+    got = dW.cpu()[others][:, used].double()
+    want = torch.zeros(K, dtype=torch.float64)
+    want.index_add_(0, slot, -g.double() * a.double() / (torch.exp(a.double()) + N - 1))
+    # 2^-39 of 2^-36 at most, fp16's and bf16's roundings, and lse's in the exponential (30 u)
+    assert bool(((got / want[used] - 1).abs() <= 2.0 ** -3 + 2.0 ** -7).all())
