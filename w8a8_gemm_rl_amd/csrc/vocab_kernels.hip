@@ -14,11 +14,11 @@
 // Four products share one kernel (vocab_tile): the logits' softmax sums; the same logits
 // again with G as output, a piece of the vocabulary at a time; that piece's part of dX
 // and its rows of dW. The sums need 2 M N K operations and W once, the gradient 6 M N K and
-// W twice (its logits are computed again: held, they would be M N values) beside dW. Up to
-// about 128 tokens memory bounds both (W of 131072 x 3584 for 1 token: 145 us, 6.5 TB/s), beyond
-// about 512 the matrix cores and the power that they take: 4096 tokens of 131072 ids, 3584 wide,
-// take 3.05 ms for the sums (1.26 PFLOP/s), 8.83 ms for the gradient (1.31), 5120 wide 3.96 ms
-// (1.39); a library product alone of the sums' shape reaches 1.38 - 1.42.
+// W twice (its logits are computed again: held, they would be M N values) beside dW, and beyond 128
+// tokens once more for its largest value. Up to about 128 tokens memory bounds both (W of 131072 x 3584 for
+// 1 token: 141 us, 6.7 TB/s), beyond about 512 the matrix cores and the power that they take: 4096 tokens
+// of 131072 ids, 3584 wide, take 2.83 ms for the sums (1.36 PFLOP/s), 10.1 ms for the gradient (1.14), 5120
+// wide 3.98 ms (1.38) and 14.2; a library product in bf16 alone of the sums' shape reaches 1.47.
 #include <cmath>
 #include <type_traits>
 
@@ -51,7 +51,7 @@ constexpr int kNone = 0x7fffffff;  // list key of no entry: past every id
 // their ids (entries of one id in the order of the list, ids outside [0, N) last).
 // p = softmax over the entries, or exp(c s - teacher_lse). L <= kVocabMaxList; ranks by
 // counting in LDS. first[b] is the first entry whose id is not below b << shift, where a tile's
-// waves begin to look for theirs. 4096 tokens of 64 entries take 8.5 us, a launch 2 of them.
+// waves begin to look for theirs. 4096 tokens of 64 entries take 9 us, a launch 2 of them.
 template <bool BF16>
 __global__ __launch_bounds__(256) void vocab_list_kernel(const int64_t* __restrict__ index,
                                                          const void* __restrict__ teacher,
@@ -271,8 +271,8 @@ __device__ __forceinline__ void vocab_peak(const VocabCompact& p, int block) {
 }
 
 // Compact numbers and rows in one launch, a block a token that counts the live ones itself.
-// M reads a block: up to kVocabCount tokens less than another launch (gradients, 5000 ids: 1 token
-// 21 us, in two launches 22, 300 tokens 38 and 39, 1024 66 and 67; 2048 101 and 100, 4096 224 and 217).
+// M reads a block: up to kVocabCount tokens less than another launch (gradients of 5000 ids, 1 token 21 us
+// and 22 in two launches; from 300 tokens to 2048 within 1 us of each other, 4096 217 in two and 224).
 constexpr int64_t kVocabCount = 512;
 __global__ __launch_bounds__(256) void vocab_compact_kernel(const VocabCompact p) {
   __shared__ int below[4], all[4];
@@ -416,11 +416,11 @@ enum { kSums, kGrad, kDX, kDW };
 // bf16: 0.0017 of them against float64, in norm, as the plain fp32 form's; G in one part of bf16 leaves
 // 0.0023 - 0.0025. Two parts are two products, which memory hides for few tokens (us in one part and in
 // two, 32768 ids, 3584 wide: 1 token 123 and 123, 33 130 and 143, 128 176 and 212; 128 of 131072 584 and 741).
-// fp16 needs the largest value of W, a pass over it, and W's fragments converted on their way to the matrix
-// cores (5% of 4096 tokens' gradient; the products themselves take 3% more power and time): us in two parts and in
-// fp16, 131072 ids, 3584 wide, 140 tokens 937 and 870, 256 1185 and 960, 512 2094 and 1564, 4096 15265 and
-// 9875 (one part of bf16: 9110); 200 tokens of 5000 ids 78 and 80, 1000 182 and 159, 1000 tokens 512 wide
-// 75 and 65.
+// fp16 needs the largest value of W, a pass over it (1.4% of 4096 tokens' gradient), W's fragments converted
+// on their way to the matrix cores (5%), and products that take more power than bf16's (4%): us in two
+// parts and in fp16, 131072 ids, 3584 wide, 140 tokens 937 and 887, 256 1185 and 974, 512 2094 and 1627,
+// 4096 15265 and 10115 (in one part of bf16 9130); 200 tokens of 5000 ids 78 and 80, 1000 182 and 159, 1000
+// tokens 512 wide 75 and 65.
 constexpr int kTwice = 128;
 
 struct VocabTile {
@@ -450,9 +450,9 @@ struct VocabTile {
   float* out32;    // kDX: [splits][rows of G][K]
   int add;         // kDX: add to what is there
   // kSums, kGrad, kDX: W's copies may carry the non-temporal hint; kDW: stores may. They do where a
-  // tile holds all tokens that count: nothing of W is read again, and dW is written to be read later (us
-  // with / without, 3584 wide, W past the MALL or not there yet): logp 1 x 131072 145 / 164, 128 x
-  // 131072 166 / 181, 1 x 32768 45 / 50; gradient 1 x 131072 466 / 575, 33 x 32768 148 / 183. kGrad reads
+  // tile holds all tokens that count: nothing of W is read again, and dW is written to be read later (less
+  // time by, 3584 wide, W past the MALL or not there yet: log-probabilities of 1 token, 131072 ids, 12%, 128
+  // 8%, 1 of 32768 10%; gradient of 1 of 131072 19%, 33 of 32768 19%). kGrad reads
   // without it where kDX will find W in the MALL (33 x 32768: 3 us), kDX where it finds it in the L2s
   // (gradient, 200 tokens, 3584 wide or 1808: 10000 ids 108 / 110, 5000 68 / 70, 4112 x 1808 50 / 46).
   bool stream;
@@ -509,8 +509,8 @@ constexpr int ring_bytes() {  // copies of 8 rows (1 KB), as many by each wave
 //
 // Products are 16 x 16 x 32: with all CUs busy they are bound by power (the clock falls to 1.5 -
 // 1.9 GHz, the matrix cores busy for 69% of it), and from registers alone these reach 2.06
-// PFLOP/s, 32 x 32 x 16 1.87. In the kernel: 4096 tokens of 131072 ids, 3584 wide, 3.05 ms and
-// 3.20, 5120 wide 3.96 and 4.14, the first's gradient 8.83 and 9.00. Register r of fragment
+// PFLOP/s, 32 x 32 x 16 1.87. In the kernel, of 4096 tokens of 131072 ids, 3584 wide, the sums take 5% less
+// so, 5120 wide 4%, the first's gradient 2%. Register r of fragment
 // (i, j): A side 16 i + 4 (lane / 16) + r, B side 16 j + lane % 16.
 //
 // A wave's tile in the 256 x 256 block is 64 x 128 (four by two waves; two by four spill registers, and
@@ -1005,8 +1005,8 @@ __device__ __forceinline__ void vocab_tile_body(const VocabTile& p, int block, u
 }
 
 // Copies that may carry the non-temporal hint take a branch each: tiles of 256 tokens have a body with
-// it for where one holds all that count (200 tokens of 131072 ids, 3584 wide, 239 -> 230 us, their
-// gradient 794 -> 768), and one without (4096 tokens: 1% faster).
+// it for where one holds all that count (log-probabilities of 200 tokens of 131072 ids, 3584 wide,
+// 239 -> 230 us), and one without (4096 tokens: 1% faster).
 template <int MODE, int BN, int BM, int WN, int WM, int S>
 __device__ __forceinline__ void vocab_tile(const VocabTile& p, int block, uint8_t* smem) {
   auto body = [&](auto half) QR_INLINE {
@@ -1039,8 +1039,8 @@ __global__ __launch_bounds__(64 * WN * WM, 1) void vocab_tile_kernel(const Vocab
 
 // The logits' tiles of 256 x 256 are planned for all tokens; where few of them count, tiles of
 // 256 x 128 take less time (a round of the CUs 0.6 of the other's), if the launch has blocks for them:
-// 200 tokens of 2048, 32768 ids, 3584 wide, 83 -> 63 us, their gradient 272 -> 241; 120 of 250, 131072 ids,
-// 225 -> 161 and 805 -> 747.
+// log-probabilities of 200 of 2048 tokens, 32768 ids, 3584 wide, 63 us and 83 without, 120 of 250, 131072 ids,
+// 162 and 225.
 template <int MODE>
 __global__ __launch_bounds__(512, 1) void vocab_wide_kernel(const VocabTile p) {
   constexpr int A = ring_bytes<256, 256, 8, 2>(), C = ring_bytes<256, 128, 8, 3>();
@@ -1054,8 +1054,8 @@ __global__ __launch_bounds__(512, 1) void vocab_wide_kernel(const VocabTile p) {
 }
 
 // A piece's part of dX (the first `dx_blocks` blocks) and rows of dW in one launch: dX has
-// few tiles of many stages, which seldom fill the CUs, dW many of few (gradients, in one launch | in two:
-// 2048 tokens of 131072 ids, 5120 wide, 6.83 | 7.52 ms; 64 of 5000, 1024 wide, 31 | 39 us).
+// few tiles of many stages, which seldom fill the CUs, dW many of few (gradients: 9% less time than in two
+// launches at 2048 tokens of 131072 ids, 5120 wide, 20% at 64 of 5000, 1024 wide).
 template <int BM, int WN, int WM, int S>
 __global__ __launch_bounds__(512, 1) void vocab_grads_kernel(const VocabTile x, const VocabTile w, int dx_blocks) {
   static_assert(WN * WM == 8, "one block size");
@@ -1124,7 +1124,8 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const VocabTile p, fl
   if (wts) {
     for (int j = lane; j < L; j += 64) {
       const double w = (double)wts[t * L + j];
-      if (keys[t * L + j] != kNone && w != 0.0) v += w * (log(w) - (((double)zl[t * L + j] - (double)top) * nat - rest));
+      const double z = ((double)zl[t * L + j] - (double)top) * nat - rest;
+      if (keys[t * L + j] != kNone && w != 0.0) v += w * (log(w) - z);
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
@@ -1138,8 +1139,8 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const VocabTile p, fl
 }
 
 // dX of all tokens: the splits' sums in order (a split's parts of G one after the other),
-// times what fp16 products leave out, rounded once; zeros for masked tokens. A block takes 256 values of a token, its waves (at
-// most kDxWaves) a run of the sums each, eight at once, which are added in order.
+// times what fp16 products leave out, rounded once; zeros for masked tokens. A block takes 256 values of a
+// token, its waves (at most kDxWaves) a run of the sums each, eight at once, which are added in order.
 constexpr int kDxWaves = 8;
 __global__ __launch_bounds__(64 * kDxWaves) void vocab_dx_kernel(const float* __restrict__ part, int64_t K,
                                                                  const int* __restrict__ inv,
@@ -1283,9 +1284,10 @@ hipError_t launch_logits(const VocabTile& p, const LogitTile& t, int64_t M, hipS
 
 // Rows of G (twice the tokens where it is held in two parts) in a tile of dX: the fewest that hold all, up to 64
 // (16 tokens of 32768 ids, 3584 wide: 86 us, on 128 rows 88; 32 rows gain nothing), else the
-// cheaper by the measured costs of 128 and 256 (us, dX with its logits, 3584 wide, 128 | 256: 33
-// tokens of 32768 93 | 106, 128 of 131072 467 | 451, 257 of 100003 545 | 576, 600 of 32768 324 | 320,
-// 512 of 131072 950 | 872, 2048 of 131072, 5120 wide, 5620 | 5130).
+// cheaper by measured costs of 128 and 256 (us, dX with its logits, 3584 wide, 128 | 256; in two parts of
+// bf16: 33 tokens of 32768 92 | 97, 128 of 131072 446 | 446, with dW 761 | 735; in fp16: 200 of 32768 162 | 175, 257
+// of 100003 655 | 706, 512 of 131072 1101 | 1050, 600 of 32768 356 | 365, 700 378 | 379, 2048 of
+// 131072, 5120 wide, 6300 | 5979).
 int dx_tile(int64_t rows) {
   if (rows <= 64) return 64;
   return ceil_div(rows, 128) * 55 < ceil_div(rows, 256) * 92 ? 128 : 256;
