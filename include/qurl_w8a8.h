@@ -286,7 +286,7 @@ int qr_acr_tis_loss(const float* logp, const float* logp_prox, const float* logp
  *   X        [M, ldx] bf16 hidden states, W [N, ldw] bf16 head (read); rows on 16-byte
  *            boundaries, strides at most 2^21. M at most 2^22, N in [1, 2^22 - 1], K a
  *            multiple of 8 in [8, 65536].
- *   scale    finite, > 0: the logits' scale, 1 / temperature (scaled logits, and scale
+ *   scale    > 0, at most 2^127: the logits' scale, 1 / temperature (scaled logits, and scale
  *            times an incoming gradient, stay in fp32's range; scaled teacher logits below it
  *            count as -inf).
  *   target   [M] int64;  index [M, L] int64, 1 <= L <= 1024;  teacher [M, L] fp32

@@ -70,4 +70,4 @@ def test_vocabulary_losses_under_host_sanitizers():
     out = r.stdout
     assert r.returncode == 0, out[-4000:]
     assert "AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
-    assert "8 passed" in out, out[-4000:]
+    assert "12 passed" in out, out[-4000:]

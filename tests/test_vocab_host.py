@@ -23,6 +23,15 @@ def test_hidden_states_and_head_are_matrices():
             B._head_args(x, w)
 
 
+@pytest.mark.parametrize("fn", ["qr_vocab_logp", "qr_vocab_logp_grad", "qr_vocab_distill", "qr_vocab_distill_grad"])
+def test_refusals_of_scales(fn):
+    """Scales whose product with log2 e is beyond fp32 are refused, all others pass (to the workspace's check)."""
+    from test_oracle_vocab import _call
+
+    for scale, status in ((3.0e38, -1), (1.8e38, -1), (2.0 ** 127, -3), (2.0 ** -149, -3)):
+        assert _call(B, fn, scale=scale) == status, scale
+
+
 def test_workspaces_up_to_the_limits():
     """Sizes and plans over the whole documented range: room for the copied rows of X at least (twice
     over where G may be in two parts), the list's tables, and the gradient's piece and sums of dX."""

@@ -1,7 +1,6 @@
 // C ABI of the losses over a large vocabulary (declared and documented in
 // include/qurl_w8a8.h). As for the other entry points, arguments are validated on
 // the host before anything is enqueued, and nothing here synchronizes.
-#include <cmath>
 #include <cstring>
 
 #include "qr_internal.h"
@@ -62,8 +61,9 @@ int check_common(const char* fn, qr::VocabArgs& a, const void* X, int64_t ldx, c
   if (st == QR_OK) st = check_rows(fn, "X", X, M, ldx, K);
   if (st == QR_OK) st = check_rows(fn, "W", W, N, ldw, K);
   if (st != QR_OK) return st;
-  if (!std::isfinite(scale) || !(scale > 0.0f))
-    return qr::set_error(QR_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
+  // its product with log2 e is a fp32 value
+  if (!(scale > 0.0f && scale <= 0x1p127f))
+    return qr::set_error(QR_ERR_INVALID_ARG, "%s: scale must be > 0 and at most 2^127", fn);
   a.X = static_cast<const uint16_t*>(X);
   a.W = static_cast<const uint16_t*>(W);
   a.ldx = ldx; a.ldw = ldw; a.M = M; a.N = N; a.K = K;
